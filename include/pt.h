@@ -427,11 +427,117 @@ pt_status pt_fold_positions(const pt_foldplan* plan, int64_t* pos, cudaStream_t 
 pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t row_bytes, unsigned long long* count,
                              cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rollout decoding: a paged key/value cache of a prefix tree, and the
+ * attention of every sample's newest tokens over it.
+ *
+ * Passage: "cp=1 shared-prefix prefix-tree attention for rollouts", PR
+ * description: a prompt is encoded once for all its completions, a completion
+ * sees the whole prompt and itself causally.  The pages train on finished
+ * rollouts; these calls are the same tree while the rollouts are generated:
+ * a node's keys and values are stored once, and each step reads them once for
+ * all samples below the node.
+ *
+ * Cache.  A cache row is a tree node: its tokens in order, in pages of
+ * page_size tokens.  tables [n_rows, max_pages] (device int32) names row i's
+ * pages; Kc and Vc are [n_pages, Hkv, page_size, D].  Token t of row i is slot
+ * tables[i][t / page_size] * page_size + t % page_size.  Rows share no page:
+ * a prompt's last page is the prompt's alone, completions start their own.
+ *
+ * pt_cache_tables: one step of the rows' lengths, on the device.  Row i holds
+ *   held[i] tokens and takes added[i] more; a negative added[i] takes tokens
+ *   back from its end (rejected drafts; -held[i] ends the row).  The pages
+ *   come from, and go back to, a ring of free page ids: entries [head, tail)
+ *   modulo ring_cap are free, counters = {head, tail} (device int64, counting
+ *   on past ring_cap).  Rows take pages in row order from the head, pages
+ *   given back go to the tail in row order; a page given back in a call is
+ *   free for the next one.  start[i] (or NULL: 0) is the position id of row
+ *   i's first token: the tokens of its ancestors.
+ *   Writes the taken ids into tables and the freed ids into ring (both in
+ *   place; entries behind a row's pages keep what they had), and into arrays
+ *   that overlap neither them nor the inputs: lens [n_rows] = held + added,
+ *   row_ptr [n_rows + 1] the exclusive sum of the tokens added, slots
+ *   [max_new] and positions [max_new] (may be NULL) of the added tokens, row
+ *   by row, -1 and 0 behind the last one, and counters_out [2].  The inputs
+ *   stay, so the call may be repeated with the same ones.
+ *   Errors on the device (pt_sync_status): PT_ERR_INVALID_ARG for a row with
+ *   held or held + added outside [0, max_pages * page_size] (it is left as it
+ *   is), for more than max_new added tokens (those behind have no slot), for
+ *   counters that are no ring of at most ring_cap entries, for more pages
+ *   given back than the ring has room for, and for a freed id below 0;
+ *   PT_ERR_NOMEM when the ring runs out: the rows behind get no page, their
+ *   tokens slot -1, and lens counts what fits in the pages they have.
+ *   Errors on the host: PT_ERR_INVALID_ARG for NULL pointers, negative sizes,
+ *   page_size or ring_cap below 1, max_new above 2^30, n_rows * max_pages
+ *   above 2^31 - 1, or overlapping arrays; PT_ERR_UNSUPPORTED above 262144
+ *   rows.
+ *
+ * pt_cache_write: K and V [T, Hkv, D] (device, dtype; tokens k_stride and
+ *   v_stride elements apart, a token's heads dense) into the slots
+ *   slots[T] (device int64).  A negative slot is passed over; one beyond the
+ *   cache is passed over and recorded (PT_ERR_INVALID_ARG).  When two tokens
+ *   name one slot, either may stay.  Any D, page size and alignment to the
+ *   element; 16-byte rows, strides and addresses are the fast ones.
+ *
+ * pt_decode_plan: the tree's paths (host; CSR path_ptr [n_samples + 1],
+ *   path_nodes, as pt_build_blockmap_tree takes them; the last node of a path
+ *   is the sample's own) for one head layout and q_len query tokens a sample.
+ *   Node ids are cache rows; n_nodes of them, in any order, some on no path,
+ *   and a sample may end at a node that others pass through.  The plan holds
+ *   no lengths: it serves every layer and step until a path changes.  Errors:
+ *   PT_ERR_INVALID_ARG for a bad count or head layout, an empty path, a node
+ *   out of range or twice on a path; PT_ERR_UNSUPPORTED above 65536 nodes.
+ * pt_decodeplan_free: returns its memory in the build stream's order.
+ *
+ * pt_attn_decode: O and LSE of the samples' newest tokens.
+ *   Q [n_samples * q_len, Hq, D] (device; tokens q_stride elements apart,
+ *   heads dense), sample by sample.  lens [n_nodes] (device int32): tokens in
+ *   the cache, the queries' own among them.  q_count [n_samples] (device
+ *   int32, or NULL: q_len each): how many of a sample's q_len rows are
+ *   queries; row j < q_count is token lens[leaf] - q_count + j of its own
+ *   node.  It keeps every token of the path's other nodes and its own node's
+ *   up to itself.  Rows j >= q_count stay as they were, in O and LSE.  A
+ *   row that keeps nothing gives O = 0, LSE = -inf.
+ *   O [n_samples * q_len, Hq, D] (dtype), LSE [Hq, n_samples * q_len] (fp32,
+ *   natural log).  scale <= 0 selects 1/sqrt(D).  What the cache holds behind
+ *   a row's tokens, NaN and infinities included, has no part in the result.
+ *   Lengths, tables and counts are read on the device at each call, so a
+ *   captured graph follows them.
+ *   workspace: at least pt_decode_workspace_bytes(plan, D) bytes, 256-byte
+ *   aligned; its contents do not matter before or after.  Calls that share
+ *   one must not overlap on the GPU.  The result does not vary between runs.
+ *   PT_BF16 with D a multiple of 8 up to 256 and page_size a multiple of 16
+ *   runs on tensor cores; other D (multiples of 8 in bf16) up to 512, other
+ *   page sizes and PT_F32 on CUDA cores.
+ *   Errors: PT_ERR_INVALID_ARG and PT_ERR_UNSUPPORTED as for pt_attn_fwd,
+ *   and for a workspace that is too small, a plan of another device or a bad
+ *   stride.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a length
+ *   outside [0, max_pages * page_size] or a count outside [0, q_len] (the
+ *   nearest is taken), a page id outside [0, n_pages) (page 0 is read).
+ * ------------------------------------------------------------------------- */
+typedef struct pt_decodeplan pt_decodeplan;
+pt_status pt_cache_tables(const int32_t* held, const int32_t* added, const int32_t* start, int32_t n_rows,
+                          int32_t page_size, int32_t* tables, int32_t max_pages, int32_t* ring, int32_t ring_cap,
+                          const int64_t* counters, int32_t* lens, int32_t* row_ptr, int64_t* slots,
+                          int64_t* positions, int32_t max_new, int64_t* counters_out, cudaStream_t stream);
+pt_status pt_cache_write(const void* K, const void* V, int64_t k_stride, int64_t v_stride, pt_dtype dtype, int32_t T,
+                         int32_t Hkv, int32_t D, const int64_t* slots, void* Kc, void* Vc, int32_t n_pages,
+                         int32_t page_size, cudaStream_t stream);
+pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, const int32_t* path_nodes, int32_t n_samples,
+                         int32_t Hq, int32_t Hkv, int32_t q_len, cudaStream_t stream, pt_decodeplan** out);
+void pt_decodeplan_free(pt_decodeplan* plan);
+size_t pt_decode_workspace_bytes(const pt_decodeplan* plan, int32_t D);
+pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, pt_dtype dtype, int32_t D,
+                         int32_t n_pages, int32_t page_size, const int32_t* tables, int32_t max_pages,
+                         const int32_t* lens, const int32_t* q_count, float scale, const pt_decodeplan* plan, void* O,
+                         float* LSE, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronise the stream, then return and clear the device status word:
  * PT_ERR_TIMEOUT if an in-kernel wait ran out since the last check,
- * PT_ERR_INVALID_ARG if a device-side check of a block map failed (see
- * pt_build_blockmap_tree and pt_build_blockmap_seg), PT_ERR_CUDA if the
- * stream reported an error, else PT_OK. */
+ * PT_ERR_INVALID_ARG if a device-side check of a block map (see
+ * pt_build_blockmap_tree and pt_build_blockmap_seg) or of the cache calls'
+ * lengths, slots and pages failed, PT_ERR_NOMEM if a cache ran out of pages,
+ * PT_ERR_CUDA if the stream reported an error, else PT_OK. */
 pt_status pt_sync_status(cudaStream_t stream);
 
 /* Message for the last failing call on this thread ("" if none). */
@@ -559,7 +665,9 @@ pt_status pt_debug_exp2(const float* x, float* y, int64_t n, int32_t method, cud
  * "bwd_dq", "bwd_simt",
  * "blockmap_classify" (tile classes, list sizes, orders),
  * "blockmap_lists" (lists and masks), and the fold calls' "fold_plan",
- * "fold", "unfold", "unfold_grad", "fold_positions", "fold_mismatches".  pt_profile_reset drops every record
+ * "fold", "unfold", "unfold_grad", "fold_positions", "fold_mismatches",
+ * and the cache and decoding calls' "cache_tables", "cache_write",
+ * "decode_simt", "decode_tc", "decode_merge".  pt_profile_reset drops every record
  * (its events go back to the pool once they have completed). */
 void pt_profile_enable(int on);
 pt_status pt_profile_read(const char* kernel, int64_t* launches, double* total_ms);

@@ -20,6 +20,7 @@ __all__ = [
     "build_blockmap_draft",
     "attn_fwd", "attn_bwd", "bwd_workspace_bytes", "sync_status", "launch_count", "LIB_PATH",
     "profile_enable", "profile_read", "profile_reset", "attn_bwd_noalloc", "FoldPlan", "fold_plan",
+    "cache_tables", "cache_write", "DecodePlan", "decode_plan", "attn_decode",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpt.so")
@@ -102,6 +103,11 @@ def load_library(path: Optional[str] = None):
             "pt_fold_positions": [vp, vp, vp],
             "pt_fold_mismatches": [vp, vp, i64, vp, vp],
             "pt_debug_pool_usage": [i32, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)],
+            "pt_cache_tables": [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp],
+            "pt_cache_write": [vp, vp, i64, i64, ctypes.c_int, i32, i32, i32, vp, vp, vp, i32, i32, vp],
+            "pt_decode_plan": [i32, vp, vp, i32, i32, i32, i32, vp, pp],
+            "pt_attn_decode": [vp, i64, vp, vp, ctypes.c_int, i32, i32, i32, vp, i32, vp, vp, f32, vp, vp, vp, vp, sz,
+                               vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -111,6 +117,10 @@ def load_library(path: Optional[str] = None):
         lib.pt_blockmap_free.restype = None
         lib.pt_foldplan_free.argtypes = [vp]
         lib.pt_foldplan_free.restype = None
+        lib.pt_decodeplan_free.argtypes = [vp]
+        lib.pt_decodeplan_free.restype = None
+        lib.pt_decode_workspace_bytes.argtypes = [vp, i32]
+        lib.pt_decode_workspace_bytes.restype = sz
         lib.pt_hoststep_free.argtypes = [vp]
         lib.pt_hoststep_free.restype = None
         lib.pt_bwd_workspace_bytes.argtypes = [i32, i32, i32]
@@ -570,3 +580,193 @@ class FoldPlan:
 def fold_plan(node_lengths, path_ptr, path_nodes, row_len: int, stream=None) -> FoldPlan:
     """Plan of the shared-prefix fold for a tree and a rollout row length."""
     return FoldPlan(node_lengths, path_ptr, path_nodes, row_len, stream)
+
+
+def _need(t, name: str, dtype, shape=None, device=None):
+    """Check one tensor of the cache calls: on the current device, of this
+    dtype, dense, and of this shape where one is given."""
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {device}")
+
+
+def _launch_stream(stream, *held):
+    """The raw stream of a call.  On a stream of the caller's choice, the
+    tensors allocated here (`held`) are marked as used on it."""
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        for t in held:
+            t.record_stream(stream)
+    return int(stream.cuda_stream)
+
+
+def cache_tables(held, added, tables, ring, counters, page_size: int, max_new: int, start=None, stream=None) -> Tuple:
+    """One step of a paged cache's rows (pt_cache_tables): row i goes from
+    held[i] to held[i] + added[i] tokens, taking pages from the ring of free
+    ids or giving them back.  CUDA int32 tensors held, added, start [n], tables
+    [n, max_pages] and ring [cap]; counters int64 [2].  tables and ring change
+    in place; returns new lens [n], counters [2], row_ptr [n + 1], and the
+    added tokens' slots and position ids (int64 [max_new])."""
+    import torch
+
+    i32, i64 = torch.int32, torch.int64
+    dev = torch.cuda.current_device()
+    n = held.numel()
+    _need(held, "held", i32, (n,), dev)
+    _need(added, "added", i32, (n,), dev)
+    _need(ring, "ring", i32, (ring.numel(),), dev)
+    _need(counters, "counters", i64, (2,), dev)
+    _need(tables, "tables", i32, None, dev)
+    if tables.dim() != 2 or tables.shape[0] != n:
+        raise ValueError(f"tables has shape {tuple(tables.shape)}, ({n}, max_pages) expected")
+    if start is not None:
+        _need(start, "start", i32, (n,), dev)
+    if not 0 <= max_new <= 1 << 30:
+        raise ValueError(f"max_new = {max_new} is out of range")
+    d = held.device
+    lens, row_ptr = _empty((n,), i32, d), _empty((n + 1,), i32, d)
+    slots, positions = _empty((max_new,), i64, d), _empty((max_new,), i64, d)
+    out = _empty((2,), i64, d)
+    _check(load_library().pt_cache_tables(
+        held.data_ptr(), added.data_ptr(), start.data_ptr() if start is not None else None, n, page_size,
+        tables.data_ptr(), tables.shape[1], ring.data_ptr(), ring.numel(), counters.data_ptr(), lens.data_ptr(),
+        row_ptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), max_new, out.data_ptr(),
+        _launch_stream(stream, lens, row_ptr, slots, positions, out)))
+    return lens, out, row_ptr, slots, positions
+
+
+def _cache_shape(Kc, Vc, dtype, dev):
+    _need(Kc, "Kc", dtype, None, dev)
+    _need(Vc, "Vc", dtype, Kc.shape, dev)
+    if Kc.dim() != 4:
+        raise ValueError("Kc and Vc are [n_pages, Hkv, page_size, D]")
+    return Kc.shape
+
+
+def _token_rows(t, name, dtype, heads, D, dev):
+    """[T, heads, D] tokens whose heads are dense (a slice of a fused
+    projection will do); returns the elements between tokens."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor [T, heads, head_dim] of {dtype} on the current device")
+    if t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, (T, {heads}, {D}) expected")
+    st = t.stride()
+    if t.numel() and ((D > 1 and st[2] != 1) or (heads > 1 and st[1] != D) or (t.shape[0] > 1 and st[0] < heads * D)):
+        raise ValueError(f"{name}: the heads of a token must be dense and tokens must not overlap")
+    return st[0] if t.shape[0] > 1 else heads * D
+
+
+def cache_write(K, V, slots, Kc, Vc, stream=None) -> None:
+    """Put tokens' K and V [T, Hkv, D] into their slots (int64 [T], negative:
+    passed over) of the cache Kc, Vc [n_pages, Hkv, page_size, D], in place."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    n_pages, Hkv, ps, D = _cache_shape(Kc, Vc, K.dtype, dev)
+    code = _dtype_code(K)
+    ks, vs = _token_rows(K, "K", K.dtype, Hkv, D, dev), _token_rows(V, "V", K.dtype, Hkv, D, dev)
+    T = K.shape[0]
+    if V.shape[0] != T:
+        raise ValueError(f"K has {T} tokens, V {V.shape[0]}")
+    _need(slots, "slots", torch.int64, (T,), dev)
+    _check(load_library().pt_cache_write(K.data_ptr(), V.data_ptr(), ks, vs, code, T, Hkv, D, slots.data_ptr(),
+                                         Kc.data_ptr(), Vc.data_ptr(), n_pages, ps, _launch_stream(stream)))
+
+
+class DecodePlan:
+    """Plan of the decoding attention for a tree's paths and a head layout
+    (pt_decode_plan).  It holds no lengths: one plan serves every layer and
+    step until a path changes."""
+
+    def __init__(self, n_nodes: int, path_ptr, path_nodes, Hq: int, Hkv: int, q_len: int = 1, stream=None):
+        import numpy as np
+
+        self._h = None
+        self._lib = load_library()
+        pp = np.ascontiguousarray(np.asarray(path_ptr, dtype=np.int32))
+        pn = np.ascontiguousarray(np.asarray(path_nodes, dtype=np.int32))
+        if pp.size < 1 or (pp.size > 1 and int(pp[-1]) > pn.size):
+            raise ValueError("path_ptr runs past path_nodes")
+        out = ctypes.c_void_p()
+        _check(self._lib.pt_decode_plan(int(n_nodes), pp.ctypes.data, pn.ctypes.data if pn.size else None,
+                                        int(pp.size - 1), int(Hq), int(Hkv), int(q_len),
+                                        ctypes.c_void_p(_stream(stream)), ctypes.byref(out)))
+        self._h = out
+        self.n_nodes, self.n_samples, self.Hq, self.Hkv, self.q_len = n_nodes, int(pp.size - 1), Hq, Hkv, q_len
+
+    @property
+    def handle(self):
+        return self._h
+
+    def workspace_bytes(self, D: int) -> int:
+        """Bytes of scratch attn_decode needs at this head_dim."""
+        return int(self._lib.pt_decode_workspace_bytes(self._h, int(D)))
+
+    def free(self):
+        if self._h is not None and self._h.value:
+            self._lib.pt_decodeplan_free(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def decode_plan(n_nodes: int, path_ptr, path_nodes, Hq: int, Hkv: int, q_len: int = 1, stream=None) -> DecodePlan:
+    """Plan of the decoding attention: host int32 CSR paths over cache rows."""
+    return DecodePlan(n_nodes, path_ptr, path_nodes, Hq, Hkv, q_len, stream)
+
+
+def attn_decode(Q, Kc, Vc, tables, lens, plan: DecodePlan, q_count=None, scale: float = 0.0, O=None, LSE=None,
+                workspace=None, stream=None) -> Tuple:
+    """O [n_samples * q_len, Hq, D] and LSE [Hq, n_samples * q_len] (fp32) of
+    the samples' newest tokens Q over the cache Kc, Vc [n_pages, Hkv,
+    page_size, D], tables [n_nodes, max_pages], lens [n_nodes] (pt_attn_decode).
+    With q_count, rows behind a sample's queries keep what O and LSE held."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    n_pages, Hkv, ps, D = _cache_shape(Kc, Vc, Q.dtype, dev)
+    code = _dtype_code(Q)
+    T = plan.n_samples * plan.q_len
+    if Hkv != plan.Hkv:
+        raise ValueError(f"the cache has {Hkv} kv heads, the plan {plan.Hkv}")
+    qs = _token_rows(Q, "Q", Q.dtype, plan.Hq, D, dev)
+    if Q.shape[0] != T:
+        raise ValueError(f"Q has {Q.shape[0]} tokens, the plan {T}")
+    _need(tables, "tables", torch.int32, None, dev)
+    if tables.dim() != 2 or tables.shape[0] != plan.n_nodes:
+        raise ValueError(f"tables has shape {tuple(tables.shape)}, ({plan.n_nodes}, max_pages) expected")
+    _need(lens, "lens", torch.int32, (plan.n_nodes,), dev)
+    if q_count is not None:
+        _need(q_count, "q_count", torch.int32, (plan.n_samples,), dev)
+    held = []
+    if O is None:
+        O = _empty((T, plan.Hq, D), Q.dtype, Q.device)
+        held.append(O)
+    else:
+        _need(O, "O", Q.dtype, (T, plan.Hq, D), dev)
+    if LSE is None:
+        LSE = _empty((plan.Hq, T), torch.float32, Q.device)
+        held.append(LSE)
+    else:
+        _need(LSE, "LSE", torch.float32, (plan.Hq, T), dev)
+    if workspace is None:
+        workspace = _empty((plan.workspace_bytes(D),), torch.uint8, Q.device)
+        held.append(workspace)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise TypeError("workspace must be a contiguous CUDA tensor on the current device")
+    _check(load_library().pt_attn_decode(
+        Q.data_ptr(), qs, Kc.data_ptr(), Vc.data_ptr(), code, D, n_pages, ps, tables.data_ptr(), tables.shape[1],
+        lens.data_ptr(), q_count.data_ptr() if q_count is not None else None, scale, plan.handle, O.data_ptr(),
+        LSE.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _launch_stream(stream, *held)))
+    return O, LSE

@@ -419,6 +419,7 @@ pt_status pt_sync_status(cudaStream_t stream) {
   int worst = 0;
   int codes[] = {pt::take_status_blockmap(stream), pt::take_status_fwd(stream), pt::take_status_bwd(stream),
                  pt::take_status_simt(stream), pt::take_status_fold(stream)};
+  const int cache[] = {pt::take_status_cache(stream), pt::take_status_decode(stream)};
   for (int c : codes) {
     if (c < 0) {
       set_error("pt_sync_status: could not read the device status word");
@@ -426,7 +427,15 @@ pt_status pt_sync_status(cudaStream_t stream) {
     }
     if (c && !worst) worst = c;
   }
-  if (worst == PT_STATUS_TIMEOUT) {
+  int cached = 0;
+  for (int c : cache) {
+    if (c < 0) {
+      set_error("pt_sync_status: could not read the device status word");
+      return PT_ERR_CUDA;
+    }
+    if (c && !cached) cached = c;
+  }
+  if (worst == PT_STATUS_TIMEOUT || (!worst && cached == PT_STATUS_TIMEOUT)) {
     set_error("a bounded in-kernel wait ran out");
     return PT_ERR_TIMEOUT;
   }
@@ -435,6 +444,15 @@ pt_status pt_sync_status(cudaStream_t stream) {
               "kept pairs missing from the lists, or more partial tiles than the lists' bound)");
     return PT_ERR_INVALID_ARG;
   }
+  if (!worst && cached == PT_STATUS_NOMEM) {
+    set_error("the cache ran out of free pages");
+    return PT_ERR_NOMEM;
+  }
+  if (!worst && cached == PT_STATUS_INVALID) {
+    set_error("a device-side check of the cache calls failed (a length, count, slot, page id or ring counter out of range)");
+    return PT_ERR_INVALID_ARG;
+  }
+  if (!worst) worst = cached;
   if (worst) {
     set_error("device status %d", worst);
     return PT_ERR_CUDA;

@@ -9,6 +9,7 @@
 #define PT_STATUS_OK 0
 #define PT_STATUS_INVALID 1
 #define PT_STATUS_TIMEOUT 4
+#define PT_STATUS_NOMEM 5
 
 // Kinds of a (q tile, kv block) pair in the block map.
 #define PT_KIND_EMPTY 0
@@ -174,6 +175,8 @@ int take_status_fwd(cudaStream_t s);
 int take_status_bwd(cudaStream_t s);
 int take_status_simt(cudaStream_t s);
 int take_status_fold(cudaStream_t s);
+int take_status_cache(cudaStream_t s);
+int take_status_decode(cudaStream_t s);
 
 // Block-map builders (pt_blockmap.cu).  Return a PT_* status code.
 int build_tree(const int32_t* node_lengths, int32_t n_nodes, const int32_t* path_ptr, const int32_t* path_nodes,
