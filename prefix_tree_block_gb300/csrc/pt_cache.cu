@@ -24,7 +24,7 @@ using namespace pt;
 
 namespace {
 
-constexpr int kTabWarps = 16;
+constexpr int kTabWarps = 32;
 constexpr int kTabMaxRows = 1 << 18;  // 12 bytes of shared memory per 32 rows
 constexpr int kTabMaxNew = 1 << 30;
 
@@ -90,13 +90,37 @@ struct TabArgs {
   int n, ps, cap, max_pages, max_new;
 };
 
+// Walks a line of units that belong to chunks of rows (cum: exclusive sums over
+// chunks, cum[nc] all of them), cut into runs of kRun for the warps: f(chunk,
+// x0, x1) for each chunk's part of a run.  A chunk counts kPad units more than
+// it has, what looking at its rows costs: without that, a run over rows of one
+// token each would visit dozens of chunks one after another.
+constexpr int kRun = 256, kPad = 64;
+template <class F>
+__device__ __forceinline__ void for_line(const int* cum, int nc, int upto, int first, int warps, F f) {
+  const int line = upto + kPad * nc;
+  for (int r = first; (long long)r * kRun < line; r += warps) {
+    int pos = r * kRun;
+    const int end = min(pos + kRun, line);
+    int c = 0;
+    for (int span = 1 << (31 - __clz(nc)); span; span >>= 1)
+      if (c + span < nc && cum[c + span] + kPad * (c + span) <= pos) c += span;
+    for (; pos < end && c < nc; ++c) {
+      const int lo = cum[c], hi = min(cum[c + 1], upto), shift = lo + kPad * c;
+      const int x0 = lo + pos - shift, x1 = min(lo + end - shift, hi);
+      if (x0 < x1) f(c, x0, x1);
+      pos = max(pos, cum[c + 1] + kPad * (c + 1));
+    }
+  }
+}
+
 // One launch.  Every CTA sums the rows' tokens and pages itself, 32 rows (a
 // chunk) per warp step, and scans the chunk sums in shared memory (three sums
-// per chunk), so no CTA waits for another.  Then chunk c's rows and page moves
-// belong to CTA c mod gridDim, and the slots to the CTAs in equal runs of
-// tokens, whatever the rows' lengths.  A slot's page comes from the row's
-// table when the row held that page before, else straight from the ring, so
-// nothing written here is read here.
+// per chunk), so no CTA waits for another.  Then the pages taken, the pages
+// given back and the tokens' slots are three lines of units, each cut evenly
+// over all warps whatever the rows' lengths.  A slot's page comes from the
+// row's table when the row held that page before, else straight from the ring,
+// so nothing written here is read here.
 __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a) {
   pdl_wait();
   extern __shared__ int sm[];
@@ -106,6 +130,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
   int* c_take = sm + (nc + 1);
   int* c_back = sm + 2 * (nc + 1);
   const long long most = (long long)a.max_pages * a.ps;
+#pragma unroll 4
   for (int c = warp; c < nc; c += kTabWarps) {
     const int i = c * 32 + lane;
     RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
@@ -151,91 +176,104 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
     a.counters_out[1] = tail + (ring_bad ? 0 : min(n_back, room));
     a.row_ptr[a.n] = n_new;
   }
-  // rows and page moves
+  // the rows' own outputs
   for (int c = blockIdx.x + gridDim.x * warp; c < nc; c += gridDim.x * kTabWarps) {
     const int i = c * 32 + lane;
     const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
     const int e_new = c_new[c] + warp_incl_scan(m.grow, lane) - m.grow;
-    const int s_take = warp_incl_scan(m.take, lane), s_back = warp_incl_scan(m.back, lane);
-    const int e_take = s_take - m.take, e_back = s_back - m.back;
-    const int w_take = __shfl_sync(0xffffffffu, s_take, 31), w_back = __shfl_sync(0xffffffffu, s_back, 31);
+    const int e_take = warp_incl_scan(m.take, lane) - m.take;
     if (i < a.n) {
       a.row_ptr[i] = e_new;
       // a row that got fewer pages than it needs holds what fits in them
       const int got = min(m.take, max(avail - (c_take[c] + e_take), 0));
       a.lens[i] = got < m.take ? (int)min((long long)m.len, (long long)(m.p0 + got) * a.ps) : m.len;
     }
-    for (int x0 = 0; x0 < w_take; x0 += 32) {
-      const int x = x0 + lane, l = lane_of(e_take, x);
-      const int k = x - __shfl_sync(0xffffffffu, e_take, l), p0 = __shfl_sync(0xffffffffu, m.p0, l);
-      if (x < w_take && c_take[c] + x < avail) {
-        int at = h0 + c_take[c] + x;
-        if (at >= a.cap) at -= a.cap;
-        a.tables[(size_t)(c * 32 + l) * a.max_pages + p0 + k] = a.ring[at];
-      }
-    }
-    for (int x0 = 0; x0 < w_back; x0 += 32) {
-      const int x = x0 + lane, l = lane_of(e_back, x);
-      const int k = x - __shfl_sync(0xffffffffu, e_back, l), p1 = __shfl_sync(0xffffffffu, m.p1, l);
-      if (x < w_back && c_back[c] + x < room && !ring_bad) {
-        int at = t0 + c_back[c] + x;
-        if (at >= a.cap) at -= a.cap;
-        const int page = a.tables[(size_t)(c * 32 + l) * a.max_pages + p1 + k];
-        if (page < 0) record_status(PT_STATUS_INVALID);
-        a.ring[at] = page;
-      }
-    }
   }
-  // slots and position ids: a warp takes 32 x kRun tokens in a row
-  constexpr int kRun = 8;
+  const int warps = gridDim.x * kTabWarps, me = blockIdx.x + gridDim.x * warp;
+  constexpr int U = 4;  // loads in flight per lane
+  if (n_take)
+    for_line(c_take, nc, min(n_take, avail), me, warps, [&](int c, int x0, int x1) {
+      const int i = c * 32 + lane;
+      const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
+      const int excl = c_take[c] + warp_incl_scan(m.take, lane) - m.take;
+      for (int x = x0; x < x1; x += 32 * U) {
+        int id[U];
+        size_t at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int y = min(x + u * 32 + lane, x1 - 1), l = lane_of(excl, y);
+          at[u] = (size_t)(c * 32 + l) * a.max_pages + __shfl_sync(0xffffffffu, m.p0, l) + y - __shfl_sync(0xffffffffu, excl, l);
+          const int r = h0 + y;
+          id[u] = a.ring[r >= a.cap ? r - a.cap : r];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (x + u * 32 + lane < x1) a.tables[at[u]] = id[u];
+      }
+    });
+  if (n_back && !ring_bad)
+    for_line(c_back, nc, min(n_back, room), warps - 1 - me, warps, [&](int c, int x0, int x1) {
+      const int i = c * 32 + lane;
+      const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
+      const int excl = c_back[c] + warp_incl_scan(m.back, lane) - m.back;
+      for (int x = x0; x < x1; x += 32 * U) {
+        int id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int y = min(x + u * 32 + lane, x1 - 1), l = lane_of(excl, y);
+          id[u] = a.tables[(size_t)(c * 32 + l) * a.max_pages + __shfl_sync(0xffffffffu, m.p1, l) + y -
+                           __shfl_sync(0xffffffffu, excl, l)];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (x + u * 32 + lane < x1) {
+            const int r = t0 + x + u * 32 + lane;
+            if (id[u] < 0) record_status(PT_STATUS_INVALID);
+            a.ring[r >= a.cap ? r - a.cap : r] = id[u];
+          }
+      }
+    });
   const int n_real = min(n_new, a.max_new);
-  const int runs = (a.max_new + 32 * kRun - 1) / (32 * kRun);
-  for (int r = blockIdx.x + gridDim.x * warp; r < runs; r += gridDim.x * kTabWarps) {
-    const int tb = r * 32 * kRun, te = min(tb + 32 * kRun, a.max_new);
-    int t = tb;
-    if (t < n_real) {
-      // the chunk that holds token t: the last with c_new <= t
-      int c = 0;
-      for (int span = 1 << (31 - __clz(nc)); span; span >>= 1)
-        if (c + span < nc && c_new[c + span] <= t) c += span;
-      const int t_end = min(te, n_real);
-      while (t < t_end) {
-        const int i = c * 32 + lane;
-        const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
-        const int e_new = c_new[c] + warp_incl_scan(m.grow, lane) - m.grow;
-        const int e_take = c_take[c] + warp_incl_scan(m.take, lane) - m.take;
-        const int st = a.start && i < a.n ? a.start[i] : 0;
-        const int c_end = min(t_end, c_new[c + 1]);
-        for (; t < c_end; t += 32) {
-          const int x = t + lane, l = lane_of(e_new, min(x, c_end - 1));
-          const int tok = __shfl_sync(0xffffffffu, m.held, l) + x - __shfl_sync(0xffffffffu, e_new, l);
+  if (n_real)
+    for_line(c_new, nc, n_real, (me + warps / 2) % warps, warps, [&](int c, int x0, int x1) {
+      const int i = c * 32 + lane;
+      const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
+      const int st = a.start && i < a.n ? a.start[i] : 0;
+      const int e_new = c_new[c] + warp_incl_scan(m.grow, lane) - m.grow;
+      const int e_take = c_take[c] + warp_incl_scan(m.take, lane) - m.take;
+      for (int x = x0; x < x1; x += 32 * U) {
+        int page[U], tok[U], pos[U], rest[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int y = min(x + u * 32 + lane, x1 - 1), l = lane_of(e_new, y);
+          tok[u] = __shfl_sync(0xffffffffu, m.held, l) + y - __shfl_sync(0xffffffffu, e_new, l);
+          pos[u] = __shfl_sync(0xffffffffu, st, l);
           const int p0 = __shfl_sync(0xffffffffu, m.p0, l), et = __shfl_sync(0xffffffffu, e_take, l);
-          const int s0 = __shfl_sync(0xffffffffu, st, l);
-          if (x < c_end) {
-            const int pi = tok / a.ps;
-            long long slot = -1;
-            int page = -1;
-            if (tok < 0 || pi >= a.max_pages) {  // only when the rows' tokens together pass kTabMaxNew
-            } else if (pi < p0) {
-              page = a.tables[(size_t)(c * 32 + l) * a.max_pages + pi];
-            } else if (et + pi - p0 < avail) {
-              int at = h0 + et + pi - p0;
-              if (at >= a.cap) at -= a.cap;
-              page = a.ring[at];
-            }
-            if (page >= 0) slot = (long long)page * a.ps + (tok - pi * a.ps);
-            a.slots[x] = slot;
-            if (a.positions) a.positions[x] = (long long)s0 + tok;
+          const int pi = tok[u] / a.ps;
+          rest[u] = tok[u] - pi * a.ps;
+          page[u] = -1;
+          if (tok[u] < 0 || pi >= a.max_pages) {  // only when the rows' tokens together pass kTabMaxNew
+          } else if (pi < p0) {
+            page[u] = a.tables[(size_t)(c * 32 + l) * a.max_pages + pi];
+          } else if (et + pi - p0 < avail) {
+            const int r = h0 + et + pi - p0;
+            page[u] = a.ring[r >= a.cap ? r - a.cap : r];
           }
         }
-        t = c_end;
-        ++c;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int y = x + u * 32 + lane;
+          if (y < x1) {
+            a.slots[y] = page[u] >= 0 ? (long long)page[u] * a.ps + rest[u] : -1;
+            if (a.positions) a.positions[y] = (long long)pos[u] + tok[u];
+          }
+        }
       }
-    }
-    for (int x = max(t, tb) + lane; x < te; x += 32) {  // behind the last token
-      a.slots[x] = -1;
-      if (a.positions) a.positions[x] = 0;
-    }
+    });
+  // behind the last token
+  for (int y = n_real + blockIdx.x * blockDim.x + threadIdx.x; y < a.max_new; y += gridDim.x * blockDim.x) {
+    a.slots[y] = -1;
+    if (a.positions) a.positions[y] = 0;
   }
 }
 
@@ -376,7 +414,7 @@ extern "C" pt_status pt_cache_tables(const int32_t* held, const int32_t* added, 
     }
     opted[dev] = true;
   }
-  // one CTA up to 4096 tokens or 512 rows; then enough for about 4096 tokens each
+  // one CTA up to 4096 tokens and 512 rows; then enough for a run or two per warp
   const long long by_new = ((long long)max_new + 4095) / 4096, by_rows = ((long long)n_rows + 511) / 512;
   const int grid = (int)std::max(1LL, std::min<long long>(std::max(by_new, by_rows), num_sms(dev)));
   cudaError_t e;

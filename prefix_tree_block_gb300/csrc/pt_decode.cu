@@ -64,9 +64,8 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
   DecPiece p;
   const int my_r = lane >> 3;  // the row whose scores this lane holds
   while (walk.next(p)) {
-    const int len = dec_len(a, p.node, false);
     int b, e;
-    dec_range(a, p.kind, len, b, e);
+    dec_range(a, p.kind, p.len, b, e);
     float q[R][DL], acc[R][DL];
     int lim_max = 0, lim_min = INT_MAX, my_lim = 0;
     int lim[R];
@@ -76,9 +75,9 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       lim[r] = 0;
       const E* src = nullptr;
       if (row < p.rows) {
-        const DecRow d = dec_row(a, p.node, p.hk, row, len);
+        const DecRow d = dec_row(a, p.member0, p.hk, row, p.len);
         lim[r] = d.lim;
-        src = Qp + (long long)(d.s * a.q_len + d.j) * a.q_stride + (long long)d.head * a.D;
+        src = Qp + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
       }
       lim_max = max(lim_max, lim[r]);
       lim_min = min(lim_min, lim[r]);
@@ -202,13 +201,14 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 // ---------------------------------------------------------------------------
 // Merge: O = sum_p 2^(lse_p - LSE) O_p over a row's pieces, in path order and
 // along each segment, so the sum's order is fixed.  A block takes one query
-// token's q head; its warps take every fourth piece, lanes the columns.
+// token's q head; its four warps take every fourth piece, lanes the columns.
+// Latency is all it is: the path's entries are looked up side by side, one per
+// lane, and four pieces are loaded at a time.
 // ---------------------------------------------------------------------------
 struct MergeArgs {
   DecArgs d;
-  DecClass c0, c1;    // the classes of the path entries: first, second
-  int first;          // class number of c0
-  int R0, R1, BT0, BT1;
+  DecClass c0, c1;  // c1: the tile class, or none
+  int R0, BT0;
   const int* path_ptr;
   const int2* path_ent;
   int n_samples;
@@ -217,41 +217,80 @@ struct MergeArgs {
 };
 
 template <int CPL>  // columns per lane
-__device__ __forceinline__ void merge_row(const MergeArgs& m, int s, int j, int head, int warp, int lane, float& mx,
-                                          float& sum, float (&acc)[CPL]) {
+struct MergeAcc {
+  float mx, sum, acc[CPL];
+  int turn;  // pieces so far, mod 4
+};
+
+// The pieces of up to 32 path entries (lane i: node, member index) in one class.
+template <int CPL, bool TILE>
+__device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& c, int node, int mem, bool have, int j,
+                                            int head, int warp, int lane, MergeAcc<CPL>& s) {
   const DecArgs& a = m.d;
-  int turn = 0;  // pieces so far, mod 4
+  const int R = TILE ? kTileR : m.R0, BT = TILE ? kTileBT : m.BT0;
   const int hk = head / a.g;
-  for (int k = m.path_ptr[s]; k < m.path_ptr[s + 1]; ++k) {
-    const int2 en = m.path_ent[k];
-    const bool first = (en.x >> 28) == m.first;
-    const DecClass& c = first ? m.c0 : m.c1;
-    const int R = first ? m.R0 : m.R1, BT = first ? m.BT0 : m.BT1;
-    const int si = en.x & ((1 << 28) - 1);
-    const int4 sg = c.seg[si];
-    int b, e;
-    dec_range(a, sg.y, dec_len(a, sg.x, false), b, e);
-    const int tiles = (e - b + BT - 1) / BT;
-    if (tiles == 0) continue;
-    const int row = (en.y * a.q_len + j) * a.g + head - hk * a.g;
-    const int rt = row / R, it = rt * a.Hkv + hk;
-    const long long per = c.pref[c.nseg], u0 = c.pref[si] + (long long)it * tiles;
-    const long long w0 = u0 / per, w1 = (u0 + tiles - 1) / per;
-    for (long long w = w0 + ((warp - turn) & 3); w <= w1; w += 4) {
-      const long long at = (w + sg.w + it) * R + (row - rt * R);
-      const float x = c.lse[at];
-      float o[CPL];
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) o[i] = lane + i * 32 < a.D ? c.opart[at * a.D + lane + i * 32] : 0.f;
-      if (x == -INFINITY) continue;
-      const float mn = fmaxf(mx, x), al = ex2(mx - mn), f = ex2(x - mn);
-      mx = mn;
-      sum = fmaf(sum, al, f);
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) acc[i] = fmaf(acc[i], al, f * o[i]);
+  int count = 0, two = 0, rin = 0;
+  long long slot0 = 0;
+  if (have) {
+    const DecSeg sg = load_seg(c.seg + node);
+    const int raw = a.lens[node];
+    const long long pref = c.pref[node], per = c.pref[c.nseg];
+    if (sg.rows_kind) {
+      int b, e;
+      dec_range(a, sg.kind(), dec_clamp(a, raw, false), b, e);
+      const int tiles = (e - b + BT - 1) / BT;
+      if (tiles > 0) {
+        const int row = (mem * a.q_len + j) * a.g + head - hk * a.g, rt = row / R, it = rt * a.Hkv + hk;
+        rin = row - rt * R;
+        two = TILE && sg.rows() - rt * R <= kTileR / 2;
+        const long long u0 = pref + (long long)it * tiles, u1 = u0 + tiles - 1;
+        long long w0, w1;
+        if (u1 < INT_MAX && per < INT_MAX)
+          w0 = (int)u0 / (int)per, w1 = (int)u1 / (int)per;
+        else
+          w0 = u0 / per, w1 = u1 / per;
+        slot0 = w0 + sg.item0 + it;
+        count = (int)(w1 - w0 + 1) << two;
+      }
     }
-    turn = (int)((turn + (w1 - w0 + 1)) & 3);
   }
+  int incl = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  const int excl = incl - count, total = __shfl_sync(0xffffffffu, incl, 31);
+  for (int x0 = (warp - s.turn) & 3; x0 < total; x0 += 16) {
+    float ls[4], o[4][CPL];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = min(x0 + 4 * u, total - 1);
+      int l = 0;
+#pragma unroll
+      for (int q = 16; q; q >>= 1)
+        if (__shfl_sync(0xffffffffu, excl, l + q) <= x) l += q;
+      const int y = x - __shfl_sync(0xffffffffu, excl, l), tw = __shfl_sync(0xffffffffu, two, l);
+      const long long at = (__shfl_sync(0xffffffffu, slot0, l) + (y >> tw)) * R + __shfl_sync(0xffffffffu, rin, l) +
+                           (y & tw) * (kTileR / 2);
+      ls[u] = -INFINITY;
+      if (x0 + 4 * u < total) {
+        ls[u] = c.lse[at];
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) o[u][i] = lane + i * 32 < a.D ? c.opart[at * a.D + lane + i * 32] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (ls[u] == -INFINITY) continue;
+      const float mn = fmaxf(s.mx, ls[u]), al = ex2(s.mx - mn), f = ex2(ls[u] - mn);
+      s.mx = mn;
+      s.sum = fmaf(s.sum, al, f);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) s.acc[i] = fmaf(s.acc[i], al, f * o[u][i]);
+    }
+  }
+  s.turn = (s.turn + total) & 3;
 }
 
 template <class E, int CPL>
@@ -262,18 +301,25 @@ __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
   const DecArgs& a = m.d;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int head = blockIdx.x % a.Hq, tok = blockIdx.x / a.Hq, s = tok / a.q_len, j = tok - s * a.q_len;
+  const int k0 = m.path_ptr[s], k1 = m.path_ptr[s + 1];
   if (a.q_count) {
     const int n = a.q_count[s];
     if ((n < 0 || n > a.q_len) && threadIdx.x == 0) record_status(PT_STATUS_INVALID);
     if (j >= dec_count(a, s)) return;  // the row stays as it was
   }
-  float mx = -INFINITY, sum = 0.f, acc[CPL];
+  MergeAcc<CPL> r;
+  r.mx = -INFINITY, r.sum = 0.f, r.turn = 0;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) acc[i] = 0.f;
-  merge_row<CPL>(m, s, j, head, warp, lane, mx, sum, acc);
-  if (lane == 0) sm_m[warp] = mx, sm_l[warp] = sum;
+  for (int i = 0; i < CPL; ++i) r.acc[i] = 0.f;
+  for (int k = k0; k < k1; k += 32) {
+    const bool have = k + lane < k1;
+    const int2 en = have ? m.path_ent[k + lane] : make_int2(0, 0);
+    if (m.c0.nitems) merge_class<CPL, false>(m, m.c0, en.x, en.y, have, j, head, warp, lane, r);
+    if (m.c1.nitems) merge_class<CPL, true>(m, m.c1, en.x, en.y, have, j, head, warp, lane, r);
+  }
+  if (lane == 0) sm_m[warp] = r.mx, sm_l[warp] = r.sum;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) sm_o[warp][lane + i * 32] = acc[i];
+  for (int i = 0; i < CPL; ++i) sm_o[warp][lane + i * 32] = r.acc[i];
   __syncthreads();
   float top = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
   float f[4], all = 0.f;
@@ -313,29 +359,33 @@ size_t pad256(size_t b) { return (b + 255) & ~size_t(255); }
 size_t class_bytes(const pt_decodeplan* p, int cls, int D) {
   const pt_decodeplan::Class& c = p->cls[cls];
   if (!c.nitems) return 0;
-  const size_t R = cls == kDecSimt ? kSimtR : cls == kDecRows ? kRowsR : kTileR;
-  const size_t slots = (size_t)c.nitems + dec_workers(p, cls);
-  return pad256(8 * ((size_t)c.nseg + 1)) + pad256(4 * slots * R) + pad256(4 * slots * R * D);
+  const size_t R = dec_r(cls), slots = (size_t)c.nitems + dec_workers(p, cls);
+  return pad256(8 * ((size_t)p->N + 1)) + pad256(4 * slots * R) + pad256(4 * slots * R * D);
 }
 
 DecClass class_args(const pt_decodeplan* p, int cls, int D, char*& ws) {
   const pt_decodeplan::Class& c = p->cls[cls];
   DecClass d = {};
   d.seg = c.seg;
-  d.nseg = c.nseg;
+  d.nseg = p->N;
   d.nitems = c.nitems;
   if (!c.nitems) return d;
-  const size_t R = cls == kDecSimt ? kSimtR : cls == kDecRows ? kRowsR : kTileR;
-  const size_t slots = (size_t)c.nitems + dec_workers(p, cls);
-  d.pref = reinterpret_cast<long long*>(ws), ws += pad256(8 * ((size_t)c.nseg + 1));
+  const size_t R = dec_r(cls), slots = (size_t)c.nitems + dec_workers(p, cls);
+  d.pref = reinterpret_cast<long long*>(ws), ws += pad256(8 * ((size_t)p->N + 1));
   d.lse = reinterpret_cast<float*>(ws), ws += pad256(4 * slots * R);
   d.opart = reinterpret_cast<float*>(ws), ws += pad256(4 * slots * R * D);
   return d;
 }
 
+// Whether a tensor-core call at this head_dim splits the nodes between the two kernels.
+bool use_tiles(const pt_decodeplan* p, int D) { return D <= kTileMaxD && p->cls[kDecTile].nitems > 0; }
+
 size_t ws_bytes(const pt_decodeplan* p, int D) {
   size_t n = std::max(class_bytes(p, kDecSimt, D), (size_t)256);
-  if (D <= 256) n = std::max(n, class_bytes(p, kDecRows, D) + class_bytes(p, kDecTile, D));
+  if (use_tiles(p, D))
+    n = std::max(n, class_bytes(p, kDecRowsFew, D) + class_bytes(p, kDecTile, D));
+  else if (D <= 256)
+    n = std::max(n, class_bytes(p, kDecRows, D));
   return n;
 }
 
@@ -384,12 +434,12 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
     return PT_ERR_INVALID_ARG;
   }
   const int N = n_nodes, S = n_samples, g = Hq / Hkv;
-  if ((long long)S * q_len * Hq > INT_MAX / 2) {
+  if ((long long)S * q_len * Hq >= 1 << 29) {
     set_error("%s: %d samples of %d tokens and %d heads are out of range", who, S, q_len, Hq);
     return PT_ERR_INVALID_ARG;
   }
-  if (N > kDecMaxSegs) {
-    set_error("%s: %d nodes, more than %d", who, N, kDecMaxSegs);
+  if (N > kDecMaxNodes) {
+    set_error("%s: %d nodes, more than %d", who, N, kDecMaxNodes);
     return PT_ERR_UNSUPPORTED;
   }
   if (path_ptr[0] != 0) {
@@ -432,42 +482,33 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
         samp[fill[n]++] = s;
       }
   }
-  // segments of each class, and each node's segments ({class << 28 | index}, at most two)
-  std::vector<int4> seg[kDecClasses];
-  long long items[kDecClasses] = {0, 0, 0};
-  std::vector<int2> of[2];
-  of[0].assign(std::max(N, 1), make_int2(-1, -1));
-  of[1].assign(std::max(N, 1), make_int2(-1, -1));
-  auto add = [&](int cls, int node, int kind, long long rows) {
-    const int R = cls == kDecSimt ? kSimtR : cls == kDecRows ? kRowsR : kTileR;
-    seg[cls].push_back(make_int4(node, kind, (int)rows, (int)std::min<long long>(items[cls], INT_MAX)));
-    items[cls] += (rows + R - 1) / R * Hkv;
-    return cls << 28 | (int)(seg[cls].size() - 1);
-  };
+  for (int s = 0; s < S; ++s)  // the member entry of the sample's own node
+    samp[np[leaf[s]] + member[path_ptr[s + 1] - 1]] |= INT_MIN;
+  // each class's share of the nodes
+  std::vector<DecSeg> seg[kDecClasses];
+  long long items[kDecClasses] = {0, 0, 0, 0};
   for (int i = 0; i < N; ++i) {
-    const long long rows = (long long)(np[i + 1] - np[i]) * q_len * g;
-    if (!rows) continue;
-    of[0][i].x = add(kDecSimt, i, kSegFull, rows);
-    of[1][i].x = add(kDecRows, i, kSegFull, rows);
+    const int n = np[i + 1] - np[i];
+    const long long rows = (long long)n * q_len * g;
+    int kind[kDecClasses] = {kSegFull, kSegFull, kSegFull, -1};
+    if (rows >= kTileMinRows) {
+      const bool mixed = is_leaf[i] && q_len > 1;
+      kind[kDecTile] = mixed ? kSegBody : kSegFull;
+      kind[kDecRowsFew] = mixed ? kSegTail : -1;
+    }
+    for (int c = 0; c < kDecClasses; ++c) {
+      const int rk = n && kind[c] >= 0 ? (int)rows | kind[c] << 29 : 0;
+      seg[c].push_back(DecSeg{rk, (int)std::min<long long>(items[c], INT_MAX), np[i], n == 1 ? samp[np[i]] & INT_MAX : -1});
+      if (rk) items[c] += (rows + dec_r(c) - 1) / dec_r(c) * Hkv;
+    }
   }
   for (int c = 0; c < kDecClasses; ++c)
     if (items[c] > INT_MAX / 512) {
       set_error("%s: %lld work items are out of range", who, items[c]);
       return PT_ERR_INVALID_ARG;
     }
-  std::vector<int32_t> pptr[2];
-  std::vector<int2> pent[2];
-  for (int v = 0; v < 2; ++v) {
-    pptr[v].assign(S + 1, 0);
-    for (int s = 0; s < S; ++s) {
-      for (int k = path_ptr[s]; k < path_ptr[s + 1]; ++k) {
-        const int2 o = of[v][path_nodes[k]];
-        if (o.x >= 0) pent[v].push_back(make_int2(o.x, member[k]));
-        if (o.y >= 0) pent[v].push_back(make_int2(o.y, member[k]));
-      }
-      pptr[v][s + 1] = (int32_t)pent[v].size();
-    }
-  }
+  std::vector<int2> ent(std::max(E, 1));
+  for (int k = 0; k < E; ++k) ent[k] = make_int2(path_nodes[k], member[k]);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     set_error("%s: no CUDA device", who);
@@ -481,14 +522,10 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
     if (bytes) std::memcpy(host.data() + at, src, bytes);
     return at;
   };
-  const size_t o_np = put(np.data(), 4 * np.size()), o_samp = put(samp.data(), 4 * (size_t)E),
-               o_leaf = put(leaf.data(), 4 * (size_t)S);
-  size_t o_seg[kDecClasses], o_pp[2], o_pe[2];
-  for (int c = 0; c < kDecClasses; ++c) o_seg[c] = put(seg[c].data(), sizeof(int4) * seg[c].size());
-  for (int v = 0; v < 2; ++v) {
-    o_pp[v] = put(pptr[v].data(), 4 * pptr[v].size());
-    o_pe[v] = put(pent[v].data(), sizeof(int2) * pent[v].size());
-  }
+  const size_t o_mem = put(samp.data(), 4 * (size_t)E), o_pp = put(path_ptr, 4 * (size_t)(S + 1)),
+               o_pe = put(ent.data(), sizeof(int2) * (size_t)E);
+  size_t o_seg[kDecClasses];
+  for (int c = 0; c < kDecClasses; ++c) o_seg[c] = put(seg[c].data(), sizeof(DecSeg) * seg[c].size());
   pt_decodeplan* p = new pt_decodeplan();
   p->device = dev;
   p->sms = num_sms(dev);
@@ -500,17 +537,12 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
     return (pt_status)rc;
   }
   char* base = static_cast<char*>(p->mem);
-  p->node_ptr = reinterpret_cast<int32_t*>(base + o_np);
-  p->node_samp = reinterpret_cast<int32_t*>(base + o_samp);
-  p->leaf = reinterpret_cast<int32_t*>(base + o_leaf);
+  p->member = reinterpret_cast<int32_t*>(base + o_mem);
+  p->path_ptr = reinterpret_cast<int32_t*>(base + o_pp);
+  p->path_ent = reinterpret_cast<int2*>(base + o_pe);
   for (int c = 0; c < kDecClasses; ++c) {
-    p->cls[c].seg = reinterpret_cast<int4*>(base + o_seg[c]);
-    p->cls[c].nseg = (int32_t)seg[c].size();
+    p->cls[c].seg = reinterpret_cast<DecSeg*>(base + o_seg[c]);
     p->cls[c].nitems = (int32_t)items[c];
-  }
-  for (int v = 0; v < 2; ++v) {
-    p->path_ptr[v] = reinterpret_cast<int32_t*>(base + o_pp[v]);
-    p->path_ent[v] = reinterpret_cast<int2*>(base + o_pe[v]);
   }
   rc = upload(p->mem, host.data(), host.size(), dev, stream);
   if (rc) {
@@ -586,7 +618,7 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   }
   if (!(scale > 0.0f)) scale = 1.0f / sqrtf((float)D);
   DecArgs a = {};
-  a.node_ptr = plan->node_ptr, a.node_samp = plan->node_samp, a.leaf = plan->leaf;
+  a.member = plan->member;
   a.lens = lens, a.tables = tables, a.q_count = q_count;
   a.Q = Q, a.Kc = Kc, a.Vc = Vc, a.q_stride = q_stride;
   a.q_len = plan->q_len, a.Hq = plan->Hq, a.Hkv = plan->Hkv, a.g = plan->Hq / plan->Hkv, a.D = D;
@@ -600,15 +632,14 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   const bool tc = dtype == PT_BF16 && decode_tc_supported(D, page_size);
   cudaError_t e = cudaSuccess;
   if (tc) {
-    m.first = kDecRows;
-    m.c0 = class_args(plan, kDecRows, D, ws);
-    m.c1 = class_args(plan, kDecTile, D, ws);
-    m.R0 = kRowsR, m.BT0 = kRowsBT, m.R1 = kTileR, m.BT1 = kTileBT;
-    ProfScope ps(stream, "decode_tc");
+    const bool tiles = use_tiles(plan, D);
+    m.c0 = class_args(plan, tiles ? kDecRowsFew : kDecRows, D, ws);
+    if (tiles) m.c1 = class_args(plan, kDecTile, D, ws);
+    m.R0 = kRowsR, m.BT0 = kRowsBT;
+    a.q_vec = (reinterpret_cast<uintptr_t>(Q) & 15u) == 0 && q_stride % 8 == 0;
     const int rc = decode_tc(plan, a, m.c0, m.c1, stream);
     if (rc) return (pt_status)rc;
   } else {
-    m.first = kDecSimt;
     m.c0 = class_args(plan, kDecSimt, D, ws);
     m.R0 = kSimtR, m.BT0 = kSimtBT;
     a.workers = dec_workers(plan, kDecSimt);
@@ -621,8 +652,8 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
     if (int rc = launch_status(who, e)) return (pt_status)rc;
   }
   m.d = a;
-  m.path_ptr = plan->path_ptr[tc ? 1 : 0];
-  m.path_ent = plan->path_ent[tc ? 1 : 0];
+  m.path_ptr = plan->path_ptr;
+  m.path_ent = plan->path_ent;
   {
     ProfScope ps(stream, "decode_merge");
     e = dtype == PT_BF16 ? launch_merge<__nv_bfloat16>(m, stream) : launch_merge<float>(m, stream);

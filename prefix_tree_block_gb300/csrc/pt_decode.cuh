@@ -19,22 +19,36 @@
 
 #include <cuda_bf16.h>
 
+#include <climits>
+
 #include "pt_device.cuh"
 
 namespace pt {
 
-constexpr int kDecMaxSegs = 1 << 16;  // 8 bytes of shared memory per 32 segments
+constexpr int kDecMaxNodes = 1 << 16;  // 8 bytes of shared memory per 32 nodes
 
-// Which of a node's tokens a segment covers.
+// Which of a node's tokens a class's segment covers.  A class has at most one
+// segment per node, so a segment's number is its node's and its length is read
+// beside its entry, not after it.
 enum : int {
   kSegFull = 0,  // all of them
   kSegBody = 1,  // a sample's own continuation up to its first query token, in whole groups of 16
   kSegTail = 2,  // the rest of it: the tokens that some of the queries must not see
 };
 
+// One node of a class.
+struct alignas(16) DecSeg {
+  int rows_kind;  // rows | kind << 29; no rows: the class passes the node over
+  int item0;      // items of the class before the node's
+  int member0;    // the node's samples in DecArgs::member
+  int solo;       // the node's only sample, else -1
+  __host__ __device__ int rows() const { return rows_kind & ((1 << 29) - 1); }
+  __host__ __device__ int kind() const { return (int)((unsigned)rows_kind >> 29); }
+};
+
 // One class of segments (one kernel's share of the tree).
 struct DecClass {
-  const int4* seg;  // {node, kind, rows, first item}
+  const DecSeg* seg;  // [n_nodes]
   int nseg, nitems;
   // the class's part of the workspace
   long long* pref;  // [nseg + 1] units before each segment; units per worker
@@ -43,24 +57,27 @@ struct DecClass {
 };
 
 struct DecArgs {
-  const int* node_ptr;   // [n_nodes + 1] CSR: samples through the node
-  const int* node_samp;
-  const int* leaf;       // [n_samples] last node of the sample's path
-  const int* lens;       // [n_nodes]
-  const int* tables;     // [n_nodes][max_pages]
-  const int* q_count;    // [n_samples] or NULL
+  const int* member;   // samples of each node, ascending; bit 31: the node is the sample's last
+  const int* lens;     // [n_nodes]
+  const int* tables;   // [n_nodes][max_pages]
+  const int* q_count;  // [n_samples] or NULL
   const void* Q;
   const void* Kc;
   const void* Vc;
-  long long q_stride;    // elements between query tokens
+  long long q_stride;  // elements between query tokens
   int q_len, Hq, Hkv, g, D;
   int ps, max_pages, n_pages;
   int workers, min_units;
+  int q_vec;           // Q's rows start on 16-byte boundaries
   float scale_log2;
 };
 
-__device__ __forceinline__ int dec_len(const DecArgs& a, int node, bool record) {
-  const int len = a.lens[node];
+__device__ __forceinline__ DecSeg load_seg(const DecSeg* p) {
+  const int4 v = *reinterpret_cast<const int4*>(p);
+  return DecSeg{v.x, v.y, v.z, v.w};
+}
+
+__device__ __forceinline__ int dec_clamp(const DecArgs& a, int len, bool record) {
   const long long cap = (long long)a.max_pages * a.ps;
   if (len < 0 || len > cap) {
     if (record) record_status(PT_STATUS_INVALID);
@@ -82,34 +99,37 @@ __device__ __forceinline__ int dec_count(const DecArgs& a, int s) {
 
 // Tiles of an item of the segment; 0 when its only sample has no queries.
 template <int BT>
-__device__ __forceinline__ int dec_tiles(const DecArgs& a, int4 sg, bool record) {
+__device__ __forceinline__ int dec_tiles(const DecArgs& a, const DecSeg& sg, int len) {
+  if (sg.rows_kind == 0) return 0;
+  if (a.q_count && sg.solo >= 0 && dec_count(a, sg.solo) == 0) return 0;
   int b, e;
-  dec_range(a, sg.y, dec_len(a, sg.x, record), b, e);
-  if (a.q_count) {
-    const int p = a.node_ptr[sg.x];
-    if (a.node_ptr[sg.x + 1] == p + 1 && dec_count(a, a.node_samp[p]) == 0) return 0;
-  }
+  dec_range(a, sg.kind(), len, b, e);
   return (e - b + BT - 1) / BT;
 }
 
-// Query row r of a segment: its sample, its query token's index and q head,
-// and the first node token that it must not see.
+// Query row r of a segment: its query token, q head, and the first token of
+// the node that it must not see.
 struct DecRow {
-  int s, j, head, lim;
+  int tok, head, lim;
 };
-__device__ __forceinline__ DecRow dec_row(const DecArgs& a, int node, int hk, int r, int len) {
+__device__ __forceinline__ DecRow dec_row(const DecArgs& a, int member0, int hk, int r, int len) {
   DecRow d;
-  const int per = a.q_len * a.g, m = r / per, rest = r - m * per;
-  d.j = rest / a.g;
-  d.head = hk * a.g + rest - d.j * a.g;
-  d.s = a.node_samp[a.node_ptr[node] + m];
-  const int cnt = dec_count(a, d.s);
-  d.lim = d.j >= cnt ? 0 : a.leaf[d.s] == node ? len - cnt + d.j + 1 : len;
+  int m = r, j = 0, h = 0;
+  if (a.g > 1) m = r / a.g, h = r - m * a.g;
+  if (a.q_len > 1) {
+    const int x = m;
+    m = x / a.q_len, j = x - m * a.q_len;
+  }
+  const int mb = a.member[member0 + m], s = mb & INT_MAX;
+  d.head = hk * a.g + h;
+  d.tok = s * a.q_len + j;
+  const int cnt = dec_count(a, s);
+  d.lim = j >= cnt ? 0 : mb < 0 ? len - cnt + j + 1 : len;
   return d;
 }
 
-// Page that holds token t of the node (an entry out of range is recorded and
-// page 0 read in its place).
+// Page that holds the node's tokens from pi * page_size (an entry out of range
+// is recorded and page 0 read in its place).
 __device__ __forceinline__ int dec_page(const DecArgs& a, int node, int pi) {
   const int p = a.tables[(size_t)node * a.max_pages + pi];
   if ((unsigned)p >= (unsigned)a.n_pages) {
@@ -128,6 +148,20 @@ __device__ __forceinline__ long long warp_incl_scan64(long long v, int lane) {
   return v;
 }
 
+// Units of segment i, and what it takes to know them.
+template <int R, int BT>
+__device__ __forceinline__ long long dec_units(const DecArgs& a, const DecClass& c, int i, bool record, DecSeg& sg,
+                                               int& len, int& tiles) {
+  sg = DecSeg{0, 0, 0, -1};
+  len = tiles = 0;
+  if (i >= c.nseg) return 0;
+  const int raw = a.lens[i];
+  sg = load_seg(c.seg + i);
+  len = dec_clamp(a, raw, record);
+  tiles = dec_tiles<BT>(a, sg, len);
+  return (long long)((sg.rows() + R - 1) / R * a.Hkv) * tiles;
+}
+
 // Exclusive sums of the class's units over chunks of 32 segments, in shared
 // memory (chunk[nc] = all of them); every thread of the block calls it.  Block
 // 0 also leaves each segment's sum and the units per worker for the merge.
@@ -135,15 +169,12 @@ template <int R, int BT>
 __device__ __forceinline__ long long dec_scan(const DecArgs& a, const DecClass& c, long long* chunk) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int nc = (c.nseg + 31) >> 5;
+  DecSeg sg;
+  int len, tiles;
   for (int k = warp; k < nc; k += nw) {
-    const int i = k * 32 + lane;
-    long long u = 0;
-    if (i < c.nseg) {
-      const int4 sg = c.seg[i];
-      u = (long long)((sg.z + R - 1) / R) * a.Hkv * dec_tiles<BT>(a, sg, blockIdx.x == 0);
-    }
-    u = warp_incl_scan64(u, lane);
-    if (lane == 31) chunk[k] = u;
+    const long long u = dec_units<R, BT>(a, c, k * 32 + lane, blockIdx.x == 0, sg, len, tiles);
+    const long long s = warp_incl_scan64(u, lane);
+    if (lane == 31) chunk[k] = s;
   }
   __syncthreads();
   if (warp == 0) {
@@ -158,15 +189,13 @@ __device__ __forceinline__ long long dec_scan(const DecArgs& a, const DecClass& 
   }
   __syncthreads();
   const long long total = chunk[nc];
-  const long long per = max((total + a.workers - 1) / a.workers, (long long)a.min_units);
-  if (blockIdx.x == 0) {
+  // (32-bit division where it will do)
+  long long per = total < INT_MAX ? ((int)total + a.workers - 1) / a.workers : (total + a.workers - 1) / a.workers;
+  per = max(per, (long long)a.min_units);
+  if (blockIdx.x == gridDim.x - 1) {  // (the last block: the line may end before its share)
     for (int k = warp; k < nc; k += nw) {
       const int i = k * 32 + lane;
-      long long u = 0;
-      if (i < c.nseg) {
-        const int4 sg = c.seg[i];
-        u = (long long)((sg.z + R - 1) / R) * a.Hkv * dec_tiles<BT>(a, sg, false);
-      }
+      const long long u = dec_units<R, BT>(a, c, i, false, sg, len, tiles);
       const long long x = warp_incl_scan64(u, lane) - u;
       if (i < c.nseg) c.pref[i] = chunk[k] + x;
     }
@@ -175,10 +204,10 @@ __device__ __forceinline__ long long dec_scan(const DecArgs& a, const DecClass& 
   return per;
 }
 
-// A piece: units [t0, t1) of item `item` of segment `seg`.
+// A piece: units [t0, t1) of one item of segment `node`.
 struct DecPiece {
-  int node, kind, rows, seg_item;  // the segment; the item's index in it
-  int rt, hk;                      // row tile and kv head
+  int node, len, kind, rows, member0;
+  int rt, hk;  // row tile and kv head
   int t0, t1;
   long long slot;
 };
@@ -192,8 +221,8 @@ struct DecWalk {
   long long pos, end, w;
   int k, nc;
   // the chunk's segments, one per lane
-  int4 sg;
-  int tiles;
+  DecSeg sg;
+  int len, tiles;
   long long excl;
 
   __device__ __forceinline__ DecWalk(const DecArgs& a_, const DecClass& c_, const long long* ch, long long worker,
@@ -211,10 +240,8 @@ struct DecWalk {
     }
   }
   __device__ __forceinline__ void load() {
-    const int lane = threadIdx.x & 31, i = k * 32 + lane;
-    sg = i < c.nseg ? c.seg[i] : make_int4(0, 0, 0, 0);
-    tiles = i < c.nseg ? dec_tiles<BT>(a, sg, false) : 0;
-    const long long u = (long long)((sg.z + R - 1) / R) * a.Hkv * tiles;
+    const int lane = threadIdx.x & 31;
+    const long long u = dec_units<R, BT>(a, c, k * 32 + lane, false, sg, len, tiles);
     excl = chunk[k] + warp_incl_scan64(u, lane) - u;
   }
   __device__ __forceinline__ bool next(DecPiece& p) {
@@ -229,28 +256,41 @@ struct DecWalk {
       const long long x = __shfl_sync(0xffffffffu, excl, l + o);
       if (x <= pos) l += o;
     }
-    p.node = __shfl_sync(0xffffffffu, sg.x, l);
-    p.kind = __shfl_sync(0xffffffffu, sg.y, l);
-    p.rows = __shfl_sync(0xffffffffu, sg.z, l);
-    const int item0 = __shfl_sync(0xffffffffu, sg.w, l);
+    const int rk = __shfl_sync(0xffffffffu, sg.rows_kind, l);
+    p.node = k * 32 + l;
+    p.len = __shfl_sync(0xffffffffu, len, l);
+    p.rows = rk & ((1 << 29) - 1);
+    p.kind = (int)((unsigned)rk >> 29);
+    p.member0 = __shfl_sync(0xffffffffu, sg.member0, l);
+    const int item0 = __shfl_sync(0xffffffffu, sg.item0, l);
     const int nt = __shfl_sync(0xffffffffu, tiles, l);
     const long long rel = pos - __shfl_sync(0xffffffffu, excl, l);
-    p.seg_item = (int)(rel / nt);
-    p.t0 = (int)(rel - (long long)p.seg_item * nt);
+    const int it = rel < INT_MAX ? (int)rel / nt : (int)(rel / nt);
+    p.t0 = (int)(rel - (long long)it * nt);
     p.t1 = (int)min((long long)nt, p.t0 + (end - pos));
-    p.rt = p.seg_item / a.Hkv;
-    p.hk = p.seg_item - p.rt * a.Hkv;
-    p.slot = w + item0 + p.seg_item;
+    p.rt = it / a.Hkv;
+    p.hk = it - p.rt * a.Hkv;
+    p.slot = w + item0 + it;
     pos += p.t1 - p.t0;
     return true;
   }
 };
 
-// The plan's classes.
-enum : int { kDecSimt = 0, kDecRows = 1, kDecTile = 2, kDecClasses = 3 };
-constexpr int kSimtR = 4, kSimtBT = 16;      // CUDA cores: rows and tokens of a tile, a warp per worker
-constexpr int kRowsR = 16, kRowsBT = 16;     // mma, a warp per worker
-constexpr int kTileR = 128, kTileBT = 128;   // tcgen05, a CTA per worker
+// The plan's classes: a call uses kDecSimt, or kDecRows, or kDecRowsFew with
+// kDecTile.
+enum : int {
+  kDecSimt = 0,     // CUDA cores: every node
+  kDecRows = 1,     // mma: every node
+  kDecRowsFew = 2,  // mma: nodes that few rows read, and the tails of the others
+  kDecTile = 3,     // tcgen05: the rest
+  kDecClasses = 4
+};
+constexpr int kSimtR = 4, kSimtBT = 16;      // rows and tokens of a tile; a warp per worker
+constexpr int kRowsR = 16, kRowsBT = 16;     // a warp per worker
+constexpr int kTileR = 256, kTileBT = 128;   // a CTA per worker; an item of up to 128 rows has two partial results
+constexpr int kTileMinRows = 65;             // rows of the nodes that go to the tile kernel
+constexpr int kTileMaxD = 0;
+inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
 
 }  // namespace pt
 
@@ -260,25 +300,22 @@ struct pt_decodeplan {
   cudaStream_t stream;  // the build stream; memory goes back to the pool in its order
   void* mem;            // one pool allocation for every array below
   int32_t N, S, Hq, Hkv, q_len;
-  int32_t* node_ptr;
-  int32_t* node_samp;
-  int32_t* leaf;
+  int32_t* member;
   struct Class {
-    int4* seg;
-    int32_t nseg, nitems;
+    pt::DecSeg* seg;
+    int32_t nitems;
   } cls[pt::kDecClasses];
-  // a sample's segments, in path order: {class << 28 | segment, member}
-  int32_t* path_ptr[2];  // [0] all segments of kDecSimt, [1] of the tensor-core classes
-  int2* path_ent[2];
+  int32_t* path_ptr;  // [S + 1]
+  int2* path_ent;     // {node, the sample's place among the node's}
 };
 
 namespace pt {
 // Tensor-core kernels (pt_decode_tc.cu).  Returns a PT_* status code.
 bool decode_tc_supported(int D, int ps);
-int decode_tc(const pt_decodeplan* p, DecArgs a, DecClass rows, DecClass tile, cudaStream_t s);
+int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile, cudaStream_t s);
 int take_status_decode_tc(cudaStream_t s);
 constexpr int kRowsWarps = 8;
 inline int dec_workers(const pt_decodeplan* p, int cls) {
-  return cls == kDecSimt ? p->sms * 16 : cls == kDecRows ? p->sms * kRowsWarps : p->sms;
+  return cls == kDecSimt ? p->sms * 16 : cls == kDecTile ? p->sms : p->sms * kRowsWarps;
 }
 }  // namespace pt

@@ -98,14 +98,14 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
     if (lp.t0 >= lp.t1) {
       if (!ahead.next(lp)) return;
       int e;
-      dec_range(a, lp.kind, dec_len(a, lp.node, false), l_base, e);
+      dec_range(a, lp.kind, lp.len, l_base, e);
       l_page0 = INT_MIN;
     }
     const int kv0 = l_base + lp.t0 * kRowsBT, pi = kv0 / a.ps;
     if (l_page0 == INT_MIN || pi >= l_page0 + 32) {
       l_page0 = pi;
       int b, e;
-      dec_range(a, lp.kind, dec_len(a, lp.node, false), b, e);
+      dec_range(a, lp.kind, lp.len, b, e);
       const int last = (min(e, b + lp.t1 * kRowsBT) - 1) / a.ps;  // last page of the piece
       my_page = pi + lane <= last ? dec_page(a, lp.node, pi + lane) : 0;
     }
@@ -137,9 +137,8 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
   const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_cb = lane >> 4;
   bool ok = true;
   while (ok && walk.next(p)) {
-    const int len = dec_len(a, p.node, false);
     int b, e;
-    dec_range(a, p.kind, len, b, e);
+    dec_range(a, p.kind, p.len, b, e);
     uint32_t q[NP * 4][4];
     int lim[2];
 #pragma unroll
@@ -148,9 +147,9 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
       const __nv_bfloat16* src = nullptr;
       lim[i] = 0;
       if (row < p.rows) {
-        const DecRow d = dec_row(a, p.node, p.hk, row, len);
+        const DecRow d = dec_row(a, p.member0, p.hk, row, p.len);
         lim[i] = d.lim;
-        src = static_cast<const __nv_bfloat16*>(a.Q) + (long long)(d.s * a.q_len + d.j) * a.q_stride + (long long)d.head * a.D;
+        src = static_cast<const __nv_bfloat16*>(a.Q) + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
       }
 #pragma unroll
       for (int k = 0; k < NP * 4; ++k) {
@@ -351,7 +350,7 @@ cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, DecArgs a,
 
 bool decode_tc_supported(int D, int ps) { return D % 8 == 0 && D <= 256 && ps % 16 == 0; }
 
-int decode_tc(const pt_decodeplan* p, DecArgs a, DecClass rows, DecClass tile, cudaStream_t s) {
+int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile, cudaStream_t s) {
   CUtensorMap mK, mV;
   const long long heads = (long long)a.n_pages * a.Hkv;
   if (heads > INT_MAX) {
