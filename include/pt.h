@@ -667,7 +667,7 @@ pt_status pt_debug_exp2(const float* x, float* y, int64_t n, int32_t method, cud
  * "blockmap_lists" (lists and masks), and the fold calls' "fold_plan",
  * "fold", "unfold", "unfold_grad", "fold_positions", "fold_mismatches",
  * and the cache and decoding calls' "cache_tables", "cache_write",
- * "decode_simt", "decode_tc", "decode_merge".  pt_profile_reset drops every record
+ * "decode_simt", "decode_rows", "decode_tile", "decode_merge".  pt_profile_reset drops every record
  * (its events go back to the pool once they have completed). */
 void pt_profile_enable(int on);
 pt_status pt_profile_read(const char* kernel, int64_t* launches, double* total_ms);

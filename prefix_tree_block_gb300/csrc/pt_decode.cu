@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       if (n <= 0) break;
       // lane i's row of the cache: token kv0 + i
       long long off = 0;
-      if (lane < n) {
-        const int pi = (kv0 + lane) / a.ps;
-        off = (((long long)dec_page(a, p.node, pi) * a.Hkv + p.hk) * a.ps + (kv0 + lane - pi * a.ps)) * a.D;
+      if (lane < kSimtBT) {  // (past the last token: the last again, so that every load below may be issued)
+        const int kv = kv0 + min(lane, n - 1), pi = kv / a.ps;
+        off = (((long long)dec_page(a, p.node, pi) * a.Hkv + p.hk) * a.ps + (kv - pi * a.ps)) * a.D;
       }
       float s[4];
 #pragma unroll
@@ -105,23 +105,18 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
         float d[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) d[i] = 0.f;
-        if (gq * 4 < n) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const long long o = __shfl_sync(0xffffffffu, off, gq * 4 + u);
-            const E* kp = static_cast<const E*>(a.Kc) + o;
-            const bool in = gq * 4 + u < n;
+        for (int u = 0; u < 4; ++u) {
+          const E* kp = static_cast<const E*>(a.Kc) + __shfl_sync(0xffffffffu, off, gq * 4 + u);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const int col = (v * 32 + lane) * VEC;
-              V kk;
-              if (in && col < a.D) {
-                kk = *reinterpret_cast<const V*>(kp + col);
+          for (int v = 0; v < NV; ++v) {
+            const int col = (v * 32 + lane) * VEC;
+            if (col < a.D) {
+              const V kk = *reinterpret_cast<const V*>(kp + col);
 #pragma unroll
-                for (int x = 0; x < VEC; ++x)
+              for (int x = 0; x < VEC; ++x)
 #pragma unroll
-                  for (int r = 0; r < R; ++r) d[r * 4 + u] = fmaf(q[r][v * VEC + x], to_f(kk.e[x]), d[r * 4 + u]);
-              }
+                for (int r = 0; r < R; ++r) d[r * 4 + u] = fmaf(q[r][v * VEC + x], to_f(kk.e[x]), d[r * 4 + u]);
             }
           }
         }
@@ -157,12 +152,10 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 #pragma unroll
         for (int i = 0; i < DL; ++i) acc[r][i] *= ar;
       }
-      const bool all_kept = kv0 + n <= lim_min;
+      const bool all_kept = n == kSimtBT && kv0 + n <= lim_min;
 #pragma unroll
       for (int i = 0; i < kSimtBT; ++i) {
-        if (i >= n) break;
-        const long long o = __shfl_sync(0xffffffffu, off, i);
-        const E* vp = static_cast<const E*>(a.Vc) + o;
+        const E* vp = static_cast<const E*>(a.Vc) + __shfl_sync(0xffffffffu, off, i);
         float pr[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) pr[r] = __shfl_sync(0xffffffffu, s[i >> 2], r * 8 + (i & 3) * 2);

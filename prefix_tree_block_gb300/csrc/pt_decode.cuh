@@ -289,7 +289,7 @@ constexpr int kSimtR = 4, kSimtBT = 16;      // rows and tokens of a tile; a war
 constexpr int kRowsR = 16, kRowsBT = 16;     // a warp per worker
 constexpr int kTileR = 256, kTileBT = 128;   // a CTA per worker; an item of up to 128 rows has two partial results
 constexpr int kTileMinRows = 65;             // rows of the nodes that go to the tile kernel
-constexpr int kTileMaxD = 0;
+constexpr int kTileMaxD = 128;               // and the head dims it takes
 inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
 
 }  // namespace pt
