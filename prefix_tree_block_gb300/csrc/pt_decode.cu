@@ -193,10 +193,14 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 
 // ---------------------------------------------------------------------------
 // Merge: O = sum_p 2^(lse_p - LSE) O_p over a row's pieces, in path order and
-// along each segment, so the sum's order is fixed.  A block takes one query
-// token's q head; its four warps take every fourth piece, lanes the columns.
-// Latency is all it is: the path's entries are looked up side by side, one per
-// lane, and four pieces are loaded at a time.
+// along each segment, so the sum's order is fixed.  A unit is one query token's
+// GH q heads of one kv head: their rows lie side by side in every piece (GH
+// divides the group and a row tile), so the pieces are looked up once for all
+// of them, the path's entries side by side, one per lane.  W warps share a
+// unit, each takes every W-th piece, lanes the columns; several pieces are
+// loaded at a time.  With many rows a unit gets one warp and up to four heads
+// (the lookup's instructions bound it otherwise: 8192 rows took 48 us with four
+// warps for each row); with few, four warps and one head (latency).
 // ---------------------------------------------------------------------------
 struct MergeArgs {
   DecArgs d;
@@ -204,26 +208,26 @@ struct MergeArgs {
   int R0, BT0;
   const int* path_ptr;
   const int2* path_ent;
-  int n_samples;
+  int n_samples, units;
   void* O;
   float* LSE;
 };
 
-template <int CPL>  // columns per lane
+template <int VEC, int NV, int GH>
 struct MergeAcc {
-  float mx, sum, acc[CPL];
-  int turn;  // pieces so far, mod 4
+  float mx[GH], sum[GH], acc[GH][NV * VEC];
+  int turn;  // pieces so far, modulo the warps
 };
 
 // The pieces of up to 32 path entries (lane i: node, member index) in one class.
-template <int CPL, bool TILE>
+template <int VEC, int NV, int GH, int W, bool TILE>
 __device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& c, int node, int mem, bool have, int j,
-                                            int head, int warp, int lane, MergeAcc<CPL>& s) {
+                                            int hk, int h0, int warp, int lane, MergeAcc<VEC, NV, GH>& s) {
+  using V = VecOf<float, VEC>;
   const DecArgs& a = m.d;
   const int R = TILE ? kTileR : m.R0, BT = TILE ? kTileBT : m.BT0;
-  const int hk = head / a.g;
-  int count = 0, two = 0, rin = 0;
-  long long slot0 = 0;
+  int count = 0, two = 0;
+  int row0 = 0;  // the row in the first piece, over all slots
   if (have) {
     const DecSeg sg = load_seg(c.seg + node);
     const int raw = a.lens[node];
@@ -233,8 +237,7 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& 
       dec_range(a, sg.kind(), dec_clamp(a, raw, false), b, e);
       const int tiles = (e - b + BT - 1) / BT;
       if (tiles > 0) {
-        const int row = (mem * a.q_len + j) * a.g + head - hk * a.g, rt = row / R, it = rt * a.Hkv + hk;
-        rin = row - rt * R;
+        const int row = (mem * a.q_len + j) * a.g + h0, rt = row / R, it = rt * a.Hkv + hk;
         two = TILE && sg.rows() - rt * R <= kTileR / 2;
         const long long u0 = pref + (long long)it * tiles, u1 = u0 + tiles - 1;
         long long w0, w1;
@@ -242,7 +245,7 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& 
           w0 = (int)u0 / (int)per, w1 = (int)u1 / (int)per;
         else
           w0 = u0 / per, w1 = u1 / per;
-        slot0 = w0 + sg.item0 + it;
+        row0 = (int)(w0 + sg.item0 + it) * R + row - rt * R;
         count = (int)(w1 - w0 + 1) << two;
       }
     }
@@ -254,87 +257,152 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& 
     if (lane >= o) incl += u;
   }
   const int excl = incl - count, total = __shfl_sync(0xffffffffu, incl, 31);
-  for (int x0 = (warp - s.turn) & 3; x0 < total; x0 += 16) {
-    float ls[4], o[4][CPL];
+  constexpr int U = GH * NV * VEC > 8 ? 2 : 4;  // pieces in flight
+  for (int x0 = W == 1 ? 0 : (warp - s.turn) & (W - 1); x0 < total; x0 += W * U) {
+    float ls[U][GH];
+    V o[U][GH][NV];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int x = min(x0 + 4 * u, total - 1);
+    for (int u = 0; u < U; ++u) {
+      const int x = min(x0 + W * u, total - 1);
       int l = 0;
 #pragma unroll
       for (int q = 16; q; q >>= 1)
         if (__shfl_sync(0xffffffffu, excl, l + q) <= x) l += q;
-      const int y = x - __shfl_sync(0xffffffffu, excl, l), tw = __shfl_sync(0xffffffffu, two, l);
-      const long long at = (__shfl_sync(0xffffffffu, slot0, l) + (y >> tw)) * R + __shfl_sync(0xffffffffu, rin, l) +
-                           (y & tw) * (kTileR / 2);
-      ls[u] = -INFINITY;
-      if (x0 + 4 * u < total) {
-        ls[u] = c.lse[at];
+      const int y = x - __shfl_sync(0xffffffffu, excl, l), tw = TILE ? __shfl_sync(0xffffffffu, two, l) : 0;
+      const int at = __shfl_sync(0xffffffffu, row0, l) + (y >> tw) * R + (TILE ? (y & tw) * (kTileR / 2) : 0);
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) o[u][i] = lane + i * 32 < a.D ? c.opart[at * a.D + lane + i * 32] : 0.f;
+      for (int h = 0; h < GH; ++h) {
+        ls[u][h] = -INFINITY;
+        if (x0 + W * u < total) {
+          ls[u][h] = c.lse[at + h];
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int col = (i * 32 + lane) * VEC;
+            if (col < a.D)
+              o[u][h][i] = *reinterpret_cast<const V*>(
+                  c.opart + (TILE ? tile_at(a.D, at / kTileR, at % kTileR + h, col) : (long long)(at + h) * a.D + col));
+            else
+              o[u][h][i] = V{};
+          }
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (ls[u] == -INFINITY) continue;
-      const float mn = fmaxf(s.mx, ls[u]), al = ex2(s.mx - mn), f = ex2(ls[u] - mn);
-      s.mx = mn;
-      s.sum = fmaf(s.sum, al, f);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) s.acc[i] = fmaf(s.acc[i], al, f * o[u][i]);
-    }
+      for (int h = 0; h < GH; ++h) {
+        if (ls[u][h] == -INFINITY) continue;
+        const float mn = fmaxf(s.mx[h], ls[u][h]), al = ex2(s.mx[h] - mn), f = ex2(ls[u][h] - mn);
+        s.mx[h] = mn;
+        s.sum[h] = fmaf(s.sum[h], al, f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int x = 0; x < VEC; ++x) s.acc[h][i * VEC + x] = fmaf(s.acc[h][i * VEC + x], al, f * o[u][h][i].e[x]);
+      }
   }
-  s.turn = (s.turn + total) & 3;
+  s.turn = (s.turn + total) & (W - 1);
 }
 
-template <class E, int CPL>
+template <class E, int VEC, int NV, int GH, int W>
 __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
   pdl_wait();
-  __shared__ float sm_m[4], sm_l[4];
-  __shared__ float sm_o[4][CPL * 32];
+  __shared__ float sm_m[W][GH], sm_l[W][GH];
+  __shared__ VecOf<float, VEC> sm_o[W == 1 ? 1 : W][W == 1 ? 1 : GH][W == 1 ? 1 : NV * 32];
   const DecArgs& a = m.d;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int head = blockIdx.x % a.Hq, tok = blockIdx.x / a.Hq, s = tok / a.q_len, j = tok - s * a.q_len;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
+  const int unit = W == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  if (unit >= m.units) return;
+  const int groups = a.Hq / GH, tok = unit / groups, head = (unit - tok * groups) * GH;
+  const int s = a.q_len > 1 ? tok / a.q_len : tok, j = tok - s * a.q_len, hk = head / a.g, h0 = head - hk * a.g;
   const int k0 = m.path_ptr[s], k1 = m.path_ptr[s + 1];
   if (a.q_count) {
     const int n = a.q_count[s];
-    if ((n < 0 || n > a.q_len) && threadIdx.x == 0) record_status(PT_STATUS_INVALID);
+    if ((n < 0 || n > a.q_len) && lane == 0) record_status(PT_STATUS_INVALID);
     if (j >= dec_count(a, s)) return;  // the row stays as it was
   }
-  MergeAcc<CPL> r;
-  r.mx = -INFINITY, r.sum = 0.f, r.turn = 0;
+  MergeAcc<VEC, NV, GH> r;
+  r.turn = 0;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) r.acc[i] = 0.f;
+  for (int h = 0; h < GH; ++h) {
+    r.mx[h] = -INFINITY, r.sum[h] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV * VEC; ++i) r.acc[h][i] = 0.f;
+  }
   for (int k = k0; k < k1; k += 32) {
     const bool have = k + lane < k1;
     const int2 en = have ? m.path_ent[k + lane] : make_int2(0, 0);
-    if (m.c0.nitems) merge_class<CPL, false>(m, m.c0, en.x, en.y, have, j, head, warp, lane, r);
-    if (m.c1.nitems) merge_class<CPL, true>(m, m.c1, en.x, en.y, have, j, head, warp, lane, r);
+    if (m.c0.nitems) merge_class<VEC, NV, GH, W, false>(m, m.c0, en.x, en.y, have, j, hk, h0, warp, lane, r);
+    if (m.c1.nitems) merge_class<VEC, NV, GH, W, true>(m, m.c1, en.x, en.y, have, j, hk, h0, warp, lane, r);
   }
-  if (lane == 0) sm_m[warp] = r.mx, sm_l[warp] = r.sum;
+  using V = VecOf<float, VEC>;
+  using VE = VecOf<E, VEC>;
+  auto put = [&](int h, int i, const V& v, float inv) {
+    const int col = (i * 32 + lane) * VEC;
+    if (col < a.D) {
+      VE w;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) sm_o[warp][lane + i * 32] = r.acc[i];
-  __syncthreads();
-  float top = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-  float f[4], all = 0.f;
+      for (int x = 0; x < VEC; ++x) {
+        if constexpr (sizeof(E) == 2)
+          w.e[x] = __float2bfloat16_rn(v.e[x] * inv);
+        else
+          w.e[x] = v.e[x] * inv;
+      }
+      *reinterpret_cast<VE*>(static_cast<E*>(m.O) + ((long long)tok * a.Hq + head + h) * a.D + col) = w;
+    }
+  };
+  auto put_lse = [&](int h, float top, float all) {
+    m.LSE[(long long)(head + h) * m.n_samples * a.q_len + tok] =
+        all == 0.f ? -INFINITY : (top + log2f(all)) * 0.69314718055994531f;
+  };
+  if constexpr (W == 1) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sm_m[w] == -INFINITY ? 0.f : ex2(sm_m[w] - top);
-    all = fmaf(f[w], sm_l[w], all);
+    for (int h = 0; h < GH; ++h) {
+      const float inv = r.sum[h] == 0.f ? 0.f : 1.f / r.sum[h];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        V v;
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) v.e[x] = r.acc[h][i * VEC + x];
+        put(h, i, v, inv);
+      }
+      if (lane == 0) put_lse(h, r.mx[h], r.sum[h]);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < GH; ++h) {
+      if (lane == 0) sm_m[warp][h] = r.mx[h], sm_l[warp][h] = r.sum[h];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        V v;
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) v.e[x] = r.acc[h][i * VEC + x];
+        sm_o[warp][h][i * 32 + lane] = v;
+      }
+    }
+    __syncthreads();
+    // warp w joins every W-th (head, column group)
+    for (int y = warp; y < GH * NV; y += W) {
+      const int h = y / NV, i = y - h * NV;
+      float top = -INFINITY, all = 0.f, f[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][h]);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        f[w] = sm_m[w][h] == -INFINITY ? 0.f : ex2(sm_m[w][h] - top);
+        all = fmaf(f[w], sm_l[w][h], all);
+      }
+      V v = {};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const V o = sm_o[w][h][i * 32 + lane];
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) v.e[x] = fmaf(f[w], o.e[x], v.e[x]);
+      }
+      put(h, i, v, all == 0.f ? 0.f : 1.f / all);
+      if (i == 0 && lane == 0) put_lse(h, top, all);
+    }
   }
-  const float inv = all == 0.f ? 0.f : 1.f / all;
-  E* O = static_cast<E*>(m.O) + ((long long)tok * a.Hq + head) * a.D;
-  for (int col = threadIdx.x; col < a.D; col += 128) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) v = fmaf(f[w], sm_o[w][col], v);
-    v *= inv;
-    if constexpr (sizeof(E) == 2)
-      O[col] = __float2bfloat16_rn(v);
-    else
-      O[col] = v;
-  }
-  if (threadIdx.x == 0)
-    m.LSE[(long long)head * m.n_samples * a.q_len + tok] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.69314718055994531f;
 }
 
 int launch_status(const char* who, cudaError_t e) {
@@ -393,14 +461,27 @@ cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t sm
   return D % 4 ? go(k_decode_simt<E, 16, 1>) : go(k_decode_simt<E, 16, 4>);
 }
 
+// From this many rows on, a merge unit is one warp and up to four heads.
+constexpr int kMergeManyRows = 4096;
+
+template <class E, int GH, int W>
+cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
+  m.units = m.n_samples * m.d.q_len * (m.d.Hq / GH);
+  const int grid = W == 1 ? (m.units + 3) / 4 : m.units, D = m.d.D;
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(128), 0, s, m); };
+  if (D <= 32) return go(k_decode_merge<E, 1, 1, GH, W>);
+  if (D <= 64) return D % 2 ? go(k_decode_merge<E, 1, 2, GH, W>) : go(k_decode_merge<E, 2, 1, GH, W>);
+  if (D <= 128) return D % 4 ? go(k_decode_merge<E, 1, 4, GH, W>) : go(k_decode_merge<E, 4, 1, GH, W>);
+  if (D <= 256) return D % 4 ? go(k_decode_merge<E, 1, 8, GH, W>) : go(k_decode_merge<E, 4, 2, GH, W>);
+  return D % 4 ? go(k_decode_merge<E, 1, 16, GH, W>) : go(k_decode_merge<E, 4, 4, GH, W>);
+}
+
 template <class E>
 cudaError_t launch_merge(const MergeArgs& m, cudaStream_t s) {
-  const int grid = m.n_samples * m.d.q_len * m.d.Hq, D = m.d.D;
-  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(128), 0, s, m); };
-  if (D <= 64) return go(k_decode_merge<E, 2>);
-  if (D <= 128) return go(k_decode_merge<E, 4>);
-  if (D <= 256) return go(k_decode_merge<E, 8>);
-  return go(k_decode_merge<E, 16>);
+  const long long rows = (long long)m.n_samples * m.d.q_len * m.d.Hq;
+  if (rows < kMergeManyRows) return launch_merge<E, 1, 4>(m, s);
+  if (m.d.g % 4 == 0 && m.d.D <= 256) return launch_merge<E, 4, 1>(m, s);
+  return launch_merge<E, 1, 1>(m, s);
 }
 
 }  // namespace

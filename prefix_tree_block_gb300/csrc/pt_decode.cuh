@@ -53,7 +53,7 @@ struct DecClass {
   // the class's part of the workspace
   long long* pref;  // [nseg + 1] units before each segment; units per worker
   float* lse;       // [slot][R]
-  float* opart;     // [slot][R][D]
+  float* opart;     // [slot][R][D]; the tile class: see tile_at
 };
 
 struct DecArgs {
@@ -290,6 +290,11 @@ constexpr int kRowsR = 16, kRowsBT = 16;     // a warp per worker
 constexpr int kTileR = 256, kTileBT = 128;   // a CTA per worker; an item of up to 128 rows has two partial results
 constexpr int kTileMinRows = 65;             // rows of the nodes that go to the tile kernel
 constexpr int kTileMaxD = 128;               // and the head dims it takes
+// Element (row, column) of a tile-class partial result: groups of 8 columns, in
+// each the rows one after another (D is a multiple of 8 there).
+__host__ __device__ inline long long tile_at(int D, long long slot, int row, int col) {
+  return ((slot * (D >> 3) + (col >> 3)) * kTileR + row) * 8 + (col & 7);
+}
 inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
 
 }  // namespace pt

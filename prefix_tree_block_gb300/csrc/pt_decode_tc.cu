@@ -27,6 +27,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// 16 bytes global -> shared, asynchronous; the rest of 16 past `bytes` (0 or 16) is zero
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 // d += a b, 16 x 8 x 16
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -347,7 +351,7 @@ struct TileCfg {
   static constexpr int OFF_CHUNK = OFF_MISC + 16;
   static constexpr size_t smem(int nseg) { return OFF_CHUNK + 8 * ((size_t)(nseg + 31) / 32 + 1) + 1024; }
   static constexpr int TM_S = 0, TM_O = 256;  // S(h) at h * 128, O(h) at 256 + h * D
-  static constexpr int THREADS = 384;         // two softmax warpgroups; producer, MMA and two idle warps
+  static constexpr int THREADS = 384;         // two softmax warpgroups; producer, MMA and two query warps
   static constexpr int REG_SOFTMAX = 216, REG_CTRL = 72, REG_LAUNCH = 168;
   static_assert(256 * REG_SOFTMAX + 128 * REG_CTRL == THREADS * REG_LAUNCH, "register split");
   static_assert(OFF_CHUNK + 8 * (kDecMaxNodes / 32 + 1) + 1024 <= 232448, "shared memory budget");
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   long long* chunk = reinterpret_cast<long long*>(smem + C::OFF_CHUNK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 256);
+    mbar_init(q_full, 64);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::KS; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
     for (int i = 0; i < C::VS; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1);
@@ -522,13 +526,59 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     __syncwarp();
   };
 
+  // Two warps gather the item's query rows (16-byte asynchronous copies, a row's
+  // lanes side by side) as soon as the last S of the piece before is done, so
+  // the loads run under that piece's last steps and its output.
+  const auto query_role = [&]() {
+    DecWalk<kTileR, kTileBT> walk(a, c, chunk, worker, per);
+    DecPiece p;
+    uint32_t it = 0;
+    bool ok = true;
+    constexpr int CPR = NP * 8, RPI = 32 / CPR;  // 16-byte pieces of a row; rows per warp instruction
+    while (walk.next(p)) {
+      const int left = p.rows - p.rt * kTileR, rows = left > kTileR / 2 ? kTileR : kTileR / 2;
+      if (it > 0) ok = mbar_wait(q_empty, (it - 1) & 1, abort_flag);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      for (int r0 = (warp - 10) * 32; r0 < rows; r0 += 64) {
+        long long src = -1;  // this lane's row
+        if (r0 + lane < left) {
+          const DecRow d = dec_row(a, p.member0, p.hk, p.rt * kTileR + r0 + lane, p.len);
+          src = (long long)d.tok * a.q_stride + (long long)d.head * a.D;
+        }
+#pragma unroll
+        for (int i = 0; i < CPR; ++i) {
+          const int x = r0 + i * RPI + lane / CPR, k = lane % CPR;
+          const long long at = __shfl_sync(0xffffffffu, src, i * RPI + lane / CPR);
+          const bool in = at >= 0 && k * 8 < a.D;
+          const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.Q) + (in ? at + k * 8 : 0);
+          uint8_t* dst = smem + C::OFF_Q + (x >> 7) * C::TILE + (k >> 3) * C::PANEL + (x & 127) * 128 + (((k & 7) ^ (x & 7)) << 4);
+          if (a.q_vec) {
+            cp_async16(dst, g, in ? 16 : 0);
+          } else {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(g);
+              v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(dst) = v;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+      ++it;
+    }
+    __syncwarp();
+  };
+
   const auto softmax_role = [&]() {
     const int h = warp >> 2, r = threadIdx.x & 127;  // warpgroup; row in its tile, TMEM lane
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t sb = tl + C::TM_S + h * 128, ob = tl + C::TM_O + h * D;
     DecWalk<kTileR, kTileBT> walk(a, c, chunk, worker, per);
     DecPiece p;
-    uint32_t n = 0, it = 0, sc = 0, oc = 0;
+    uint32_t n = 0, sc = 0, oc = 0;
     bool ok = true;
     while (ok && walk.next(p)) {
       int b, e;
@@ -538,36 +588,6 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
       const int tiles = p.t1 - p.t0, steps = tiles << pair;
       const int n_rows = min(pair ? left - h * 128 : left, 128);  // this warpgroup's rows
       const bool live = (warp & 3) * 32 < n_rows;                 // this warp has some
-      // Q: each warpgroup its own tile; of a small item, half of the columns each
-      if (it > 0) {
-        ok = mbar_wait(q_empty, (it - 1) & 1, abort_flag);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      }
-      {
-        const __nv_bfloat16* src = nullptr;
-        if (r < n_rows) {
-          const DecRow d = dec_row(a, p.member0, p.hk, p.rt * kTileR + (pair ? h * 128 : 0) + r, p.len);
-          src = static_cast<const __nv_bfloat16*>(a.Q) + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
-        }
-        uint8_t* dst = smem + C::OFF_Q + (pair ? h * C::TILE : 0) + r * 128;
-        const int c0 = pair ? 0 : h * (NP * 4), c1 = pair ? NP * 8 : c0 + NP * 4;
-#pragma unroll 4
-        for (int k = c0; k < c1; ++k) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (src && k * 8 < a.D) {
-            if (a.q_vec) {
-              v = *reinterpret_cast<const uint4*>(src + k * 8);
-            } else {
-              const uint32_t* w = reinterpret_cast<const uint32_t*>(src + k * 8);
-              v = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          *reinterpret_cast<uint4*>(dst + (k >> 3) * C::PANEL + (((k & 7) ^ (r & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full);
-      }
-      ++it;
       float m_use = -INFINITY, l = 0.f;
       bool any = false;
       for (int u = h; u < steps; u += 2, ++sc) {
@@ -650,8 +670,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
       if (!ok) break;
       n += tiles;
       // the warpgroup's partial result
-      const int row = pair ? h * 128 + r : r;
-      const long long at = p.slot * kTileR + (pair ? row : h * 128 + r);
+      const long long at = p.slot * kTileR + h * 128 + r;
       if (any) {
         ok = mbar_wait(o_full + h, oc & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -660,7 +679,9 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         if (live) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           if (r < n_rows) c.lse[at] = l == 0.f ? -INFINITY : m_use + log2f(l);
-          float* dst = c.opart + at * a.D;
+          // 8 columns of all rows side by side (tile_at): a warp's store covers 1 KB in one piece, where rows of
+          // their own would scatter it over 32 lines
+          float* dst = c.opart + tile_at(a.D, p.slot, h * 128 + r, 0);
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t orr[32];
@@ -670,7 +691,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 if (k * 32 + i < a.D)
-                  *reinterpret_cast<float4*>(dst + k * 32 + i) =
+                  *reinterpret_cast<float4*>(dst + (k * 4 + (i >> 3)) * (kTileR * 8) + (i & 4)) =
                       make_float4(__uint_as_float(orr[i]) * inv, __uint_as_float(orr[i + 1]) * inv,
                                   __uint_as_float(orr[i + 2]) * inv, __uint_as_float(orr[i + 3]) * inv);
             }
@@ -691,6 +712,8 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
       producer_role();
     else if (warp == 9)
       mma_role();
+    else
+      query_role();
   } else {
     regs_inc<C::REG_SOFTMAX>();
     softmax_role();

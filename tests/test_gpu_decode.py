@@ -32,6 +32,7 @@ TREES = {
     "long": ([700, 300], [[0, 1]]),
     "deep": ([130, 31, 0, 64, 2, 3, 250, 1], [[0, 1, 4], [0, 1, 5], [0, 2, 6], [0, 3, 7], [0, 3], [0]]),
     "crowd": ([290] + [3 + 2 * (i % 7) for i in range(70)], [[0, i] for i in range(1, 71)]),
+    "wide": ([1500, 260] + [1 + 9 * (i % 5) for i in range(150)], [[0, i] for i in range(2, 102)] + [[0, 1, i] for i in range(102, 152)]),
     "shared leaf": ([33, 20], [[0, 1], [0, 1], [1], [0]]),
     "unused rows, any order": ([8, 100, 9, 40, 3], [[4, 1], [4, 0]]),
 }
@@ -158,6 +159,29 @@ def test_fused_query_rows_and_own_buffers():
     pt.attn_decode(Q, Kc.cuda(), Vc.cuda(), torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), plan, O=O, LSE=L, workspace=ws)
     pt.sync_status()
     check(O.cpu(), L.cpu(), Q.cpu(), Kc, Vc, tables, lens, paths, 1)
+
+
+@pytest.mark.parametrize("extra", [0, 2, 8])
+def test_query_rows_between_16_byte_boundaries(extra):
+    """A node that many rows read, with query tokens of every alignment allowed."""
+    lens, paths = TREES["crowd"]
+    Hq, Hkv, D, ps = 4, 2, 64, 16
+    tables, n_pages = pages_of(lens, ps, np.random.default_rng(1))
+    Kc, Vc = cache_of(lens, tables, n_pages, Hkv, ps, D, BF, 1)
+    x = torch.randn(len(paths), Hq * D + extra, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
+    Q = x.as_strided((len(paths), Hq, D), (Hq * D + extra, D, 1), extra)
+    plan = pt.decode_plan(len(lens), *csr(paths), Hq, Hkv)
+    O, L = pt.attn_decode(Q, Kc.cuda(), Vc.cuda(), torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), plan)
+    pt.sync_status()
+    check(O.cpu(), L.cpu(), Q.cpu(), Kc, Vc, tables, lens, paths, 1)
+
+
+def test_many_rows():
+    """Enough query rows that the merge takes several heads to a warp."""
+    lens, paths = [300] + [20 + i % 9 for i in range(130)], [[0, i] for i in range(1, 131)]
+    for Hq, Hkv, D, dtype in ((32, 4, 64, BF), (40, 4, 128, BF), (36, 12, 64, BF), (32, 8, 32, F32)):
+        _run(lens, paths, Hq, Hkv, D, dtype, 16, seed=3)
+    _run(lens, paths, 8, 2, 128, BF, 16, q_len=5, seed=3)
 
 
 def test_far_pages():
