@@ -75,6 +75,9 @@ __device__ __forceinline__ int lane_of(int excl, int x) {
   return at;
 }
 
+// (a call each: 64-bit divisions are long, and their instructions come from memory)
+__device__ __noinline__ long long mod_call(long long a, long long b) { return a % b; }
+
 struct TabArgs {
   const int* held;
   const int* added;
@@ -99,12 +102,15 @@ constexpr int kRun = 256, kPad = 64;
 template <class F>
 __device__ __forceinline__ void for_line(const int* cum, int nc, int upto, int first, int warps, F f) {
   const int line = upto + kPad * nc;
+#pragma unroll 1
   for (int r = first; (long long)r * kRun < line; r += warps) {
     int pos = r * kRun;
     const int end = min(pos + kRun, line);
     int c = 0;
+#pragma unroll 1
     for (int span = 1 << (31 - __clz(nc)); span; span >>= 1)
       if (c + span < nc && cum[c + span] + kPad * (c + span) <= pos) c += span;
+#pragma unroll 1
     for (; pos < end && c < nc; ++c) {
       const int lo = cum[c], hi = min(cum[c + 1], upto), shift = lo + kPad * c;
       const int x0 = lo + pos - shift, x1 = min(lo + end - shift, hi);
@@ -130,10 +136,13 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
   int* c_take = sm + (nc + 1);
   int* c_back = sm + 2 * (nc + 1);
   const long long most = (long long)a.max_pages * a.ps;
-#pragma unroll 4
+  int h = 0, ad = 0;  // of this lane's row, loaded a chunk ahead
+  if (warp * 32 + lane < a.n) h = a.held[warp * 32 + lane], ad = a.added[warp * 32 + lane];
+#pragma unroll 1
   for (int c = warp; c < nc; c += kTabWarps) {
-    const int i = c * 32 + lane;
-    RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
+    const RowMove m = row_move(h, ad, a.ps, most);
+    const int i = (c + kTabWarps) * 32 + lane;
+    h = i < a.n ? a.held[i] : 0, ad = i < a.n ? a.added[i] : 0;
     if (m.bad && blockIdx.x == 0) record_status(PT_STATUS_INVALID);
     // tokens in two halves: 32 rows can hold more than 2^31 of them
     const long long g = ((long long)__reduce_add_sync(0xffffffffu, m.grow >> 16) << 16) +
@@ -145,6 +154,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
   if (warp < 3) {  // exclusive scan of one of the three sums (tokens stop at kTabMaxNew + 1, over any max_new)
     int* v = warp == 0 ? c_new : warp == 1 ? c_take : c_back;
     long long carry = 0;
+#pragma unroll 1
     for (int c0 = 0; c0 < nc; c0 += 32) {
       const long long x = c0 + lane < nc ? v[c0 + lane] : 0;
       long long s = x;
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
   const bool ring_bad = head < 0 || avail_l < 0 || avail_l > a.cap;
   if (ring_bad) avail_l = 0;
   const int avail = (int)avail_l;
-  const int h0 = ring_bad ? 0 : (int)(head % a.cap), t0 = ring_bad ? 0 : (int)(tail % a.cap);
+  const int h0 = ring_bad ? 0 : (int)mod_call(head, a.cap), t0 = ring_bad ? 0 : (int)mod_call(tail, a.cap);
   const int n_new = c_new[nc], n_take = c_take[nc], n_back = c_back[nc];
   // pages given back beyond the ring's room are dropped (the caller's page
   // count is then wrong, which is recorded)
@@ -177,6 +187,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
     a.row_ptr[a.n] = n_new;
   }
   // the rows' own outputs
+#pragma unroll 1
   for (int c = blockIdx.x + gridDim.x * warp; c < nc; c += gridDim.x * kTabWarps) {
     const int i = c * 32 + lane;
     const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
       const int i = c * 32 + lane;
       const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
       const int excl = c_take[c] + warp_incl_scan(m.take, lane) - m.take;
+#pragma unroll 1
       for (int x = x0; x < x1; x += 32 * U) {
         int id[U];
         size_t at[U];
@@ -216,6 +228,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
       const int i = c * 32 + lane;
       const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
       const int excl = c_back[c] + warp_incl_scan(m.back, lane) - m.back;
+#pragma unroll 1
       for (int x = x0; x < x1; x += 32 * U) {
         int id[U];
 #pragma unroll
@@ -241,6 +254,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
       const int st = a.start && i < a.n ? a.start[i] : 0;
       const int e_new = c_new[c] + warp_incl_scan(m.grow, lane) - m.grow;
       const int e_take = c_take[c] + warp_incl_scan(m.take, lane) - m.take;
+#pragma unroll 1
       for (int x = x0; x < x1; x += 32 * U) {
         int page[U], tok[U], pos[U], rest[U];
 #pragma unroll
@@ -271,6 +285,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
       }
     });
   // behind the last token
+#pragma unroll 1
   for (int y = n_real + blockIdx.x * blockDim.x + threadIdx.x; y < a.max_new; y += gridDim.x * blockDim.x) {
     a.slots[y] = -1;
     if (a.positions) a.positions[y] = 0;
@@ -278,6 +293,8 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
 }
 
 // ---------------------------------------------------------------------------
+__device__ __noinline__ long long div_call(long long a, long long b) { return a / b; }
+
 struct WriteArgs {
   const char* K;
   const char* V;
@@ -300,6 +317,7 @@ __global__ void __launch_bounds__(256) k_cache_write(const WriteArgs a) {
   const int per = 256 / a.tx, v0 = threadIdx.x % a.tx, tg = threadIdx.x / a.tx;
   if (tg >= per) return;
   constexpr int U = 4;
+#pragma unroll 1
   for (long long tb = (long long)blockIdx.x * per * U; tb < a.T; tb += (long long)gridDim.x * per * U) {
     long long off[U];  // first vector of the slot's row in head 0, or -1
 #pragma unroll
@@ -310,11 +328,12 @@ __global__ void __launch_bounds__(256) k_cache_write(const WriteArgs a) {
       if (s >= a.n_slots) {
         if (v0 == 0) record_status(PT_STATUS_INVALID);
       } else if (s >= 0) {
-        const long long page = a.shift >= 0 ? s >> a.shift : s / a.ps;
+        const long long page = a.shift >= 0 ? s >> a.shift : div_call(s, a.ps);
         const int row = (int)(s - page * a.ps);
         off[u] = page * ((long long)a.nv * a.ps) + (long long)row * a.hv;
       }
     }
+#pragma unroll 1
     for (int v = v0; v < a.nv; v += a.tx) {
       const int h = v / a.hv;
       const long long in_page = (long long)h * a.ps * a.hv + (v - h * a.hv);

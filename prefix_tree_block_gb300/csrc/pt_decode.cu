@@ -40,7 +40,7 @@ struct alignas(sizeof(E) * V) VecOf {
 };
 
 // ---------------------------------------------------------------------------
-// CUDA cores: a warp per worker, kSimtR = 4 query rows, 16 tokens a step.
+// CUDA cores: a warp per worker, kSimtR = 4 query rows, 8 tokens a step.
 //
 // Lanes hold the columns (DL each, VEC of them contiguous), so a token's key
 // is one coalesced load, and four keys against four rows leave 16 partial dot
@@ -54,20 +54,23 @@ struct alignas(sizeof(E) * V) VecOf {
 template <class E, int DL, int VEC>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {
   pdl_wait();
-  extern __shared__ long long chunk[];
-  const long long per = dec_scan<kSimtR, kSimtBT>(a, c, chunk);
+  extern __shared__ int chunk[];
+  dec_scan(a, c, kSimt, chunk, nullptr, false);
+  const int per = dec_share(chunk[(c.nseg + 31) >> 5], a.workers, a.min_units);
+  if (blockIdx.x == gridDim.x - 1) dec_publish(a, c, kSimt, chunk, per);
   const int lane = threadIdx.x & 31;
   constexpr int R = kSimtR, NV = DL / VEC;
   using V = VecOf<E, VEC>;
   const E* Qp = static_cast<const E*>(a.Q);
-  DecWalk<R, kSimtBT> walk(a, c, chunk, (long long)blockIdx.x * 8 + (threadIdx.x >> 5), per);
+  DecWalk walk(a, c, kSimt, chunk, (int)blockIdx.x * 8 + (threadIdx.x >> 5), per);
   DecPiece p;
   const int my_r = lane >> 3;  // the row whose scores this lane holds
+#pragma unroll 1
   while (walk.next(p)) {
     int b, e;
     dec_range(a, p.kind, p.len, b, e);
     float q[R][DL], acc[R][DL];
-    int lim_max = 0, lim_min = INT_MAX, my_lim = 0;
+    int lim_max = 0, my_lim = 0;
     int lim[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -80,7 +83,6 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
         src = Qp + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
       }
       lim_max = max(lim_max, lim[r]);
-      lim_min = min(lim_min, lim[r]);
       if (r == my_r) my_lim = lim[r];
 #pragma unroll
       for (int i = 0; i < DL; ++i) {
@@ -90,18 +92,17 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       }
     }
     float m = -INFINITY, l = 0.f;  // of row my_r, the same on its eight lanes
-    for (int t = p.t0; t < p.t1; ++t) {
-      const int kv0 = b + t * kSimtBT, n = min(min(kSimtBT, e - kv0), lim_max - kv0);
-      if (n <= 0) break;
-      // lane i's row of the cache: token kv0 + i
-      long long off = 0;
-      if (lane < kSimtBT) {  // (past the last token: the last again, so that every load below may be issued)
-        const int kv = kv0 + min(lane, n - 1), pi = kv / a.ps;
+#pragma unroll 1
+    for (int kv0 = b + p.t0 * kSimtBT, end = min(min(b + p.t1 * kSimtBT, e), lim_max); kv0 < end; kv0 += 8) {
+      // lane i's row of the cache: token kv0 + i (past the last token: the last again, so that every load may be issued)
+      long long off;
+      {
+        const int kv = min(kv0 + (lane & 7), end - 1), pi = kv / a.ps;
         off = (((long long)dec_page(a, p.node, pi) * a.Hkv + p.hk) * a.ps + (kv - pi * a.ps)) * a.D;
       }
-      float s[4];
+      float s[2];
 #pragma unroll
-      for (int gq = 0; gq < 4; ++gq) {
+      for (int gq = 0; gq < 2; ++gq) {
         float d[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) d[i] = 0.f;
@@ -132,17 +133,16 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
         }
         d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
         const int kv = kv0 + gq * 4 + ((lane >> 1) & 3);
-        s[gq] = kv < kv0 + n && kv < my_lim ? d[0] : -INFINITY;
+        s[gq] = kv < end && kv < my_lim ? d[0] : -INFINITY;
       }
-      float mt = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      float mt = fmaxf(s[0], s[1]);
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
       const float mn = fmaxf(m, mt), ref = mn == -INFINITY ? 0.f : mn;
       const float al = ex2(m - ref);
       m = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int gq = 0; gq < 4; ++gq) s[gq] = ex2(s[gq] - ref), sum += s[gq];
+      s[0] = ex2(s[0] - ref), s[1] = ex2(s[1] - ref);
+      float sum = s[0] + s[1];
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       l = fmaf(l, al, sum);
@@ -152,9 +152,8 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 #pragma unroll
         for (int i = 0; i < DL; ++i) acc[r][i] *= ar;
       }
-      const bool all_kept = n == kSimtBT && kv0 + n <= lim_min;
 #pragma unroll
-      for (int i = 0; i < kSimtBT; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const E* vp = static_cast<const E*>(a.Vc) + __shfl_sync(0xffffffffu, off, i);
         float pr[R];
 #pragma unroll
@@ -167,9 +166,10 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 #pragma unroll
             for (int x = 0; x < VEC; ++x)
 #pragma unroll
-              for (int r = 0; r < R; ++r)  // a value that the row must not see does not reach it, whatever it is
-                if (all_kept || kv0 + i < lim[r])
-                  acc[r][v * VEC + x] = fmaf(pr[r], to_f(vv.e[x]), acc[r][v * VEC + x]);
+              for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
+                const float y = fmaf(pr[r], to_f(vv.e[x]), acc[r][v * VEC + x]);
+                acc[r][v * VEC + x] = kv0 + i < lim[r] ? y : acc[r][v * VEC + x];
+              }
           }
         }
       }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       if (p.rt * R + r >= p.rows) break;
       const float lr = __shfl_sync(0xffffffffu, l, r * 8), mr = __shfl_sync(0xffffffffu, m, r * 8);
       const float inv = lr == 0.f ? 0.f : 1.f / lr;
-      const long long row = p.slot * R + r;
+      const long long row = (long long)p.slot * R + r;
       if (lane == 0) c.lse[row] = lr == 0.f ? -INFINITY : mr + log2f(lr);
 #pragma unroll
       for (int i = 0; i < DL; ++i) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 struct MergeArgs {
   DecArgs d;
   DecClass c0, c1;  // c1: the tile class, or none
-  int R0, BT0;
+  DecTiling g0;       // c0's
   const int* path_ptr;
   const int2* path_ent;
   int n_samples, units;
@@ -220,32 +220,31 @@ struct MergeAcc {
 };
 
 // The pieces of up to 32 path entries (lane i: node, member index) in one class.
-template <int VEC, int NV, int GH, int W, bool TILE>
-__device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& c, int node, int mem, bool have, int j,
-                                            int hk, int h0, int warp, int lane, MergeAcc<VEC, NV, GH>& s) {
+template <int VEC, int NV, int GH, int W>
+__device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int node, int mem, bool have, int j, int hk,
+                                            int h0, int warp, int lane, MergeAcc<VEC, NV, GH>& s) {
   using V = VecOf<float, VEC>;
   const DecArgs& a = m.d;
-  const int R = TILE ? kTileR : m.R0, BT = TILE ? kTileBT : m.BT0;
+  const DecSeg* seg = tile ? m.c1.seg : m.c0.seg;
+  const int* pref = tile ? m.c1.pref : m.c0.pref;
+  const float* lse = tile ? m.c1.lse : m.c0.lse;
+  const float* opart = tile ? m.c1.opart : m.c0.opart;
+  const int rl = tile ? kTile.r : m.g0.r, bl = tile ? kTile.t : m.g0.t;
   int count = 0, two = 0;
   int row0 = 0;  // the row in the first piece, over all slots
   if (have) {
-    const DecSeg sg = load_seg(c.seg + node);
+    const DecSeg sg = load_seg(seg + node);
     const int raw = a.lens[node];
-    const long long pref = c.pref[node], per = c.pref[c.nseg];
+    const int before = pref[node], per = pref[m.c0.nseg];
     if (sg.rows_kind) {
       int b, e;
-      dec_range(a, sg.kind(), dec_clamp(a, raw, false), b, e);
-      const int tiles = (e - b + BT - 1) / BT;
+      dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
+      const int tiles = (e - b + (1 << bl) - 1) >> bl;
       if (tiles > 0) {
-        const int row = (mem * a.q_len + j) * a.g + h0, rt = row / R, it = rt * a.Hkv + hk;
-        two = TILE && sg.rows() - rt * R <= kTileR / 2;
-        const long long u0 = pref + (long long)it * tiles, u1 = u0 + tiles - 1;
-        long long w0, w1;
-        if (u1 < INT_MAX && per < INT_MAX)
-          w0 = (int)u0 / (int)per, w1 = (int)u1 / (int)per;
-        else
-          w0 = u0 / per, w1 = u1 / per;
-        row0 = (int)(w0 + sg.item0 + it) * R + row - rt * R;
+        const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
+        two = tile && sg.rows() - (rt << rl) <= kTileR / 2;
+        const unsigned u0 = before + it * tiles, w0 = u0 / (unsigned)per, w1 = (u0 + tiles - 1) / (unsigned)per;
+        row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
         count = (int)(w1 - w0 + 1) << two;
       }
     }
@@ -257,48 +256,44 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, const DecClass& 
     if (lane >= o) incl += u;
   }
   const int excl = incl - count, total = __shfl_sync(0xffffffffu, incl, 31);
+  // a row's columns: groups of 8, far apart in the tile class and side by side in the others
+  const int row_step = tile ? 8 : a.D, col_step = tile ? kTileR * 8 : 8;
   constexpr int U = GH * NV * VEC > 8 ? 2 : 4;  // pieces in flight
+#pragma unroll 1
   for (int x0 = W == 1 ? 0 : (warp - s.turn) & (W - 1); x0 < total; x0 += W * U) {
     float ls[U][GH];
     V o[U][GH][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int x = min(x0 + W * u, total - 1);
-      int l = 0;
+      const int l = 31 - __clz(__ballot_sync(0xffffffffu, excl <= x));
+      const int y = x - __shfl_sync(0xffffffffu, excl, l), tw = __shfl_sync(0xffffffffu, two, l);
+      const int at = __shfl_sync(0xffffffffu, row0, l) + ((y >> tw) << rl) + (y & tw) * (kTileR / 2);
+      const bool in = x0 + W * u < total;
+      const float* src = opart + (long long)(at >> rl) * (a.D << rl) + (at & ((1 << rl) - 1)) * row_step;
 #pragma unroll
-      for (int q = 16; q; q >>= 1)
-        if (__shfl_sync(0xffffffffu, excl, l + q) <= x) l += q;
-      const int y = x - __shfl_sync(0xffffffffu, excl, l), tw = TILE ? __shfl_sync(0xffffffffu, two, l) : 0;
-      const int at = __shfl_sync(0xffffffffu, row0, l) + (y >> tw) * R + (TILE ? (y & tw) * (kTileR / 2) : 0);
+      for (int i = 0; i < NV; ++i) {
+        const int col = (i * 32 + lane) * VEC;
+        const float* from = src + (col >> 3) * col_step + (col & 7);
 #pragma unroll
-      for (int h = 0; h < GH; ++h) {
-        ls[u][h] = -INFINITY;
-        if (x0 + W * u < total) {
-          ls[u][h] = c.lse[at + h];
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int col = (i * 32 + lane) * VEC;
-            if (col < a.D)
-              o[u][h][i] = *reinterpret_cast<const V*>(
-                  c.opart + (TILE ? tile_at(a.D, at / kTileR, at % kTileR + h, col) : (long long)(at + h) * a.D + col));
-            else
-              o[u][h][i] = V{};
-          }
-        }
+        for (int h = 0; h < GH; ++h) o[u][h][i] = in && col < a.D ? *reinterpret_cast<const V*>(from + h * row_step) : V{};
       }
+#pragma unroll
+      for (int h = 0; h < GH; ++h) ls[u][h] = in ? lse[at + h] : -INFINITY;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < GH; ++h) {
-        if (ls[u][h] == -INFINITY) continue;
-        const float mn = fmaxf(s.mx[h], ls[u][h]), al = ex2(s.mx[h] - mn), f = ex2(ls[u][h] - mn);
+        // (a piece that kept nothing weighs nothing, whatever the slot held)
+        const float mn = fmaxf(s.mx[h], ls[u][h]), ref = mn == -INFINITY ? 0.f : mn;
+        const float al = ex2(s.mx[h] - ref), f = ex2(ls[u][h] - ref);
         s.mx[h] = mn;
         s.sum[h] = fmaf(s.sum[h], al, f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int x = 0; x < VEC; ++x) s.acc[h][i * VEC + x] = fmaf(s.acc[h][i * VEC + x], al, f * o[u][h][i].e[x]);
+          for (int x = 0; x < VEC; ++x) s.acc[h][i * VEC + x] = fmaf(s.acc[h][i * VEC + x], al, ls[u][h] == -INFINITY ? 0.f : f * o[u][h][i].e[x]);
       }
   }
   s.turn = (s.turn + total) & (W - 1);
@@ -329,11 +324,13 @@ __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
 #pragma unroll
     for (int i = 0; i < NV * VEC; ++i) r.acc[h][i] = 0.f;
   }
+#pragma unroll 1
   for (int k = k0; k < k1; k += 32) {
     const bool have = k + lane < k1;
     const int2 en = have ? m.path_ent[k + lane] : make_int2(0, 0);
-    if (m.c0.nitems) merge_class<VEC, NV, GH, W, false>(m, m.c0, en.x, en.y, have, j, hk, h0, warp, lane, r);
-    if (m.c1.nitems) merge_class<VEC, NV, GH, W, true>(m, m.c1, en.x, en.y, have, j, hk, h0, warp, lane, r);
+#pragma unroll 1
+    for (int cls = m.c0.nitems ? 0 : 1; cls < (m.c1.nitems ? 2 : 1); ++cls)
+      merge_class<VEC, NV, GH, W>(m, cls == 1, en.x, en.y, have, j, hk, h0, warp, lane, r);
   }
   using V = VecOf<float, VEC>;
   using VE = VecOf<E, VEC>;
@@ -382,6 +379,7 @@ __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
     }
     __syncthreads();
     // warp w joins every W-th (head, column group)
+#pragma unroll 1
     for (int y = warp; y < GH * NV; y += W) {
       const int h = y / NV, i = y - h * NV;
       float top = -INFINITY, all = 0.f, f[W];
@@ -421,7 +419,7 @@ size_t class_bytes(const pt_decodeplan* p, int cls, int D) {
   const pt_decodeplan::Class& c = p->cls[cls];
   if (!c.nitems) return 0;
   const size_t R = dec_r(cls), slots = (size_t)c.nitems + dec_workers(p, cls);
-  return pad256(8 * ((size_t)p->N + 1)) + pad256(4 * slots * R) + pad256(4 * slots * R * D);
+  return pad256(4 * ((size_t)p->N + 1)) + pad256(4 * slots * R) + pad256(4 * slots * R * D);
 }
 
 DecClass class_args(const pt_decodeplan* p, int cls, int D, char*& ws) {
@@ -432,7 +430,7 @@ DecClass class_args(const pt_decodeplan* p, int cls, int D, char*& ws) {
   d.nitems = c.nitems;
   if (!c.nitems) return d;
   const size_t R = dec_r(cls), slots = (size_t)c.nitems + dec_workers(p, cls);
-  d.pref = reinterpret_cast<long long*>(ws), ws += pad256(8 * ((size_t)p->N + 1));
+  d.pref = reinterpret_cast<int*>(ws), ws += pad256(4 * ((size_t)p->N + 1));
   d.lse = reinterpret_cast<float*>(ws), ws += pad256(4 * slots * R);
   d.opart = reinterpret_cast<float*>(ws), ws += pad256(4 * slots * R * D);
   return d;
@@ -461,7 +459,9 @@ cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t sm
   return D % 4 ? go(k_decode_simt<E, 16, 1>) : go(k_decode_simt<E, 16, 4>);
 }
 
-// From this many rows on, a merge unit is one warp and up to four heads.
+// From this many rows on, a merge unit is four heads on one warp (8192 rows: 14
+// us, 20 with four warps, 48 with four warps for each row); where the group has
+// no multiple of four, one head on one warp from four times as many.
 constexpr int kMergeManyRows = 4096;
 
 template <class E, int GH, int W>
@@ -479,9 +479,9 @@ cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
 template <class E>
 cudaError_t launch_merge(const MergeArgs& m, cudaStream_t s) {
   const long long rows = (long long)m.n_samples * m.d.q_len * m.d.Hq;
-  if (rows < kMergeManyRows) return launch_merge<E, 1, 4>(m, s);
-  if (m.d.g % 4 == 0 && m.d.D <= 256) return launch_merge<E, 4, 1>(m, s);
-  return launch_merge<E, 1, 1>(m, s);
+  const bool heads = m.d.g % 4 == 0 && m.d.D <= 256 && rows >= kMergeManyRows;
+  if (heads) return launch_merge<E, 4, 1>(m, s);
+  return rows < 4 * kMergeManyRows ? launch_merge<E, 1, 4>(m, s) : launch_merge<E, 1, 1>(m, s);
 }
 
 }  // namespace
@@ -696,29 +696,37 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   a.lens = lens, a.tables = tables, a.q_count = q_count;
   a.Q = Q, a.Kc = Kc, a.Vc = Vc, a.q_stride = q_stride;
   a.q_len = plan->q_len, a.Hq = plan->Hq, a.Hkv = plan->Hkv, a.g = plan->Hq / plan->Hkv, a.D = D;
-  a.ps = page_size, a.max_pages = max_pages, a.n_pages = n_pages;
+  a.ps = page_size, a.max_pages = max_pages, a.n_pages = n_pages, a.cap = max_pages * page_size;
   a.scale_log2 = scale * 1.4426950408889634f;
+  const bool tc = dtype == PT_BF16 && decode_tc_supported(D, page_size);
+  const bool tiles = tc && use_tiles(plan, D);
+  for (int c = 0; c < kDecClasses; ++c) {
+    const bool used = c == kDecSimt ? !tc : c == kDecRows ? tc && !tiles : tiles;
+    const int bt = c == kDecSimt ? kSimtBT : c == kDecTile ? kTileBT : kRowsBT;
+    if (used && (long long)plan->cls[c].nitems * ((a.cap + bt - 1) / bt) > INT_MAX) {
+      set_error("%s: %d work items over tables of %d tokens are out of range", who, plan->cls[c].nitems, a.cap);
+      return PT_ERR_UNSUPPORTED;
+    }
+  }
   char* ws = static_cast<char*>(workspace);
   MergeArgs m = {};
   m.n_samples = plan->S;
   m.O = O;
   m.LSE = LSE;
-  const bool tc = dtype == PT_BF16 && decode_tc_supported(D, page_size);
   cudaError_t e = cudaSuccess;
   if (tc) {
-    const bool tiles = use_tiles(plan, D);
     m.c0 = class_args(plan, tiles ? kDecRowsFew : kDecRows, D, ws);
     if (tiles) m.c1 = class_args(plan, kDecTile, D, ws);
-    m.R0 = kRowsR, m.BT0 = kRowsBT;
+    m.g0 = kRows;
     a.q_vec = (reinterpret_cast<uintptr_t>(Q) & 15u) == 0 && q_stride % 8 == 0;
     const int rc = decode_tc(plan, a, m.c0, m.c1, stream);
     if (rc) return (pt_status)rc;
   } else {
     m.c0 = class_args(plan, kDecSimt, D, ws);
-    m.R0 = kSimtR, m.BT0 = kSimtBT;
+    m.g0 = kSimt;
     a.workers = dec_workers(plan, kDecSimt);
     a.min_units = 2;
-    const size_t smem = 8 * (((size_t)m.c0.nseg + 31) / 32 + 1);
+    const size_t smem = 4 * (((size_t)m.c0.nseg + 31) / 32 + 1);
     ProfScope ps(stream, "decode_simt");
     e = dtype == PT_BF16 ? launch_simt<__nv_bfloat16>(a, m.c0, a.workers / 8, smem, stream)
                          : launch_simt<float>(a, m.c0, a.workers / 8, smem, stream);

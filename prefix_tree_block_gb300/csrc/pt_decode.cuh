@@ -25,7 +25,38 @@
 
 namespace pt {
 
-constexpr int kDecMaxNodes = 1 << 16;  // 8 bytes of shared memory per 32 nodes
+constexpr int kDecMaxNodes = 1 << 16;  // 4 or 8 bytes of shared memory per 32 nodes
+
+// Row and token tiles of a class: 2^r rows, 2^t tokens.
+struct DecTiling {
+  int r, t;
+};
+
+// The plan's classes: a call uses kDecSimt, or kDecRows, or kDecRowsFew with
+// kDecTile.
+enum : int {
+  kDecSimt = 0,     // CUDA cores: every node
+  kDecRows = 1,     // mma: every node
+  kDecRowsFew = 2,  // mma: nodes that few rows read, and the tails of the others
+  kDecTile = 3,     // tcgen05: the rest
+  kDecClasses = 4
+};
+constexpr DecTiling kSimt = {2, 4};  // a warp per worker
+constexpr DecTiling kRows = {4, 4};  // a warp per worker
+constexpr DecTiling kTile = {8, 7};  // a CTA per worker; an item of up to 128 rows has two partial results
+constexpr int kSimtR = 1 << kSimt.r, kSimtBT = 1 << kSimt.t;
+constexpr int kRowsR = 1 << kRows.r, kRowsBT = 1 << kRows.t;
+constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
+constexpr int kTileMinRows = 65;             // rows of the nodes that go to the tile kernel
+constexpr int kTileMaxD = 128;               // and the head dims it takes
+// Element (row, column) of a tile-class partial result: groups of 8 columns, in
+// each the rows one after another (D is a multiple of 8 there).
+__host__ __device__ inline long long tile_at(int D, long long slot, int row, int col) {
+  return ((slot * (D >> 3) + (col >> 3)) * kTileR + row) * 8 + (col & 7);
+}
+inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
+
+constexpr int kItemUnits = 3;  // what an item costs beside its units, in units
 
 // Which of a node's tokens a class's segment covers.  A class has at most one
 // segment per node, so a segment's number is its node's and its length is read
@@ -51,7 +82,7 @@ struct DecClass {
   const DecSeg* seg;  // [n_nodes]
   int nseg, nitems;
   // the class's part of the workspace
-  long long* pref;  // [nseg + 1] units before each segment; units per worker
+  int* pref;        // [nseg + 1] units before each segment; units per worker
   float* lse;       // [slot][R]
   float* opart;     // [slot][R][D]; the tile class: see tile_at
 };
@@ -67,7 +98,9 @@ struct DecArgs {
   long long q_stride;  // elements between query tokens
   int q_len, Hq, Hkv, g, D;
   int ps, max_pages, n_pages;
-  int workers, min_units;
+  int cap;             // max_pages * ps: tokens of a full table row
+  int sms;
+  int workers, min_units;  // CUDA cores
   int q_vec;           // Q's rows start on 16-byte boundaries
   float scale_log2;
 };
@@ -77,14 +110,8 @@ __device__ __forceinline__ DecSeg load_seg(const DecSeg* p) {
   return DecSeg{v.x, v.y, v.z, v.w};
 }
 
-__device__ __forceinline__ int dec_clamp(const DecArgs& a, int len, bool record) {
-  const long long cap = (long long)a.max_pages * a.ps;
-  if (len < 0 || len > cap) {
-    if (record) record_status(PT_STATUS_INVALID);
-    return len < 0 ? 0 : (int)cap;
-  }
-  return len;
-}
+// A node's length, or the nearest that its table can hold.
+__device__ __forceinline__ int dec_clamp(const DecArgs& a, int len) { return min(max(len, 0), a.cap); }
 
 // Tokens [b, e) of a node of len tokens.
 __device__ __forceinline__ void dec_range(const DecArgs& a, int kind, int len, int& b, int& e) {
@@ -97,16 +124,6 @@ __device__ __forceinline__ int dec_count(const DecArgs& a, int s) {
   return a.q_count ? min(max(a.q_count[s], 0), a.q_len) : a.q_len;
 }
 
-// Tiles of an item of the segment; 0 when its only sample has no queries.
-template <int BT>
-__device__ __forceinline__ int dec_tiles(const DecArgs& a, const DecSeg& sg, int len) {
-  if (sg.rows_kind == 0) return 0;
-  if (a.q_count && sg.solo >= 0 && dec_count(a, sg.solo) == 0) return 0;
-  int b, e;
-  dec_range(a, sg.kind(), len, b, e);
-  return (e - b + BT - 1) / BT;
-}
-
 // Query row r of a segment: its query token, q head, and the first token of
 // the node that it must not see.
 struct DecRow {
@@ -114,12 +131,9 @@ struct DecRow {
 };
 __device__ __forceinline__ DecRow dec_row(const DecArgs& a, int member0, int hk, int r, int len) {
   DecRow d;
-  int m = r, j = 0, h = 0;
-  if (a.g > 1) m = r / a.g, h = r - m * a.g;
-  if (a.q_len > 1) {
-    const int x = m;
-    m = x / a.q_len, j = x - m * a.q_len;
-  }
+  const int x = (int)((unsigned)r / (unsigned)a.g), h = r - x * a.g;
+  int m = x, j = 0;
+  if (a.q_len > 1) m = (int)((unsigned)x / (unsigned)a.q_len), j = x - m * a.q_len;
   const int mb = a.member[member0 + m], s = mb & INT_MAX;
   d.head = hk * a.g + h;
   d.tok = s * a.q_len + j;
@@ -139,69 +153,96 @@ __device__ __forceinline__ int dec_page(const DecArgs& a, int node, int pi) {
   return p;
 }
 
-__device__ __forceinline__ long long warp_incl_scan64(long long v, int lane) {
+// Code that runs once per launch is kept short here: its instructions come from
+// memory at about 2 GB/s per SM, 60 ns for every 128 bytes, and that is most of
+// these kernels' fixed cost.  So loops that are not hot stay rolled, a kernel
+// has one copy of the walk along the units, and units are counted in 32 bits
+// (the host refuses trees whose items, times the tiles of a full table row,
+// pass 2^31).
+__device__ __forceinline__ int warp_incl_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
 }
 
-// Units of segment i, and what it takes to know them.
-template <int R, int BT>
-__device__ __forceinline__ long long dec_units(const DecArgs& a, const DecClass& c, int i, bool record, DecSeg& sg,
-                                               int& len, int& tiles) {
+// Units of segment i, and what it takes to know them: its entry, its length
+// and the tiles of one of its items (0 when its only sample has no queries).
+__device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, DecTiling g, int i, DecSeg& sg, int& raw,
+                                         int& tiles) {
   sg = DecSeg{0, 0, 0, -1};
-  len = tiles = 0;
-  if (i >= c.nseg) return 0;
-  const int raw = a.lens[i];
-  sg = load_seg(c.seg + i);
-  len = dec_clamp(a, raw, record);
-  tiles = dec_tiles<BT>(a, sg, len);
-  return (long long)((sg.rows() + R - 1) / R * a.Hkv) * tiles;
+  raw = 0;
+  if (i < c.nseg) {
+    raw = a.lens[i];
+    sg = load_seg(c.seg + i);
+  }
+  int b, e;
+  dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
+  tiles = (e - b + (1 << g.t) - 1) >> g.t;
+  if (a.q_count && sg.solo >= 0 && a.q_count[sg.solo] <= 0) tiles = 0;
+  return ((sg.rows() + (1 << g.r) - 1) >> g.r) * a.Hkv * tiles;
 }
 
 // Exclusive sums of the class's units over chunks of 32 segments, in shared
-// memory (chunk[nc] = all of them); every thread of the block calls it.  Block
-// 0 also leaves each segment's sum and the units per worker for the merge.
-template <int R, int BT>
-__device__ __forceinline__ long long dec_scan(const DecArgs& a, const DecClass& c, long long* chunk) {
+// memory (chunk[nc] = all of them); every thread of the block calls it.
+// cost (or NULL): a shared counter, zero before, that receives what the units
+// cost, kItemUnits for each item among it, and for `tiles` a second time those
+// of row tiles more than half full.
+__device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c, DecTiling g, int* chunk,
+                                         unsigned long long* cost, bool tile) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int nc = (c.nseg + 31) >> 5;
-  DecSeg sg;
-  int len, tiles;
+#pragma unroll 1
   for (int k = warp; k < nc; k += nw) {
-    const long long u = dec_units<R, BT>(a, c, k * 32 + lane, blockIdx.x == 0, sg, len, tiles);
-    const long long s = warp_incl_scan64(u, lane);
-    if (lane == 31) chunk[k] = s;
+    DecSeg sg;
+    int raw, tiles;
+    const int u = dec_units(a, c, g, k * 32 + lane, sg, raw, tiles);
+    if (blockIdx.x == 0 && (raw < 0 || raw > a.cap)) record_status(PT_STATUS_INVALID);
+    const int sum = __reduce_add_sync(0xffffffffu, u);
+    if (lane == 0) chunk[k] = sum;
+    if (cost) {
+      const int rt = (sg.rows() + (1 << g.r) - 1) >> g.r, last = sg.rows() - ((rt - 1) << g.r);
+      unsigned x = u ? (unsigned)(u + kItemUnits * rt * a.Hkv) : 0u;
+      if (tile) x += u - (last <= 1 << (g.r - 1) ? a.Hkv * tiles : 0);
+      const unsigned hi = __reduce_add_sync(0xffffffffu, x >> 16), lo = __reduce_add_sync(0xffffffffu, x & 0xffffu);
+      if (lane == 0) atomicAdd(cost, ((unsigned long long)hi << 16) + lo);
+    }
   }
   __syncthreads();
   if (warp == 0) {
-    long long carry = 0;
+    int carry = 0;
+#pragma unroll 1
     for (int k0 = 0; k0 < nc; k0 += 32) {
-      const long long x = k0 + lane < nc ? chunk[k0 + lane] : 0;
-      const long long s = warp_incl_scan64(x, lane);
+      const int x = k0 + lane < nc ? chunk[k0 + lane] : 0;
+      const int s = warp_incl_scan(x, lane);
       if (k0 + lane < nc) chunk[k0 + lane] = carry + s - x;
       carry += __shfl_sync(0xffffffffu, s, 31);
     }
     if (lane == 0) chunk[nc] = carry;
   }
   __syncthreads();
-  const long long total = chunk[nc];
-  // (32-bit division where it will do)
-  long long per = total < INT_MAX ? ((int)total + a.workers - 1) / a.workers : (total + a.workers - 1) / a.workers;
-  per = max(per, (long long)a.min_units);
-  if (blockIdx.x == gridDim.x - 1) {  // (the last block: the line may end before its share)
-    for (int k = warp; k < nc; k += nw) {
-      const int i = k * 32 + lane;
-      const long long u = dec_units<R, BT>(a, c, i, false, sg, len, tiles);
-      const long long x = warp_incl_scan64(u, lane) - u;
-      if (i < c.nseg) c.pref[i] = chunk[k] + x;
-    }
-    if (threadIdx.x == 0) c.pref[c.nseg] = per;
+}
+
+// Units per worker.
+__device__ __forceinline__ int dec_share(int total, int workers, int min_units) {
+  return max((int)(((unsigned)total + workers - 1) / (unsigned)workers), min_units);
+}
+
+// What the merge needs of a class: the units before each segment, and a
+// worker's share.  One block of the grid calls it.
+__device__ __forceinline__ void dec_publish(const DecArgs& a, const DecClass& c, DecTiling g, const int* chunk, int per) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll 1
+  for (int k = warp; k < (c.nseg + 31) >> 5; k += nw) {
+    DecSeg sg;
+    int raw, tiles;
+    const int i = k * 32 + lane, u = dec_units(a, c, g, i, sg, raw, tiles);
+    const int x = warp_incl_scan(u, lane) - u;
+    if (i < c.nseg) c.pref[i] = chunk[k] + x;
   }
-  return per;
+  if (threadIdx.x == 0) c.pref[c.nseg] = per;
 }
 
 // A piece: units [t0, t1) of one item of segment `node`.
@@ -209,93 +250,66 @@ struct DecPiece {
   int node, len, kind, rows, member0;
   int rt, hk;  // row tile and kv head
   int t0, t1;
-  long long slot;
+  int slot;
 };
 
 // A worker's way along the line of units; every lane of a warp walks alike.
-template <int R, int BT>
 struct DecWalk {
   const DecArgs& a;
   const DecClass& c;
-  const long long* chunk;
-  long long pos, end, w;
+  const DecTiling g;
+  const int* chunk;
+  int pos, end, w;
   int k, nc;
   // the chunk's segments, one per lane
   DecSeg sg;
-  int len, tiles;
-  long long excl;
+  int raw, tiles, excl;
 
-  __device__ __forceinline__ DecWalk(const DecArgs& a_, const DecClass& c_, const long long* ch, long long worker,
-                                     long long per)
-      : a(a_), c(c_), chunk(ch), w(worker) {
+  __device__ __forceinline__ DecWalk(const DecArgs& a_, const DecClass& c_, DecTiling g_, const int* ch, int worker,
+                                     int per)
+      : a(a_), c(c_), g(g_), chunk(ch), w(worker) {
     nc = (c.nseg + 31) >> 5;
-    const long long total = chunk[nc];
-    pos = min(worker * per, total);
-    end = min(pos + per, total);
+    const int total = chunk[nc];
+    pos = (int)min((long long)worker * per, (long long)total);
+    end = (int)min((long long)pos + per, (long long)total);
     k = 0;
     if (pos < end) {
+#pragma unroll 1
       for (int span = 1 << (31 - __clz(nc)); span; span >>= 1)
         if (k + span < nc && chunk[k + span] <= pos) k += span;
-      load();
     }
-  }
-  __device__ __forceinline__ void load() {
-    const int lane = threadIdx.x & 31;
-    const long long u = dec_units<R, BT>(a, c, k * 32 + lane, false, sg, len, tiles);
-    excl = chunk[k] + warp_incl_scan64(u, lane) - u;
+    --k;  // loaded by the first next()
   }
   __device__ __forceinline__ bool next(DecPiece& p) {
     if (pos >= end) return false;
-    while (pos >= chunk[k + 1]) {
-      ++k;
-      load();
+    if (k < 0 || pos >= chunk[k + 1]) {
+#pragma unroll 1
+      do ++k;
+      while (pos >= chunk[k + 1]);
+      const int lane = threadIdx.x & 31, u = dec_units(a, c, g, k * 32 + lane, sg, raw, tiles);
+      excl = chunk[k] + warp_incl_scan(u, lane) - u;
     }
-    int l = 0;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const long long x = __shfl_sync(0xffffffffu, excl, l + o);
-      if (x <= pos) l += o;
-    }
+    // the segment that holds pos: the last that starts at or before it
+    const int l = 31 - __clz(__ballot_sync(0xffffffffu, excl <= pos));
     const int rk = __shfl_sync(0xffffffffu, sg.rows_kind, l);
     p.node = k * 32 + l;
-    p.len = __shfl_sync(0xffffffffu, len, l);
+    p.len = dec_clamp(a, __shfl_sync(0xffffffffu, raw, l));
     p.rows = rk & ((1 << 29) - 1);
     p.kind = (int)((unsigned)rk >> 29);
     p.member0 = __shfl_sync(0xffffffffu, sg.member0, l);
     const int item0 = __shfl_sync(0xffffffffu, sg.item0, l);
     const int nt = __shfl_sync(0xffffffffu, tiles, l);
-    const long long rel = pos - __shfl_sync(0xffffffffu, excl, l);
-    const int it = rel < INT_MAX ? (int)rel / nt : (int)(rel / nt);
-    p.t0 = (int)(rel - (long long)it * nt);
-    p.t1 = (int)min((long long)nt, p.t0 + (end - pos));
-    p.rt = it / a.Hkv;
+    const int rel = pos - __shfl_sync(0xffffffffu, excl, l);
+    const int it = (int)((unsigned)rel / (unsigned)nt);
+    p.t0 = rel - it * nt;
+    p.t1 = min(nt, p.t0 + (end - pos));
+    p.rt = (int)((unsigned)it / (unsigned)a.Hkv);
     p.hk = it - p.rt * a.Hkv;
     p.slot = w + item0 + it;
     pos += p.t1 - p.t0;
     return true;
   }
 };
-
-// The plan's classes: a call uses kDecSimt, or kDecRows, or kDecRowsFew with
-// kDecTile.
-enum : int {
-  kDecSimt = 0,     // CUDA cores: every node
-  kDecRows = 1,     // mma: every node
-  kDecRowsFew = 2,  // mma: nodes that few rows read, and the tails of the others
-  kDecTile = 3,     // tcgen05: the rest
-  kDecClasses = 4
-};
-constexpr int kSimtR = 4, kSimtBT = 16;      // rows and tokens of a tile; a warp per worker
-constexpr int kRowsR = 16, kRowsBT = 16;     // a warp per worker
-constexpr int kTileR = 256, kTileBT = 128;   // a CTA per worker; an item of up to 128 rows has two partial results
-constexpr int kTileMinRows = 65;             // rows of the nodes that go to the tile kernel
-constexpr int kTileMaxD = 128;               // and the head dims it takes
-// Element (row, column) of a tile-class partial result: groups of 8 columns, in
-// each the rows one after another (D is a multiple of 8 there).
-__host__ __device__ inline long long tile_at(int D, long long slot, int row, int col) {
-  return ((slot * (D >> 3) + (col >> 3)) * kTileR + row) * 8 + (col & 7);
-}
-inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
 
 }  // namespace pt
 

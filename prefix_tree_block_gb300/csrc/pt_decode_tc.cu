@@ -31,6 +31,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
+// 8 floats times f, one 32-byte store
+__device__ __forceinline__ void st_8(float* p, const uint32_t* v, float f) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(__uint_as_float(v[0]) * f),
+               "f"(__uint_as_float(v[1]) * f), "f"(__uint_as_float(v[2]) * f), "f"(__uint_as_float(v[3]) * f),
+               "f"(__uint_as_float(v[4]) * f), "f"(__uint_as_float(v[5]) * f), "f"(__uint_as_float(v[6]) * f),
+               "f"(__uint_as_float(v[7]) * f)
+               : "memory");
+}
 // d += a b, 16 x 8 x 16
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -63,194 +71,184 @@ struct RowsCfg {
   static constexpr int STAGES = NP == 1 ? 6 : NP == 2 ? 3 : NP == 3 ? 2 : 3;
   static constexpr int PANEL = 16 * 128;            // bytes: 16 tokens x 64 columns
   static constexpr int STAGE = 2 * NP * PANEL;      // K panels, V panels
-  static constexpr int OFF_BAR = WARPS * STAGES * STAGE;
-  static constexpr int OFF_CHUNK = OFF_BAR + WARPS * STAGES * 8;
+  static constexpr int RING = STAGES * STAGE;       // a warp's
+  static constexpr int OFF_BAR = WARPS * RING;
+  static constexpr int OFF_PIECE = OFF_BAR + WARPS * STAGES * 8;
+  static constexpr int OFF_CHUNK = OFF_PIECE + WARPS * 8 * (int)sizeof(DecPiece);
   static constexpr size_t smem(int nseg) { return OFF_CHUNK + 8 * ((size_t)(nseg + 31) / 32 + 1) + 1024; }
 };
 
+// One worker: a warp, with its ring (1024-byte aligned), its barriers
+// (initialised for one arrival) and room for kRowsPieces pieces.
+constexpr int kRowsPieces = 8;
 template <int NP>
-__global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
-    k_decode_rows(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const DecArgs a,
-                  const DecClass c) {
+__device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a,
+                                            const DecClass& c, const int* chunk, int per, int worker,
+                                            uint8_t* ring, uint64_t* full, DecPiece* pieces, volatile int* abort_flag) {
   using C = RowsCfg<NP>;
-  pdl_wait();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::STAGES;
-  long long* chunk = reinterpret_cast<long long*>(smem + C::OFF_CHUNK);
-  volatile __shared__ int abort_flag;
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < C::WARPS * C::STAGES; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + i, 1);
-    fence_mbar_init();
-    prefetch_tmap(&mK);
-    prefetch_tmap(&mV);
-  }
-  const long long per = dec_scan<kRowsR, kRowsBT>(a, c, chunk);  // (also publishes the barriers)
-  uint8_t* ring = smem + warp * (C::STAGES * C::STAGE);
+  static_assert(C::STAGES + 1 < kRowsPieces, "a piece per stage in flight, and the current one");
+  const int lane = threadIdx.x & 31;
   const uint32_t ring_u = smem_u32(ring);
-  const long long worker = (long long)blockIdx.x * C::WARPS + warp;
-
-  // --- loads: one tile a call, in the order of the arithmetic below
-  DecWalk<kRowsR, kRowsBT> ahead(a, c, chunk, worker, per);
+  DecWalk walk(a, c, kRows, chunk, worker, per);
+  // loads: the piece they are at, its first token and last page, and pages l_page0 + lane
   DecPiece lp;
   lp.t0 = lp.t1 = 0;
-  int l_base = 0, l_page0 = 0, my_page = 0;  // first token of the segment; pages l_page0 + lane
-  uint32_t issued = 0;
-  auto issue = [&]() {
-    if (lp.t0 >= lp.t1) {
-      if (!ahead.next(lp)) return;
-      int e;
-      dec_range(a, lp.kind, lp.len, l_base, e);
-      l_page0 = INT_MIN;
-    }
-    const int kv0 = l_base + lp.t0 * kRowsBT, pi = kv0 / a.ps;
-    if (l_page0 == INT_MIN || pi >= l_page0 + 32) {
-      l_page0 = pi;
-      int b, e;
-      dec_range(a, lp.kind, lp.len, b, e);
-      const int last = (min(e, b + lp.t1 * kRowsBT) - 1) / a.ps;  // last page of the piece
-      my_page = pi + lane <= last ? dec_page(a, lp.node, pi + lane) : 0;
-    }
-    const int page = __shfl_sync(0xffffffffu, my_page, pi - l_page0);
-    const uint32_t s = issued % C::STAGES;
-    if (lane == 0) {
-      mbar_expect_tx(full + s, C::STAGE);
-      const int row = kv0 - pi * a.ps, ph = page * a.Hkv + lp.hk;
-#pragma unroll
-      for (int pn = 0; pn < NP; ++pn) {
-        tma_load_3d(ring + s * C::STAGE + pn * C::PANEL, &mK, full + s, pn * 64, row, ph);
-        tma_load_3d(ring + s * C::STAGE + (NP + pn) * C::PANEL, &mV, full + s, pn * 64, row, ph);
-      }
-    }
-    ++lp.t0;
-    ++issued;
-  };
-#pragma unroll 1
-  for (int i = 0; i < C::STAGES; ++i) issue();
-
-  // --- arithmetic
-  DecWalk<kRowsR, kRowsBT> walk(a, c, chunk, worker, per);
-  DecPiece p;
-  uint32_t used = 0;
+  int l_base = 0, l_last = 0, l_page0 = 0, my_page = 0;
+  uint32_t issued = 0, used = 0, found = 0, at = 0;  // tiles; pieces
+  // the current piece
+  int t = 0, t1 = 0, kv_base = 0, rows_left = 0, lim_min = 0, lim_max = 0;
+  int lim[2] = {0, 0};
+  int slot = 0;
+  uint32_t q[NP * 4][4];
+  float o[NP * 8][4], m[2], l[2];
   const int r_lo = lane >> 2, c2 = (lane & 3) * 2;  // this lane's rows r_lo, r_lo + 8; its column pair
   // ldmatrix rows: K (matrices: tokens 0-7 / 8-15 by lane bit 4, columns by bit 3), V transposed (tokens by bit 3,
   // columns by bit 4); 16-byte pieces XOR the row's low three bits
   const int k_row = (lane & 7) + ((lane >> 4) << 3), k_cb = (lane >> 3) & 1;
   const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_cb = lane >> 4;
   bool ok = true;
-  while (ok && walk.next(p)) {
-    int b, e;
-    dec_range(a, p.kind, p.len, b, e);
-    uint32_t q[NP * 4][4];
-    int lim[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = p.rt * kRowsR + r_lo + i * 8;
-      const __nv_bfloat16* src = nullptr;
-      lim[i] = 0;
-      if (row < p.rows) {
-        const DecRow d = dec_row(a, p.member0, p.hk, row, p.len);
-        lim[i] = d.lim;
-        src = static_cast<const __nv_bfloat16*>(a.Q) + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
-      }
-#pragma unroll
-      for (int k = 0; k < NP * 4; ++k) {
-        const int col = k * 16 + c2;
-        q[k][i] = src && col < a.D ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
-        q[k][i + 2] = src && col + 8 < a.D ? *reinterpret_cast<const uint32_t*>(src + col + 8) : 0u;
-      }
-    }
-    // bounds of the piece's rows (rows that are none count as seeing nothing only for the upper one)
-    const int own_lo = min(p.rt * kRowsR + r_lo < p.rows ? lim[0] : INT_MAX, p.rt * kRowsR + r_lo + 8 < p.rows ? lim[1] : INT_MAX);
-    const int lim_min = __reduce_min_sync(0xffffffffu, own_lo);
-    const int lim_max = min(__reduce_max_sync(0xffffffffu, max(lim[0], lim[1])), e);
-    float o[NP * 8][4];
-#pragma unroll
-    for (int i = 0; i < NP * 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll 1
-    for (int t = p.t0; t < p.t1; ++t) {
-      const uint32_t s = used % C::STAGES;
-      ok = mbar_wait(full + s, (used / C::STAGES) & 1, &abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t kb = ring_u + s * C::STAGE, vb = kb + NP * C::PANEL;
-      const int kv0 = b + t * kRowsBT;
-      // S, in two chains of accumulation a column tile
-      float sc[2][2][4];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sc[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < NP * 4; ++k) {
-        uint32_t f[4];
-        ldsm4(f, kb + (k >> 2) * C::PANEL + k_row * 128 + ((((k & 3) * 2 + k_cb) ^ (k_row & 7)) << 4));
-        mma16816(sc[k & 1][0], q[k], f[0], f[1]);
-        mma16816(sc[k & 1][1], q[k], f[2], f[3]);
+  while (true) {
+    // --- loads, up to a ring ahead of the arithmetic
+#pragma unroll 1
+    while (issued - used < C::STAGES) {
+      if (lp.t0 >= lp.t1) {
+        if (!walk.next(lp)) break;
+        if (lane == 0) pieces[found % kRowsPieces] = lp;
+        ++found;
+        int e;
+        dec_range(a, lp.kind, lp.len, l_base, e);
+        l_last = (min(e, l_base + lp.t1 * kRowsBT) - 1) / a.ps;
+        l_page0 = -64;
       }
-      float x[2][4];  // [column tile of 8][(row lo: 2 columns), (row hi: 2 columns)]
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[n][i] = (sc[0][n][i] + sc[1][n][i]) * a.scale_log2;
-      const bool cut = kv0 + kRowsBT > lim_min;
-      if (cut) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1]) x[n][i] = -INFINITY;
+      const int kv0 = l_base + lp.t0 * kRowsBT, pi = kv0 / a.ps;
+      if (pi >= l_page0 + 32) {
+        l_page0 = pi;
+        my_page = pi + lane <= l_last ? dec_page(a, lp.node, pi + lane) : 0;
       }
-      bool grow = false;
-      float ref[2], al[2];
+      const int page = __shfl_sync(0xffffffffu, my_page, pi - l_page0);
+      const uint32_t s = issued % C::STAGES;
+      if (lane == 0) {
+        mbar_expect_tx(full + s, C::STAGE);
+        const int row = kv0 - pi * a.ps, ph = page * a.Hkv + lp.hk;
+#pragma unroll
+        for (int pn = 0; pn < NP; ++pn) {
+          tma_load_3d(ring + s * C::STAGE + pn * C::PANEL, &mK, full + s, pn * 64, row, ph);
+          tma_load_3d(ring + s * C::STAGE + (NP + pn) * C::PANEL, &mV, full + s, pn * 64, row, ph);
+        }
+      }
+      ++lp.t0;
+      ++issued;
+    }
+    if (used == issued) break;
+    // --- a new piece: its rows
+    if (t >= t1) {
+      __syncwarp();
+      const DecPiece& p = pieces[at % kRowsPieces];
+      ++at;
+      int e;
+      dec_range(a, p.kind, p.len, kv_base, e);
+      t = p.t0, t1 = p.t1, slot = p.slot;
+      rows_left = p.rows - p.rt * kRowsR;
+      int own_lo = INT_MAX;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const bool up = mx > m[i] + 8.f;
-        const float mn = up ? mx : m[i];
-        ref[i] = mn == -INFINITY ? 0.f : mn;
-        al[i] = up ? ex2(m[i] - ref[i]) : 1.f;
-        grow |= up;
-        m[i] = mn;
-      }
-      uint32_t pa[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[n][i] = ex2(x[n][i] - ref[i >> 1]);
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int i = 0; i < NP * 8; ++i) {
-          o[i][0] *= al[0], o[i][1] *= al[0];
-          o[i][2] *= al[1], o[i][3] *= al[1];
+        const int r = r_lo + i * 8;
+        const __nv_bfloat16* src = nullptr;
+        lim[i] = 0;
+        if (r < rows_left) {
+          const DecRow d = dec_row(a, p.member0, p.hk, p.rt * kRowsR + r, p.len);
+          lim[i] = d.lim;
+          own_lo = min(own_lo, d.lim);
+          src = static_cast<const __nv_bfloat16*>(a.Q) + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
         }
-        l[0] *= al[0];
-        l[1] *= al[1];
-      }
-      l[0] += (x[0][0] + x[0][1]) + (x[1][0] + x[1][1]);
-      l[1] += (x[0][2] + x[0][3]) + (x[1][2] + x[1][3]);
-      pa[0] = pack_bf16(x[0][0], x[0][1]);
-      pa[1] = pack_bf16(x[0][2], x[0][3]);
-      pa[2] = pack_bf16(x[1][0], x[1][1]);
-      pa[3] = pack_bf16(x[1][2], x[1][3]);
-      if (!cut) {
 #pragma unroll
         for (int k = 0; k < NP * 4; ++k) {
-          uint32_t f[4];
-          ldsm4t(f, vb + (k >> 2) * C::PANEL + v_row * 128 + ((((k & 3) * 2 + v_cb) ^ (v_row & 7)) << 4));
-          mma16816(o[2 * k], pa, f[0], f[1]);
-          mma16816(o[2 * k + 1], pa, f[2], f[3]);
+          const int col = k * 16 + c2;
+          q[k][i] = src && col < a.D ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
+          q[k][i + 2] = src && col + 8 < a.D ? *reinterpret_cast<const uint32_t*>(src + col + 8) : 0u;
         }
-      } else {
-        // Values that no row keeps are cleared: a probability of 0 times what
-        // lies behind the node's tokens must stay 0.  Tokens that some rows
-        // keep and others do not go through the product too unless one is not
-        // finite: then they are left out of it and added row by row.
-        const int n_all = min(max(lim_min - kv0, 0), kRowsBT), n_any = min(max(lim_max - kv0, 0), kRowsBT);
+        m[i] = -INFINITY, l[i] = 0.f;
+      }
+      // what all of the rows see, and what any of them does
+      lim_min = __reduce_min_sync(0xffffffffu, own_lo);
+      lim_max = min(__reduce_max_sync(0xffffffffu, max(lim[0], lim[1])), e);
+#pragma unroll
+      for (int i = 0; i < NP * 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+    // --- a tile of 16 tokens
+    const uint32_t s = used % C::STAGES;
+    ok = mbar_wait(full + s, (used / C::STAGES) & 1, abort_flag);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const uint32_t kb = ring_u + s * C::STAGE, vb = kb + NP * C::PANEL;
+    const int kv0 = kv_base + t * kRowsBT;
+    // S, in two chains of accumulation a column tile
+    float sc[2][2][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sc[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP * 4; ++k) {
+      uint32_t f[4];
+      ldsm4(f, kb + (k >> 2) * C::PANEL + k_row * 128 + ((((k & 3) * 2 + k_cb) ^ (k_row & 7)) << 4));
+      mma16816(sc[k & 1][0], q[k], f[0], f[1]);
+      mma16816(sc[k & 1][1], q[k], f[2], f[3]);
+    }
+    float x[2][4];  // [column tile of 8][(row lo: 2 columns), (row hi: 2 columns)]
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[n][i] = (sc[0][n][i] + sc[1][n][i]) * a.scale_log2;
+        if (kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1]) x[n][i] = -INFINITY;
+      }
+    bool grow = false;
+    float ref[2], al[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const bool up = mx > m[i] + 8.f;
+      const float mn = up ? mx : m[i];
+      ref[i] = mn == -INFINITY ? 0.f : mn;
+      al[i] = up ? ex2(m[i] - ref[i]) : 1.f;
+      grow |= up;
+      m[i] = mn;
+    }
+    uint32_t pa[4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = ex2(x[n][i] - ref[i >> 1]);
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int i = 0; i < NP * 8; ++i) {
+        o[i][0] *= al[0], o[i][1] *= al[0];
+        o[i][2] *= al[1], o[i][3] *= al[1];
+      }
+      l[0] *= al[0];
+      l[1] *= al[1];
+    }
+    l[0] += (x[0][0] + x[0][1]) + (x[1][0] + x[1][1]);
+    l[1] += (x[0][2] + x[0][3]) + (x[1][2] + x[1][3]);
+    pa[0] = pack_bf16(x[0][0], x[0][1]);
+    pa[1] = pack_bf16(x[0][2], x[0][3]);
+    pa[2] = pack_bf16(x[1][0], x[1][1]);
+    pa[3] = pack_bf16(x[1][2], x[1][3]);
+    // Values that no row keeps are cleared: a probability of 0 times what lies
+    // behind the node's tokens must stay 0.  Tokens that some rows keep and
+    // others do not go through the product too unless one is not finite: then
+    // they are left out of it and added row by row.
+    uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
+    int n_mul = kRowsBT, n_any = kRowsBT;
+    if (kv0 + kRowsBT > lim_min) {
+      n_any = min(max(lim_max - kv0, 0), kRowsBT);
+      n_mul = n_any;
+      const int n_all = min(max(lim_min - kv0, 0), kRowsBT);
+      if (n_all < n_any) {
         bool odd = false;
+#pragma unroll 1
         for (int i = n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
           const uint4 v = *reinterpret_cast<const uint4*>(ring + s * C::STAGE + (NP + ((i % (NP * 8)) >> 3)) * C::PANEL +
                                                           (i / (NP * 8)) * 128 + (i & 7) * 16);
@@ -258,52 +256,52 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
 #pragma unroll
           for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
         }
-        odd = __any_sync(0xffffffffu, odd);
-        const int n_mul = odd ? n_all : n_any;
-        // this lane's V elements of a fragment: tokens c2, c2 + 1 (f[0], f[2]) and c2 + 8, c2 + 9 (f[1], f[3])
-        const uint32_t k0 = (c2 < n_mul ? 0xffffu : 0u) | (c2 + 1 < n_mul ? 0xffff0000u : 0u);
-        const uint32_t k1 = (c2 + 8 < n_mul ? 0xffffu : 0u) | (c2 + 9 < n_mul ? 0xffff0000u : 0u);
-#pragma unroll
-        for (int k = 0; k < NP * 4; ++k) {
-          uint32_t f[4];
-          ldsm4t(f, vb + (k >> 2) * C::PANEL + v_row * 128 + ((((k & 3) * 2 + v_cb) ^ (v_row & 7)) << 4));
-          mma16816(o[2 * k], pa, f[0] & k0, f[1] & k1);
-          mma16816(o[2 * k + 1], pa, f[2] & k0, f[3] & k1);
-        }
-        for (int n = n_mul; n < n_any; ++n) {
-          float pr[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float even = n & 8 ? x[1][2 * i] : x[0][2 * i], oddc = n & 8 ? x[1][2 * i + 1] : x[0][2 * i + 1];
-            pr[i] = __shfl_sync(0xffffffffu, n & 1 ? oddc : even, (lane & ~3) | ((n & 7) >> 1));
-          }
-#pragma unroll
-          for (int k = 0; k < NP * 8; ++k) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + s * C::STAGE + (NP + (k >> 3)) * C::PANEL + n * 128 +
-                                                                  (((k & 7) ^ (n & 7)) << 4) + (lane & 3) * 4);
-            const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (kv0 + n < lim[i]) {
-                o[k][2 * i] = fmaf(pr[i], v0, o[k][2 * i]);
-                o[k][2 * i + 1] = fmaf(pr[i], v1, o[k][2 * i + 1]);
-              }
-          }
-        }
+        if (__any_sync(0xffffffffu, odd)) n_mul = n_all;
       }
-      ++used;
-      __syncwarp();  // every lane has read the stage
-      issue();
+      // this lane's V elements of a fragment: tokens c2, c2 + 1 (f[0], f[2]) and c2 + 8, c2 + 9 (f[1], f[3])
+      k0 = (c2 < n_mul ? 0xffffu : 0u) | (c2 + 1 < n_mul ? 0xffff0000u : 0u);
+      k1 = (c2 + 8 < n_mul ? 0xffffu : 0u) | (c2 + 9 < n_mul ? 0xffff0000u : 0u);
     }
-    if (!ok) break;
-    // the piece's partial result
+#pragma unroll
+    for (int k = 0; k < NP * 4; ++k) {
+      uint32_t f[4];
+      ldsm4t(f, vb + (k >> 2) * C::PANEL + v_row * 128 + ((((k & 3) * 2 + v_cb) ^ (v_row & 7)) << 4));
+      mma16816(o[2 * k], pa, f[0] & k0, f[1] & k1);
+      mma16816(o[2 * k + 1], pa, f[2] & k0, f[3] & k1);
+    }
+#pragma unroll 1
+    for (int n = n_mul; n < n_any; ++n) {
+      float pr[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float even = n & 8 ? x[1][2 * i] : x[0][2 * i], oddc = n & 8 ? x[1][2 * i + 1] : x[0][2 * i + 1];
+        pr[i] = __shfl_sync(0xffffffffu, n & 1 ? oddc : even, (lane & ~3) | ((n & 7) >> 1));
+      }
+#pragma unroll
+      for (int k = 0; k < NP * 8; ++k) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + s * C::STAGE + (NP + (k >> 3)) * C::PANEL + n * 128 +
+                                                              (((k & 7) ^ (n & 7)) << 4) + (lane & 3) * 4);
+        const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (kv0 + n < lim[i]) {
+            o[k][2 * i] = fmaf(pr[i], v0, o[k][2 * i]);
+            o[k][2 * i + 1] = fmaf(pr[i], v1, o[k][2 * i + 1]);
+          }
+      }
+    }
+    ++used;
+    ++t;
+    __syncwarp();  // every lane has read the stage
+    if (t < t1) continue;
+    // --- the piece's partial result
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (p.rt * kRowsR + r_lo + i * 8 >= p.rows) continue;
+      if (r_lo + i * 8 >= rows_left) continue;
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-      const long long row = p.slot * kRowsR + r_lo + i * 8;
+      const long long row = (long long)slot * kRowsR + r_lo + i * 8;
       if (c2 == 0) c.lse[row] = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
       float* dst = c.opart + row * a.D + c2;
 #pragma unroll
@@ -316,9 +314,80 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
   }
 }
 
+// The fewest tile units worth a partial result of their own.
+constexpr int kTileMinUnits = 2;
+
+// How the SMs are divided when a call has both kinds of segments (below): every
+// CTA of both kernels scans both classes and finds the same numbers.
+struct DecSplit {
+  int n_tile;         // SMs of the tile kernel; the rows kernel has the others
+  int per_t, per_r;   // units per worker
+};
+template <int NP>
+__device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& ct, const DecClass& cr, int* chunk_t,
+                                              int* chunk_r, unsigned long long* cost, int sms, int rows_per_sm) {
+#pragma unroll 1
+  for (int i = ct.nitems ? 0 : 1; i < (cr.nitems ? 2 : 1); ++i)
+    dec_scan(a, i ? cr : ct, DecTiling{i ? kRows.r : kTile.r, i ? kRows.t : kTile.t}, i ? chunk_r : chunk_t, ct.nitems && cr.nitems ? cost + i : nullptr, i == 0);
+  const int nc = (max(ct.nseg, cr.nseg) + 31) >> 5;
+  const int units_t = ct.nitems ? chunk_t[nc] : 0, units_r = cr.nitems ? chunk_r[nc] : 0;
+  DecSplit s;
+  s.n_tile = units_t > 0 ? sms : 0;
+  if (units_t > 0 && units_r > 0) {
+    // a tile unit of up to 128 rows costs an SM about as much as this many units of 16 rows and tokens
+    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f);
+    s.n_tile = min(max((int)(sms * (x / (x + (float)cost[1]))), 1), sms - 1);
+  }
+  s.per_t = dec_share(units_t, max(s.n_tile, 1), kTileMinUnits);
+  s.per_r = dec_share(units_r, max(sms - s.n_tile, 1) * rows_per_sm, 1);
+  return s;
+}
+
+template <int NP>
+__global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
+    k_decode_rows(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const DecArgs a,
+                  const DecClass c, const DecClass ct) {
+  using C = RowsCfg<NP>;
+  // Beside a tile kernel this one starts when that one has begun (it has then
+  // waited for what came before both), runs on the SMs that it leaves, and
+  // ends after it, so that waiting for this kernel is waiting for both.
+  const bool beside = ct.nitems > 0;
+  if (!beside) pdl_wait();
+  pdl_launch();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  int* chunk = reinterpret_cast<int*>(smem + C::OFF_CHUNK);
+  volatile __shared__ int abort_flag;
+  __shared__ unsigned long long cost[2];
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    cost[0] = cost[1] = 0;
+#pragma unroll 1
+    for (int i = 0; i < C::WARPS * C::STAGES; ++i) mbar_init(bars + i, 1);
+    fence_mbar_init();
+    prefetch_tmap(&mK);
+    prefetch_tmap(&mV);
+  }
+  __syncthreads();
+  const DecSplit sp = dec_split<NP>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::WARPS);
+  if ((int)blockIdx.x == 0) dec_publish(a, c, kRows, chunk, sp.per_r);
+  if ((int)blockIdx.x < (a.sms - sp.n_tile) * C::CTAS)
+    rows_worker<NP>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::WARPS + warp, smem + warp * C::RING,
+                    bars + warp * C::STAGES, reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE) + warp * kRowsPieces,
+                    &abort_flag);
+  if (beside) pdl_wait();
+}
+
 // ---------------------------------------------------------------------------
-// Segments that many rows read (a prompt under many completions): tcgen05, a
-// CTA per worker, up to 256 query rows an item, 128 tokens a step.
+// Trees in which many rows read a segment (a prompt under many completions):
+// such segments run on tcgen05, a CTA per worker, up to 256 query rows an item,
+// 128 tokens a step; the others as above, in the kernel launched behind this
+// one.  The first kind is bound by its softmax and tensor work, the second by
+// memory, so the SMs are divided between the two by what their units cost and
+// they overlap: the CTAs of this kernel that have no share end at once, and the
+// other's take their SMs.
 //
 // The forward's structure with the mask gone: a producer warp brings K and V
 // tiles by TMA (boxes of whole pages, or of the power of two that divides
@@ -340,15 +409,18 @@ struct TileCfg {
   static constexpr int D = NP * 64;
   static constexpr int PANEL = 128 * 128;  // bytes: 128 rows x 64 columns
   static constexpr int TILE = NP * PANEL;
-  static constexpr int KS = NP == 1 ? 4 : 2, VS = NP == 1 ? 4 : 2;
+  static constexpr int KS = NP == 1 ? 4 : 2, VS = KS;
   static constexpr int OFF_Q = 0;  // two tiles of 128 rows
   static constexpr int OFF_K = OFF_Q + 2 * TILE;
   static constexpr int OFF_V = OFF_K + KS * TILE;
   static constexpr int OFF_BAR = OFF_V + VS * TILE;
   // q_full q_empty k_full[KS] k_empty[KS] v_full[VS] v_empty[VS] s_full[2] p_full[2] o_full[2] o_free[2] done
   static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 9;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_CHUNK = OFF_MISC + 16;
+  static constexpr int OFF_PIECE_BAR = OFF_BAR + NBAR * 8;  // full[PIECES] empty[PIECES]
+  static constexpr int PIECES = 4;
+  static constexpr int OFF_PIECE = OFF_PIECE_BAR + 2 * PIECES * 8;
+  static constexpr int OFF_MISC = OFF_PIECE + PIECES * (int)sizeof(DecPiece);
+  static constexpr int OFF_CHUNK = OFF_MISC + 16;  // the classes' chunk sums: tile, rows
   static constexpr size_t smem(int nseg) { return OFF_CHUNK + 8 * ((size_t)(nseg + 31) / 32 + 1) + 1024; }
   static constexpr int TM_S = 0, TM_O = 256;  // S(h) at h * 128, O(h) at 256 + h * D
   static constexpr int THREADS = 384;         // two softmax warpgroups; producer, MMA and two query warps
@@ -361,10 +433,11 @@ struct TileCfg {
 template <int NP>
 __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     k_decode_tile(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const DecArgs a,
-                  const DecClass c, const int box_rows, const int oob_head) {
+                  const DecClass c, const DecClass cr, const int rows_per_sm, const int box_rows, const int oob_head) {
   using C = TileCfg<NP>;
   constexpr int D = C::D;
   pdl_wait();
+  pdl_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -378,12 +451,16 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   uint64_t* o_full = p_full + 2;
   uint64_t* o_free = o_full + 2;
   uint64_t* done = o_free + 2;
+  uint64_t* piece_full = reinterpret_cast<uint64_t*>(smem + C::OFF_PIECE_BAR);
+  uint64_t* piece_empty = piece_full + C::PIECES;
+  DecPiece* pieces = reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  long long* chunk = reinterpret_cast<long long*>(smem + C::OFF_CHUNK);
+  int* chunk = reinterpret_cast<int*>(smem + C::OFF_CHUNK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ unsigned long long cost[2];
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 64);
+    mbar_init(q_full, 8);
     mbar_init(q_empty, 1);
     for (int i = 0; i < C::KS; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
     for (int i = 0; i < C::VS; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1);
@@ -394,28 +471,58 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
       mbar_init(o_free + h, 128);
     }
     mbar_init(done, 1);
+#pragma unroll 1
+    for (int i = 0; i < C::PIECES; ++i) mbar_init(piece_full + i, 1), mbar_init(piece_empty + i, 11);
     *abort_flag = 0;
+    cost[0] = cost[1] = 0;
     fence_mbar_init();
     prefetch_tmap(&mK);
     prefetch_tmap(&mV);
   }
+  __syncthreads();
+  const DecSplit sp = dec_split<NP>(a, c, cr, chunk, chunk + ((c.nseg + 31) >> 5) + 1, cost, gridDim.x, rows_per_sm);
+  if (blockIdx.x == 0) dec_publish(a, c, kTile, chunk, sp.per_t);
+  if ((int)blockIdx.x >= sp.n_tile) return;
+  const int worker = blockIdx.x, per = sp.per_t;
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  const long long per = dec_scan<kTileR, kTileBT>(a, c, chunk);  // (its barriers publish the above)
+  __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const long long worker = blockIdx.x;
+
+  // The producer walks along the CTA's units and hands each piece to the other
+  // warps through a ring; one without rows ends it.
+  const auto get_piece = [&](DecPiece& p, uint32_t i) {  // the i-th; all lanes of a warp
+    const uint32_t s = i % C::PIECES;
+    bool ok = mbar_wait(piece_full + s, (i / C::PIECES) & 1, abort_flag);
+    if (!(ok = __all_sync(0xffffffffu, ok))) return false;
+    p = pieces[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(piece_empty + s);
+    return p.rows > 0;
+  };
 
   const auto producer_role = [&]() {
-    DecWalk<kTileR, kTileBT> walk(a, c, chunk, worker, per);
+    DecWalk walk(a, c, kTile, chunk, worker, per);
     DecPiece p;
-    uint32_t n = 0;  // tiles issued
+    uint32_t n = 0, np = 0;  // tiles issued; pieces
     bool ok = true;
     const int boxes = kTileBT / box_rows;  // 1..8, a power of two
-    while (ok && walk.next(p)) {
+#pragma unroll 1
+    while (true) {
+      const bool more = walk.next(p);
+      if (!more) p.rows = 0;
+      if (np >= C::PIECES) ok = mbar_wait(piece_empty + np % C::PIECES, (np / C::PIECES - 1) & 1, abort_flag);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (lane == 0) {
+        pieces[np % C::PIECES] = p;
+        mbar_arrive(piece_full + np % C::PIECES);
+      }
+      ++np;
+      if (!more) break;
       int b, e;
       dec_range(a, p.kind, p.len, b, e);
       const int bt = lane & (boxes - 1);  // this lane's box of the tile; its page, looked up a tile ahead
@@ -424,6 +531,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         return t < p.t1 && kv < e ? dec_page(a, p.node, kv / a.ps) : -1;
       };
       int page = page_of(p.t0);
+#pragma unroll 1
       for (int t = p.t0; t < p.t1; ++t, ++n) {
         const int ahead = page_of(t + 1);
         const int kv = t * kTileBT + bt * box_rows;
@@ -454,6 +562,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         }
         page = ahead;
       }
+      if (!ok) break;
     }
     if (!ok && lane == 0) {  // let the copies in flight land
       for (uint32_t i = 0; i < C::KS && i < n; ++i) mbar_wait_drain(k_full + (n - 1 - i) % C::KS, ((n - 1 - i) / C::KS) & 1, 20000000);
@@ -466,53 +575,57 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
     constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
     const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
-    DecWalk<kTileR, kTileBT> walk(a, c, chunk, worker, per);
     DecPiece p;
     uint32_t n = 0, it = 0;       // tiles before this piece; pieces
     uint32_t pc[2] = {0, 0};      // PV steps per warpgroup
     uint32_t oc[2] = {0, 0};      // pieces in which the warpgroup had steps
     bool ok = true;
-    while (ok && walk.next(p)) {
+#pragma unroll 1
+    while (ok && get_piece(p, it)) {
       const int pair = p.rows - p.rt * kTileR > kTileR / 2 ? 1 : 0;
       const int tiles = p.t1 - p.t0, steps = tiles << pair;
       ok = __all_sync(0xffffffffu, mbar_wait(q_full, it & 1, abort_flag));
-      for (int u = 0; u < steps + 2 && ok; ++u) {
-        const int h = u & 1;
-        if (u >= 2) {  // PV of step u - 2
-          const uint32_t x = n + ((u - 2) >> pair), vs = x % C::VS;
-          ok = mbar_wait(p_full + h, pc[h] & 1, abort_flag) && mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
-          if (u < 4 && oc[h] > 0) ok = ok && mbar_wait(o_free + h, (oc[h] - 1) & 1, abort_flag);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc_fence_after();
-          if (lane == 0) {
+#pragma unroll 1
+      for (int u0 = 0; u0 < steps + 2 && ok; u0 += 2) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tbase + C::TM_O + h * D, tbase + C::TM_S + h * 128 + kk * 8,
-                     sdesc_sw128(sV + vs * C::TILE + kk * 2048, C::PANEL, 1024), IDESC_PV, u >= 4 || kk > 0);
-            if (!pair || h == 1) mma_commit(v_empty + vs);
-            if (u >= steps) mma_commit(o_full + h);  // the warpgroup's last
-          }
-          ++pc[h];
-        }
-        if (u < steps) {
-          const uint32_t x = n + (u >> pair), ks = x % C::KS;
-          ok = mbar_wait(k_full + ks, (x / C::KS) & 1, abort_flag);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t qa = sQ + (pair ? h * C::TILE : 0);
+        for (int h = 0; h < 2; ++h) {  // (constant, so that the counters stay in registers)
+          const int u = u0 + h;
+          if (u >= 2 && u < steps + 2) {  // PV of step u - 2
+            const uint32_t x = n + ((u - 2) >> pair), vs = x % C::VS;
+            ok = mbar_wait(p_full + h, pc[h] & 1, abort_flag) && mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
+            if (u < 4 && oc[h] > 0) ok = ok && mbar_wait(o_free + h, (oc[h] - 1) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
-              mma_ss(tbase + C::TM_S + h * 128, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(sK + ks * C::TILE + off, 16, 1024),
-                     IDESC_S, kk > 0);
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(tbase + C::TM_O + h * D, tbase + C::TM_S + h * 128 + kk * 8,
+                       sdesc_sw128(sV + vs * C::TILE + kk * 2048, C::PANEL, 1024), IDESC_PV, u >= 4 || kk > 0);
+              if (!pair || h == 1) mma_commit(v_empty + vs);
+              if (u >= steps) mma_commit(o_full + h);  // the warpgroup's last
             }
-            mma_commit(s_full + h);
-            if (!pair || h == 1) mma_commit(k_empty + ks);
-            if (u == steps - 1) mma_commit(q_empty);
+            ++pc[h];
           }
+          if (u < steps) {
+            const uint32_t x = n + (u >> pair), ks = x % C::KS;
+            ok = mbar_wait(k_full + ks, (x / C::KS) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t qa = sQ + (pair ? h * C::TILE : 0);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
+                mma_ss(tbase + C::TM_S + h * 128, sdesc_sw128(qa + off, 16, 1024),
+                       sdesc_sw128(sK + ks * C::TILE + off, 16, 1024), IDESC_S, kk > 0);
+              }
+              mma_commit(s_full + h);
+              if (!pair || h == 1) mma_commit(k_empty + ks);
+              if (u == steps - 1) mma_commit(q_empty);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       n += tiles;
       ++it;
@@ -526,48 +639,56 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     __syncwarp();
   };
 
-  // Two warps gather the item's query rows (16-byte asynchronous copies, a row's
-  // lanes side by side) as soon as the last S of the piece before is done, so
-  // the loads run under that piece's last steps and its output.
-  const auto query_role = [&]() {
-    DecWalk<kTileR, kTileBT> walk(a, c, chunk, worker, per);
-    DecPiece p;
-    uint32_t it = 0;
-    bool ok = true;
+  // Gathers an item's query rows into the Q tiles, warp w of every `nw`: 16-byte
+  // asynchronous copies, a row's lanes side by side.
+  const auto gather_rows = [&](const DecPiece& p, int w, int nw) {
     constexpr int CPR = NP * 8, RPI = 32 / CPR;  // 16-byte pieces of a row; rows per warp instruction
-    while (walk.next(p)) {
-      const int left = p.rows - p.rt * kTileR, rows = left > kTileR / 2 ? kTileR : kTileR / 2;
-      if (it > 0) ok = mbar_wait(q_empty, (it - 1) & 1, abort_flag);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      for (int r0 = (warp - 10) * 32; r0 < rows; r0 += 64) {
-        long long src = -1;  // this lane's row
-        if (r0 + lane < left) {
-          const DecRow d = dec_row(a, p.member0, p.hk, p.rt * kTileR + r0 + lane, p.len);
-          src = (long long)d.tok * a.q_stride + (long long)d.head * a.D;
-        }
-#pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          const int x = r0 + i * RPI + lane / CPR, k = lane % CPR;
-          const long long at = __shfl_sync(0xffffffffu, src, i * RPI + lane / CPR);
-          const bool in = at >= 0 && k * 8 < a.D;
-          const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.Q) + (in ? at + k * 8 : 0);
-          uint8_t* dst = smem + C::OFF_Q + (x >> 7) * C::TILE + (k >> 3) * C::PANEL + (x & 127) * 128 + (((k & 7) ^ (x & 7)) << 4);
-          if (a.q_vec) {
-            cp_async16(dst, g, in ? 16 : 0);
-          } else {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (in) {
-              const uint32_t* w = reinterpret_cast<const uint32_t*>(g);
-              v = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            *reinterpret_cast<uint4*>(dst) = v;
+    const int k = lane % CPR, ir = lane / CPR;
+    const int left = p.rows - p.rt * kTileR, rows = left > kTileR / 2 ? kTileR : kTileR / 2;
+#pragma unroll 1
+    for (int r0 = w * 32; r0 < rows; r0 += nw * 32) {
+      long long src = -1;  // element offset of this lane's row, or -1
+      if (r0 + lane < left) {
+        const DecRow d = dec_row(a, p.member0, p.hk, p.rt * kTileR + r0 + lane, p.len);
+        src = (long long)d.tok * a.q_stride + (long long)d.head * a.D;
+      }
+#pragma unroll 4
+      for (int i = 0; i < 32; i += RPI) {
+        const int x = r0 + i + ir;
+        const long long at = __shfl_sync(0xffffffffu, src, i + ir);
+        const bool in = at >= 0 && k * 8 < a.D;
+        const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.Q) + (in ? at + k * 8 : 0);
+        uint8_t* dst = smem + C::OFF_Q + (x >> 7) * C::TILE + (k >> 3) * C::PANEL + (x & 127) * 128 + (((k & 7) ^ (x & 7)) << 4);
+        if (a.q_vec) {
+          cp_async16(dst, g, in ? 16 : 0);
+        } else {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (in) {
+            const uint32_t* y = reinterpret_cast<const uint32_t*>(g);
+            v = make_uint4(y[0], y[1], y[2], y[3]);
           }
+          *reinterpret_cast<uint4*>(dst) = v;
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
-      ++it;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cnt(q_full, 8 / nw);
+  };
+
+  // The first piece's rows come by the softmax warps, which have nothing else
+  // to do then; the others' by two warps of their own, as soon as the last S of
+  // the piece before is done, so the loads run under that piece's last steps
+  // and its output.
+  const auto query_role = [&]() {
+    DecPiece p;
+#pragma unroll 1
+    for (uint32_t it = 0; get_piece(p, it); ++it) {
+      if (it == 0) continue;
+      bool ok = mbar_wait(q_empty, (it - 1) & 1, abort_flag);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      gather_rows(p, warp - 10, 2);
     }
     __syncwarp();
   };
@@ -576,23 +697,30 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     const int h = warp >> 2, r = threadIdx.x & 127;  // warpgroup; row in its tile, TMEM lane
     const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t sb = tl + C::TM_S + h * 128, ob = tl + C::TM_O + h * D;
-    DecWalk<kTileR, kTileBT> walk(a, c, chunk, worker, per);
-    DecPiece p;
-    uint32_t n = 0, sc = 0, oc = 0;
+    uint32_t n = 0, sc = 0, oc = 0, it = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
-      int b, e;
-      dec_range(a, p.kind, p.len, b, e);
-      const int left = p.rows - p.rt * kTileR;
-      const int pair = left > kTileR / 2 ? 1 : 0;
-      const int tiles = p.t1 - p.t0, steps = tiles << pair;
-      const int n_rows = min(pair ? left - h * 128 : left, 128);  // this warpgroup's rows
-      const bool live = (warp & 3) * 32 < n_rows;                 // this warp has some
+#pragma unroll 1
+    while (ok) {
+      // of the piece: row tiles in it, its steps, this warpgroup's rows, tokens from its first tile on, partial result
+      int pair, steps, n_rows, tok, slot;
+      {
+        DecPiece p;
+        if (!get_piece(p, it)) break;
+        if (it++ == 0) gather_rows(p, warp, 8);
+        int b;
+        dec_range(a, p.kind, p.len, b, tok);
+        tok -= p.t0 * kTileBT;
+        const int left = p.rows - p.rt * kTileR;
+        pair = left > kTileR / 2 ? 1 : 0;
+        steps = (p.t1 - p.t0) << pair;
+        n_rows = min(pair ? left - h * 128 : left, 128);
+        slot = p.slot;
+      }
+      const bool live = (warp & 3) * 32 < n_rows;  // this warp has some
       float m_use = -INFINITY, l = 0.f;
-      bool any = false;
+#pragma unroll 1
       for (int u = h; u < steps; u += 2, ++sc) {
-        any = true;
-        const int t = p.t0 + (u >> pair), n_tok = min(e - t * kTileBT, kTileBT);
+        const int n_tok = min(tok - (u >> pair) * kTileBT, kTileBT);
         if (n_tok < kTileBT) {  // clear V's rows behind the last token (both warpgroups of a pair: the same zeros)
           const uint32_t x = n + (u >> pair), vs = x % C::VS;
           ok = mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
@@ -668,10 +796,10 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         mbar_arrive(p_full + h);
       }
       if (!ok) break;
-      n += tiles;
+      n += steps >> pair;
       // the warpgroup's partial result
-      const long long at = p.slot * kTileR + h * 128 + r;
-      if (any) {
+      const long long at = (long long)slot * kTileR + h * 128 + r;
+      if (h < steps) {
         ok = mbar_wait(o_full + h, oc & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         ++oc;
@@ -681,7 +809,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
           if (r < n_rows) c.lse[at] = l == 0.f ? -INFINITY : m_use + log2f(l);
           // 8 columns of all rows side by side (tile_at): a warp's store covers 1 KB in one piece, where rows of
           // their own would scatter it over 32 lines
-          float* dst = c.opart + tile_at(a.D, p.slot, h * 128 + r, 0);
+          float* dst = c.opart + tile_at(a.D, slot, h * 128 + r, 0);
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t orr[32];
@@ -689,11 +817,8 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
             tmem_ld_wait();
             if (r < n_rows) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                if (k * 32 + i < a.D)
-                  *reinterpret_cast<float4*>(dst + (k * 4 + (i >> 3)) * (kTileR * 8) + (i & 4)) =
-                      make_float4(__uint_as_float(orr[i]) * inv, __uint_as_float(orr[i + 1]) * inv,
-                                  __uint_as_float(orr[i + 2]) * inv, __uint_as_float(orr[i + 3]) * inv);
+              for (int i = 0; i < 32; i += 8)
+                if (k * 32 + i < a.D) st_8(dst + (k * 4 + (i >> 3)) * (kTileR * 8), orr + i, inv);
             }
           }
         }
@@ -746,29 +871,26 @@ bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long lon
 }
 
 template <int NP>
-cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, DecArgs a, const DecClass& c, int sms,
-                        cudaStream_t s) {
+cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
+                        const DecClass& ct, cudaStream_t s) {
   using C = RowsCfg<NP>;
   const size_t smem = C::smem(c.nseg);
   cudaError_t e = cudaFuncSetAttribute(k_decode_rows<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  a.workers = sms * C::CTAS * C::WARPS;
-  a.min_units = 1;
   count_launch();
-  return launch_pdl(k_decode_rows<NP>, dim3(sms * C::CTAS), dim3(C::WARPS * 32), smem, s, mK, mV, a, c);
+  return launch_pdl(k_decode_rows<NP>, dim3(a.sms * C::CTAS), dim3(C::WARPS * 32), smem, s, mK, mV, a, c, ct);
 }
 
 template <int NP>
-cudaError_t launch_tile(const CUtensorMap& mK, const CUtensorMap& mV, DecArgs a, const DecClass& c, int sms, int box_rows,
-                        int heads, cudaStream_t s) {
+cudaError_t launch_tile(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
+                        const DecClass& cr, int box_rows, int heads, cudaStream_t s) {
   using C = TileCfg<NP>;
   const size_t smem = C::smem(c.nseg);
   cudaError_t e = cudaFuncSetAttribute(k_decode_tile<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  a.workers = sms;
-  a.min_units = 1;
   count_launch();
-  return launch_pdl(k_decode_tile<NP>, dim3(sms), dim3(C::THREADS), smem, s, mK, mV, a, c, box_rows, heads);
+  return launch_pdl(k_decode_tile<NP>, dim3(a.sms), dim3(C::THREADS), smem, s, mK, mV, a, c, cr,
+                    RowsCfg<NP>::CTAS * RowsCfg<NP>::WARPS, box_rows, heads);
 }
 
 }  // namespace
@@ -781,26 +903,25 @@ int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const Dec
     set_error("pt_attn_decode: %d pages of %d heads are out of range", a.n_pages, a.Hkv);
     return PT_ERR_INVALID_ARG;
   }
-  CUtensorMap mK, mV;
+  CUtensorMap mK, mV, mKt, mVt;
   cudaError_t e = cudaSuccess;
   const int np = (a.D + 63) / 64;
+  if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, 16) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, 16))
+    return PT_ERR_CUDA;
+  a.sms = p->sms;
+  ProfScope ps(s, tile.nitems ? "decode_tile" : "decode_rows");  // (two kernels that overlap have one scope)
   if (tile.nitems) {
     const int box = std::min(a.ps & -a.ps, kTileBT);  // the largest power of two that divides a page
-    if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, box) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, box))
+    if (!make_tmap_pages(&mKt, a.Kc, a.D, a.ps, heads, box) || !make_tmap_pages(&mVt, a.Vc, a.D, a.ps, heads, box))
       return PT_ERR_CUDA;
-    ProfScope ps(s, "decode_tile");
-    e = np == 1 ? launch_tile<1>(mK, mV, a, tile, p->sms, box, (int)heads, s)
-                : launch_tile<2>(mK, mV, a, tile, p->sms, box, (int)heads, s);
+    e = np == 1 ? launch_tile<1>(mKt, mVt, a, tile, rows, box, (int)heads, s)
+                : launch_tile<2>(mKt, mVt, a, tile, rows, box, (int)heads, s);
   }
-  if (e == cudaSuccess && rows.nitems) {
-    if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, 16) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, 16))
-      return PT_ERR_CUDA;
-    ProfScope ps(s, "decode_rows");
-    e = np == 1   ? launch_rows<1>(mK, mV, a, rows, p->sms, s)
-        : np == 2 ? launch_rows<2>(mK, mV, a, rows, p->sms, s)
-        : np == 3 ? launch_rows<3>(mK, mV, a, rows, p->sms, s)
-                  : launch_rows<4>(mK, mV, a, rows, p->sms, s);
-  }
+  if (e == cudaSuccess && rows.nitems)
+    e = np == 1   ? launch_rows<1>(mK, mV, a, rows, tile, s)
+        : np == 2 ? launch_rows<2>(mK, mV, a, rows, tile, s)
+        : np == 3 ? launch_rows<3>(mK, mV, a, rows, tile, s)
+                  : launch_rows<4>(mK, mV, a, rows, tile, s);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("pt_attn_decode: launch failed: %s", cudaGetErrorString(e));

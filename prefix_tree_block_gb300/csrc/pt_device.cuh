@@ -303,6 +303,10 @@ __device__ __forceinline__ void tmem_st16_zero(uint32_t taddr) {
 // preceding kernel still uses); without the attribute it returns at once.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel of the stream be launched (its CTAs take the places that
+// this grid's leave); it still waits, in pdl_wait, for this grid to end.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Named barrier over `count` threads (ids other than 0, which __syncthreads uses).
 __device__ __forceinline__ void named_bar_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
