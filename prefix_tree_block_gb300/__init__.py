@@ -61,6 +61,8 @@ class PTError(RuntimeError):
 def load_library(path: Optional[str] = None):
     """Load libpt.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -582,25 +584,50 @@ def fold_plan(node_lengths, path_ptr, path_nodes, row_len: int, stream=None) -> 
     return FoldPlan(node_lengths, path_ptr, path_nodes, row_len, stream)
 
 
-def _need(t, name: str, dtype, shape=None, device=None):
-    """Check one tensor of the cache calls: on the current device, of this
-    dtype, dense, and of this shape where one is given."""
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+# The calls below run once per layer and step, next to kernels of a few
+# microseconds, so their Python side is kept short: one attribute or method of
+# a tensor costs about 0.1 us here, an allocation 1.5 us.
+_T = None  # torch, its int32, int64, float32 and bfloat16, and two queries of its CUDA state
+
+
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            raw = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
+        _T = torch, torch.int32, torch.int64, torch.float32, torch.bfloat16, raw
+    return _T
+
+
+def _bad(t, name: str, dtype, dev):
+    """Raise for a tensor of the cache calls that is not dense, of this dtype
+    and on the current device."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA tensor of {dtype}")
-    if shape is not None and t.shape != shape:
+    raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
+
+
+def _need(t, name: str, dtype, shape, dev):
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, name, dtype, dev)
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {device}")
 
 
-def _launch_stream(stream, *held):
+def _out(shape, dtype, like):
+    return _T[0].empty(shape, dtype=dtype, device=like.device) if _alloc_hook is None else \
+        _alloc_hook(tuple(shape), dtype, like.device)
+
+
+def _launch_stream(stream, dev, *held):
     """The raw stream of a call.  On a stream of the caller's choice, the
     tensors allocated here (`held`) are marked as used on it."""
-    import torch
-
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if isinstance(stream, torch.cuda.Stream):
+        return _T[5](dev)
+    if isinstance(stream, _T[0].cuda.Stream):
         for t in held:
             t.record_stream(stream)
     return int(stream.cuda_stream)
@@ -613,70 +640,76 @@ def cache_tables(held, added, tables, ring, counters, page_size: int, max_new: i
     [n, max_pages] and ring [cap]; counters int64 [2].  tables and ring change
     in place; returns new lens [n], counters [2], row_ptr [n + 1], and the
     added tokens' slots and position ids (int64 [max_new])."""
-    import torch
-
-    i32, i64 = torch.int32, torch.int64
+    torch, i32, i64, _, _, _ = _torch()
     dev = torch.cuda.current_device()
-    n = held.numel()
-    _need(held, "held", i32, (n,), dev)
-    _need(added, "added", i32, (n,), dev)
-    _need(ring, "ring", i32, (ring.numel(),), dev)
+    n, cap = held.numel(), ring.numel()
+    row = (n,)
+    _need(held, "held", i32, row, dev)
+    _need(added, "added", i32, row, dev)
+    _need(ring, "ring", i32, (cap,), dev)
     _need(counters, "counters", i64, (2,), dev)
-    _need(tables, "tables", i32, None, dev)
-    if tables.dim() != 2 or tables.shape[0] != n:
+    if tables.dim() != 2:
         raise ValueError(f"tables has shape {tuple(tables.shape)}, ({n}, max_pages) expected")
+    width = tables.shape[1]
+    _need(tables, "tables", i32, (n, width), dev)
     if start is not None:
-        _need(start, "start", i32, (n,), dev)
+        _need(start, "start", i32, row, dev)
     if not 0 <= max_new <= 1 << 30:
         raise ValueError(f"max_new = {max_new} is out of range")
-    d = held.device
-    lens, row_ptr = _empty((n,), i32, d), _empty((n + 1,), i32, d)
-    slots, positions = _empty((max_new,), i64, d), _empty((max_new,), i64, d)
-    out = _empty((2,), i64, d)
-    _check(load_library().pt_cache_tables(
-        held.data_ptr(), added.data_ptr(), start.data_ptr() if start is not None else None, n, page_size,
-        tables.data_ptr(), tables.shape[1], ring.data_ptr(), ring.numel(), counters.data_ptr(), lens.data_ptr(),
-        row_ptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), max_new, out.data_ptr(),
-        _launch_stream(stream, lens, row_ptr, slots, positions, out)))
+    lens, row_ptr = _out(row, i32, held), _out((n + 1,), i32, held)
+    slots, positions, out = _out((max_new,), i64, held), _out((max_new,), i64, held), _out((2,), i64, held)
+    rc = load_library().pt_cache_tables(
+        held.data_ptr(), added.data_ptr(), None if start is None else start.data_ptr(), n, page_size,
+        tables.data_ptr(), width, ring.data_ptr(), cap, counters.data_ptr(), lens.data_ptr(), row_ptr.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), max_new, out.data_ptr(),
+        _launch_stream(stream, dev, lens, row_ptr, slots, positions, out))
+    if rc:
+        _check(rc)
     return lens, out, row_ptr, slots, positions
 
 
 def _cache_shape(Kc, Vc, dtype, dev):
-    _need(Kc, "Kc", dtype, None, dev)
-    _need(Vc, "Vc", dtype, Kc.shape, dev)
-    if Kc.dim() != 4:
+    """(code of the dtype, cache shape)."""
+    code = PT_BF16 if dtype == _T[4] else PT_F32 if dtype == _T[3] else None
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    shape = Kc.shape
+    if len(shape) != 4:
         raise ValueError("Kc and Vc are [n_pages, Hkv, page_size, D]")
-    return Kc.shape
+    if Kc.dtype != dtype or Kc.get_device() != dev or not Kc.is_contiguous():
+        _bad(Kc, "Kc", dtype, dev)
+    _need(Vc, "Vc", dtype, shape, dev)
+    return code, shape
 
 
-def _token_rows(t, name, dtype, heads, D, dev):
+def _token_rows(t, name, dtype, T, heads, D, dev):
     """[T, heads, D] tokens whose heads are dense (a slice of a fused
     projection will do); returns the elements between tokens."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.get_device() != dev:
+    if t.dtype != dtype or t.get_device() != dev:
         raise TypeError(f"{name} must be a CUDA tensor [T, heads, head_dim] of {dtype} on the current device")
-    if t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, (T, {heads}, {D}) expected")
-    st = t.stride()
-    if t.numel() and ((D > 1 and st[2] != 1) or (heads > 1 and st[1] != D) or (t.shape[0] > 1 and st[0] < heads * D)):
-        raise ValueError(f"{name}: the heads of a token must be dense and tokens must not overlap")
-    return st[0] if t.shape[0] > 1 else heads * D
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, ({T}, {heads}, {D}) expected")
+    s, h, d = t.stride()
+    if (d != 1 and D > 1) or (h != D and heads > 1) or (s < heads * D and T > 1):
+        if T and heads and D:
+            raise ValueError(f"{name}: the heads of a token must be dense and tokens must not overlap")
+    return s if T > 1 else heads * D
 
 
 def cache_write(K, V, slots, Kc, Vc, stream=None) -> None:
     """Put tokens' K and V [T, Hkv, D] into their slots (int64 [T], negative:
     passed over) of the cache Kc, Vc [n_pages, Hkv, page_size, D], in place."""
-    import torch
-
+    torch, _, i64, _, _, _ = _torch()
     dev = torch.cuda.current_device()
-    n_pages, Hkv, ps, D = _cache_shape(Kc, Vc, K.dtype, dev)
-    code = _dtype_code(K)
-    ks, vs = _token_rows(K, "K", K.dtype, Hkv, D, dev), _token_rows(V, "V", K.dtype, Hkv, D, dev)
+    dtype = K.dtype
+    code, (n_pages, Hkv, ps, D) = _cache_shape(Kc, Vc, dtype, dev)
     T = K.shape[0]
-    if V.shape[0] != T:
-        raise ValueError(f"K has {T} tokens, V {V.shape[0]}")
-    _need(slots, "slots", torch.int64, (T,), dev)
-    _check(load_library().pt_cache_write(K.data_ptr(), V.data_ptr(), ks, vs, code, T, Hkv, D, slots.data_ptr(),
-                                         Kc.data_ptr(), Vc.data_ptr(), n_pages, ps, _launch_stream(stream)))
+    ks, vs = _token_rows(K, "K", dtype, T, Hkv, D, dev), _token_rows(V, "V", dtype, T, Hkv, D, dev)
+    _need(slots, "slots", i64, (T,), dev)
+    rc = load_library().pt_cache_write(K.data_ptr(), V.data_ptr(), ks, vs, code, T, Hkv, D, slots.data_ptr(),
+                                       Kc.data_ptr(), Vc.data_ptr(), n_pages, ps, _launch_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 class DecodePlan:
@@ -699,6 +732,7 @@ class DecodePlan:
                                         ctypes.c_void_p(_stream(stream)), ctypes.byref(out)))
         self._h = out
         self.n_nodes, self.n_samples, self.Hq, self.Hkv, self.q_len = n_nodes, int(pp.size - 1), Hq, Hkv, q_len
+        self.n_rows = self.n_samples * q_len  # query tokens of a call
 
     @property
     def handle(self):
@@ -731,42 +765,42 @@ def attn_decode(Q, Kc, Vc, tables, lens, plan: DecodePlan, q_count=None, scale: 
     the samples' newest tokens Q over the cache Kc, Vc [n_pages, Hkv,
     page_size, D], tables [n_nodes, max_pages], lens [n_nodes] (pt_attn_decode).
     With q_count, rows behind a sample's queries keep what O and LSE held."""
-    import torch
-
+    torch, i32, _, f32, _, _ = _torch()
     dev = torch.cuda.current_device()
-    n_pages, Hkv, ps, D = _cache_shape(Kc, Vc, Q.dtype, dev)
-    code = _dtype_code(Q)
-    T = plan.n_samples * plan.q_len
+    dtype = Q.dtype
+    code, (n_pages, Hkv, ps, D) = _cache_shape(Kc, Vc, dtype, dev)
+    T, Hq, N = plan.n_rows, plan.Hq, plan.n_nodes
     if Hkv != plan.Hkv:
         raise ValueError(f"the cache has {Hkv} kv heads, the plan {plan.Hkv}")
-    qs = _token_rows(Q, "Q", Q.dtype, plan.Hq, D, dev)
-    if Q.shape[0] != T:
-        raise ValueError(f"Q has {Q.shape[0]} tokens, the plan {T}")
-    _need(tables, "tables", torch.int32, None, dev)
-    if tables.dim() != 2 or tables.shape[0] != plan.n_nodes:
-        raise ValueError(f"tables has shape {tuple(tables.shape)}, ({plan.n_nodes}, max_pages) expected")
-    _need(lens, "lens", torch.int32, (plan.n_nodes,), dev)
+    qs = _token_rows(Q, "Q", dtype, T, Hq, D, dev)
+    if tables.dim() != 2:
+        raise ValueError(f"tables has shape {tuple(tables.shape)}, ({N}, max_pages) expected")
+    width = tables.shape[1]
+    _need(tables, "tables", i32, (N, width), dev)
+    _need(lens, "lens", i32, (N,), dev)
     if q_count is not None:
-        _need(q_count, "q_count", torch.int32, (plan.n_samples,), dev)
+        _need(q_count, "q_count", i32, (plan.n_samples,), dev)
     held = []
     if O is None:
-        O = _empty((T, plan.Hq, D), Q.dtype, Q.device)
+        O = _out((T, Hq, D), dtype, Q)
         held.append(O)
     else:
-        _need(O, "O", Q.dtype, (T, plan.Hq, D), dev)
+        _need(O, "O", dtype, (T, Hq, D), dev)
     if LSE is None:
-        LSE = _empty((plan.Hq, T), torch.float32, Q.device)
+        LSE = _out((Hq, T), f32, Q)
         held.append(LSE)
     else:
-        _need(LSE, "LSE", torch.float32, (plan.Hq, T), dev)
+        _need(LSE, "LSE", f32, (Hq, T), dev)
     if workspace is None:
-        workspace = _empty((plan.workspace_bytes(D),), torch.uint8, Q.device)
+        workspace = _out((plan.workspace_bytes(D),), torch.uint8, Q)
         held.append(workspace)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != dev:
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor on the current device")
-    _check(load_library().pt_attn_decode(
-        Q.data_ptr(), qs, Kc.data_ptr(), Vc.data_ptr(), code, D, n_pages, ps, tables.data_ptr(), tables.shape[1],
-        lens.data_ptr(), q_count.data_ptr() if q_count is not None else None, scale, plan.handle, O.data_ptr(),
+    rc = load_library().pt_attn_decode(
+        Q.data_ptr(), qs, Kc.data_ptr(), Vc.data_ptr(), code, D, n_pages, ps, tables.data_ptr(), width,
+        lens.data_ptr(), None if q_count is None else q_count.data_ptr(), scale, plan.handle, O.data_ptr(),
         LSE.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _launch_stream(stream, *held)))
+        _launch_stream(stream, dev, *held))
+    if rc:
+        _check(rc)
     return O, LSE

@@ -55,7 +55,7 @@ template <class E, int DL, int VEC>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {
   pdl_wait();
   extern __shared__ int chunk[];
-  dec_scan(a, c, kSimt, chunk, nullptr, false);
+  dec_scan(a, c, c, kSimt, kSimt, chunk, nullptr, nullptr);
   const int per = dec_share(chunk[(c.nseg + 31) >> 5], a.workers, a.min_units);
   if (blockIdx.x == gridDim.x - 1) dec_publish(a, c, kSimt, chunk, per);
   const int lane = threadIdx.x & 31;
@@ -219,34 +219,30 @@ struct MergeAcc {
   int turn;  // pieces so far, modulo the warps
 };
 
-// The pieces of up to 32 path entries (lane i: node, member index) in one class.
+// The pieces of up to 32 path entries in one class (lane i: node, its segment
+// and length, the sample's place among the node's).
 template <int VEC, int NV, int GH, int W>
-__device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int node, int mem, bool have, int j, int hk,
-                                            int h0, int warp, int lane, MergeAcc<VEC, NV, GH>& s) {
+__device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int node, const DecSeg& sg, int raw, int mem,
+                                            int j, int hk, int h0, int warp, int lane, MergeAcc<VEC, NV, GH>& s) {
   using V = VecOf<float, VEC>;
   const DecArgs& a = m.d;
-  const DecSeg* seg = tile ? m.c1.seg : m.c0.seg;
   const int* pref = tile ? m.c1.pref : m.c0.pref;
   const float* lse = tile ? m.c1.lse : m.c0.lse;
   const float* opart = tile ? m.c1.opart : m.c0.opart;
   const int rl = tile ? kTile.r : m.g0.r, bl = tile ? kTile.t : m.g0.t;
   int count = 0, two = 0;
   int row0 = 0;  // the row in the first piece, over all slots
-  if (have) {
-    const DecSeg sg = load_seg(seg + node);
-    const int raw = a.lens[node];
+  if (sg.rows_kind) {
     const int before = pref[node], per = pref[m.c0.nseg];
-    if (sg.rows_kind) {
-      int b, e;
-      dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
-      const int tiles = (e - b + (1 << bl) - 1) >> bl;
-      if (tiles > 0) {
-        const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
-        two = tile && sg.rows() - (rt << rl) <= kTileR / 2;
-        const unsigned u0 = before + it * tiles, w0 = u0 / (unsigned)per, w1 = (u0 + tiles - 1) / (unsigned)per;
-        row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
-        count = (int)(w1 - w0 + 1) << two;
-      }
+    int b, e;
+    dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
+    const int tiles = (e - b + (1 << bl) - 1) >> bl;
+    if (tiles > 0) {
+      const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
+      two = tile && sg.rows() - (rt << rl) <= kTileR / 2;
+      const unsigned u0 = before + it * tiles, w0 = u0 / (unsigned)per, w1 = (u0 + tiles - 1) / (unsigned)per;
+      row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
+      count = (int)(w1 - w0 + 1) << two;
     }
   }
   int incl = count;
@@ -301,21 +297,41 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
 
 template <class E, int VEC, int NV, int GH, int W>
 __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
-  pdl_wait();
   __shared__ float sm_m[W][GH], sm_l[W][GH];
   __shared__ VecOf<float, VEC> sm_o[W == 1 ? 1 : W][W == 1 ? 1 : GH][W == 1 ? 1 : NV * 32];
   const DecArgs& a = m.d;
   const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
   const int unit = W == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  if (unit >= m.units) return;
+  if (unit >= m.units) {
+    pdl_wait();  // (so that the grid does not end before the one before it)
+    return;
+  }
   const int groups = a.Hq / GH, tok = unit / groups, head = (unit - tok * groups) * GH;
   const int s = a.q_len > 1 ? tok / a.q_len : tok, j = tok - s * a.q_len, hk = head / a.g, h0 = head - hk * a.g;
+  // What the kernels before do not write is read while they end: they were
+  // launched after all that came before them had ended.
   const int k0 = m.path_ptr[s], k1 = m.path_ptr[s + 1];
+  int2 en = make_int2(0, 0);
+  DecSeg sg[2] = {DecSeg{0, 0, 0, -1}, DecSeg{0, 0, 0, -1}};
+  int raw = 0;
+  auto look = [&](int k) {
+    sg[0].rows_kind = sg[1].rows_kind = 0;
+    if (k + lane < k1) {
+      en = m.path_ent[k + lane];
+      raw = a.lens[en.x];
+      if (m.c0.nitems) sg[0] = load_seg(m.c0.seg + en.x);
+      if (m.c1.nitems) sg[1] = load_seg(m.c1.seg + en.x);
+    }
+  };
+  look(k0);
+  bool idle = false;
   if (a.q_count) {
     const int n = a.q_count[s];
     if ((n < 0 || n > a.q_len) && lane == 0) record_status(PT_STATUS_INVALID);
-    if (j >= dec_count(a, s)) return;  // the row stays as it was
+    idle = j >= dec_count(a, s);  // the row stays as it was
   }
+  pdl_wait();
+  if (idle) return;
   MergeAcc<VEC, NV, GH> r;
   r.turn = 0;
 #pragma unroll
@@ -325,12 +341,13 @@ __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
     for (int i = 0; i < NV * VEC; ++i) r.acc[h][i] = 0.f;
   }
 #pragma unroll 1
-  for (int k = k0; k < k1; k += 32) {
-    const bool have = k + lane < k1;
-    const int2 en = have ? m.path_ent[k + lane] : make_int2(0, 0);
+  for (int k = k0;;) {
 #pragma unroll 1
     for (int cls = m.c0.nitems ? 0 : 1; cls < (m.c1.nitems ? 2 : 1); ++cls)
-      merge_class<VEC, NV, GH, W>(m, cls == 1, en.x, en.y, have, j, hk, h0, warp, lane, r);
+      merge_class<VEC, NV, GH, W>(m, cls == 1, en.x, cls ? sg[1] : sg[0], raw, en.y, j, hk, h0, warp, lane, r);
+    k += 32;
+    if (k >= k1) break;
+    look(k);
   }
   using V = VecOf<float, VEC>;
   using VE = VecOf<E, VEC>;
@@ -436,15 +453,17 @@ DecClass class_args(const pt_decodeplan* p, int cls, int D, char*& ws) {
   return d;
 }
 
-// Whether a tensor-core call at this head_dim splits the nodes between the two kernels.
-bool use_tiles(const pt_decodeplan* p, int D) { return D <= kTileMaxD && p->cls[kDecTile].nitems > 0; }
+// Whether a tensor-core call splits the nodes between the two kernels: never at
+// this head_dim, or by the tokens of a full table row.
+bool may_tile(const pt_decodeplan* p, int D) { return D <= kTileMaxD && p->cls[kDecTile].nitems > 0; }
+bool use_tiles(const pt_decodeplan* p, int D, int cap) {
+  return may_tile(p, D) && p->tile_gain * (float)cap / 128.f >= kTileMinGain;
+}
 
 size_t ws_bytes(const pt_decodeplan* p, int D) {
   size_t n = std::max(class_bytes(p, kDecSimt, D), (size_t)256);
-  if (use_tiles(p, D))
-    n = std::max(n, class_bytes(p, kDecRowsFew, D) + class_bytes(p, kDecTile, D));
-  else if (D <= 256)
-    n = std::max(n, class_bytes(p, kDecRows, D));
+  if (may_tile(p, D)) n = std::max(n, class_bytes(p, kDecRowsFew, D) + class_bytes(p, kDecTile, D));
+  if (D <= 256) n = std::max(n, class_bytes(p, kDecRows, D));
   return n;
 }
 
@@ -561,6 +580,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
   // each class's share of the nodes
   std::vector<DecSeg> seg[kDecClasses];
   long long items[kDecClasses] = {0, 0, 0, 0};
+  double tile_gain = 0.0;
   for (int i = 0; i < N; ++i) {
     const int n = np[i + 1] - np[i];
     const long long rows = (long long)n * q_len * g;
@@ -569,6 +589,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
       const bool mixed = is_leaf[i] && q_len > 1;
       kind[kDecTile] = mixed ? kSegBody : kSegFull;
       kind[kDecRowsFew] = mixed ? kSegTail : -1;
+      tile_gain += Hkv * (0.9 * (double)((rows + 15) / 16) - 1.1 * (double)((rows + 127) / 128));
     }
     for (int c = 0; c < kDecClasses; ++c) {
       const int rk = n && kind[c] >= 0 ? (int)rows | kind[c] << 29 : 0;
@@ -604,7 +625,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
   p->device = dev;
   p->sms = num_sms(dev);
   p->stream = stream;
-  p->N = N, p->S = S, p->Hq = Hq, p->Hkv = Hkv, p->q_len = q_len;
+  p->N = N, p->S = S, p->Hq = Hq, p->Hkv = Hkv, p->q_len = q_len, p->tile_gain = (float)tile_gain;
   int rc = pool_alloc(&p->mem, host.size(), dev, stream);
   if (rc) {
     delete p;
@@ -699,7 +720,7 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   a.ps = page_size, a.max_pages = max_pages, a.n_pages = n_pages, a.cap = max_pages * page_size;
   a.scale_log2 = scale * 1.4426950408889634f;
   const bool tc = dtype == PT_BF16 && decode_tc_supported(D, page_size);
-  const bool tiles = tc && use_tiles(plan, D);
+  const bool tiles = tc && use_tiles(plan, D, max_pages * page_size);
   for (int c = 0; c < kDecClasses; ++c) {
     const bool used = c == kDecSimt ? !tc : c == kDecRows ? tc && !tiles : tiles;
     const int bt = c == kDecSimt ? kSimtBT : c == kDecTile ? kTileBT : kRowsBT;

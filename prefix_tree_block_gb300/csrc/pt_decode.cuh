@@ -47,8 +47,18 @@ constexpr DecTiling kTile = {8, 7};  // a CTA per worker; an item of up to 128 r
 constexpr int kSimtR = 1 << kSimt.r, kSimtBT = 1 << kSimt.t;
 constexpr int kRowsR = 1 << kRows.r, kRowsBT = 1 << kRows.t;
 constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
-constexpr int kTileMinRows = 65;             // rows of the nodes that go to the tile kernel
-constexpr int kTileMaxD = 128;               // and the head dims it takes
+// Which nodes the tile kernel takes, and when a call uses it: nodes that more
+// than 32 rows read (three row tiles of the other kernel, which reads a node
+// once for each), up to this head_dim, and only where that saves enough, since
+// both kernels then start later than the one alone.  128 tokens of an item take
+// an SM about 0.9 us for each tile of 16 rows, or 1.1 us for 128 rows and 2.2
+// for 256; kTileMinGain is in such us, over the tokens of a full table row.
+// Two prompts of 1024 tokens, 64 samples, 32 q heads over 8: 55 us on rows
+// alone, 36 with tiles; a depth-3 tree of 1024 + 512 tokens, 16 samples, 16 q
+// heads over 4: 16 and 20 us; two prompts of 4096 tokens, 16 samples, 32 over
+// 8: 39 and 40.
+constexpr int kTileMinRows = 33, kTileMaxD = 128;
+constexpr float kTileMinGain = 1500.f;
 // Element (row, column) of a tile-class partial result: groups of 8 columns, in
 // each the rows one after another (D is a multiple of 8 there).
 __host__ __device__ inline long long tile_at(int D, long long slot, int row, int col) {
@@ -185,33 +195,38 @@ __device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, De
   return ((sg.rows() + (1 << g.r) - 1) >> g.r) * a.Hkv * tiles;
 }
 
-// Exclusive sums of the class's units over chunks of 32 segments, in shared
-// memory (chunk[nc] = all of them); every thread of the block calls it.
-// cost (or NULL): a shared counter, zero before, that receives what the units
-// cost, kItemUnits for each item among it, and for `tiles` a second time those
-// of row tiles more than half full.
-__device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c, DecTiling g, int* chunk,
-                                         unsigned long long* cost, bool tile) {
+// Exclusive sums of the units over chunks of 32 segments, in shared memory
+// (chunk[nc] = all of them); every thread of the block calls it.  With cost, of
+// two classes, the tile class first; cost[i], zero before, then receives what
+// class i's units cost, kItemUnits for each item among it.
+__device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, const DecClass& c1, DecTiling g0,
+                                         DecTiling g1, int* chunk0, int* chunk1, unsigned long long* cost) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int nc = (c.nseg + 31) >> 5;
+  const int nc = (c0.nseg + 31) >> 5;
 #pragma unroll 1
   for (int k = warp; k < nc; k += nw) {
-    DecSeg sg;
-    int raw, tiles;
-    const int u = dec_units(a, c, g, k * 32 + lane, sg, raw, tiles);
-    if (blockIdx.x == 0 && (raw < 0 || raw > a.cap)) record_status(PT_STATUS_INVALID);
-    const int sum = __reduce_add_sync(0xffffffffu, u);
-    if (lane == 0) chunk[k] = sum;
-    if (cost) {
-      const int rt = (sg.rows() + (1 << g.r) - 1) >> g.r, last = sg.rows() - ((rt - 1) << g.r);
-      unsigned x = u ? (unsigned)(u + kItemUnits * rt * a.Hkv) : 0u;
-      if (tile) x += u - (last <= 1 << (g.r - 1) ? a.Hkv * tiles : 0);
-      const unsigned hi = __reduce_add_sync(0xffffffffu, x >> 16), lo = __reduce_add_sync(0xffffffffu, x & 0xffffu);
-      if (lane == 0) atomicAdd(cost, ((unsigned long long)hi << 16) + lo);
+#pragma unroll 1
+    for (int i = 0; i < (cost ? 2 : 1); ++i) {
+      DecSeg sg;
+      int raw, tiles;
+      const DecTiling g = {i ? g1.r : g0.r, i ? g1.t : g0.t};
+      const int u = dec_units(a, i ? c1 : c0, g, k * 32 + lane, sg, raw, tiles);
+      if (blockIdx.x == 0 && (raw < 0 || raw > a.cap)) record_status(PT_STATUS_INVALID);
+      const int sum = __reduce_add_sync(0xffffffffu, u);
+      if (lane == 0) (i ? chunk1 : chunk0)[k] = sum;
+      if (cost) {
+        const int rt = (sg.rows() + (1 << g.r) - 1) >> g.r, last = sg.rows() - ((rt - 1) << g.r);
+        // (rows: units; tiles: eighths of what a unit of 256 rows costs)
+        unsigned x = u ? (unsigned)((i ? u : 8 * u) + kItemUnits * rt * a.Hkv) : 0u;
+        if (i == 0 && last <= 1 << (g.r - 1)) x -= 3 * a.Hkv * tiles;
+        const unsigned hi = __reduce_add_sync(0xffffffffu, x >> 16), lo = __reduce_add_sync(0xffffffffu, x & 0xffffu);
+        if (lane == 0) atomicAdd(cost + i, ((unsigned long long)hi << 16) + lo);
+      }
     }
   }
   __syncthreads();
-  if (warp == 0) {
+  if (warp < (cost ? 2 : 1)) {
+    int* chunk = warp ? chunk1 : chunk0;
     int carry = 0;
 #pragma unroll 1
     for (int k0 = 0; k0 < nc; k0 += 32) {
@@ -319,6 +334,7 @@ struct pt_decodeplan {
   cudaStream_t stream;  // the build stream; memory goes back to the pool in its order
   void* mem;            // one pool allocation for every array below
   int32_t N, S, Hq, Hkv, q_len;
+  float tile_gain;      // what the tile kernel saves per 128 tokens of every node that it takes
   int32_t* member;
   struct Class {
     pt::DecSeg* seg;

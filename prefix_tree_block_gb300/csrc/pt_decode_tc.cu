@@ -66,9 +66,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // ---------------------------------------------------------------------------
 template <int NP>
 struct RowsCfg {
-  static constexpr int WARPS = 4;
-  static constexpr int CTAS = NP == 4 ? 1 : 2;  // per SM
-  static constexpr int STAGES = NP == 1 ? 6 : NP == 2 ? 3 : NP == 3 ? 2 : 3;
+  static constexpr int WARPS = NP == 4 ? 3 : 4;
+  static constexpr int CTAS = 2;  // per SM
+  static constexpr int STAGES = NP == 1 ? 6 : NP == 2 ? 3 : 2;
   static constexpr int PANEL = 16 * 128;            // bytes: 16 tokens x 64 columns
   static constexpr int STAGE = 2 * NP * PANEL;      // K panels, V panels
   static constexpr int RING = STAGES * STAGE;       // a warp's
@@ -90,10 +90,10 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
   const int lane = threadIdx.x & 31;
   const uint32_t ring_u = smem_u32(ring);
   DecWalk walk(a, c, kRows, chunk, worker, per);
-  // loads: the piece they are at, its first token and last page, and pages l_page0 + lane
+  // loads: the piece they are at, its last page, pages l_page0 + lane, and the next tile's page and row in it
   DecPiece lp;
   lp.t0 = lp.t1 = 0;
-  int l_base = 0, l_last = 0, l_page0 = 0, my_page = 0;
+  int l_last = 0, l_page0 = 0, l_page = 0, l_row = 0, my_page = 0;
   uint32_t issued = 0, used = 0, found = 0, at = 0;  // tiles; pieces
   // the current piece
   int t = 0, t1 = 0, kv_base = 0, rows_left = 0, lim_min = 0, lim_max = 0;
@@ -116,27 +116,40 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
         if (!walk.next(lp)) break;
         if (lane == 0) pieces[found % kRowsPieces] = lp;
         ++found;
-        int e;
-        dec_range(a, lp.kind, lp.len, l_base, e);
-        l_last = (min(e, l_base + lp.t1 * kRowsBT) - 1) / a.ps;
-        l_page0 = -64;
+        int b, e;
+        dec_range(a, lp.kind, lp.len, b, e);
+        const int kv0 = b + lp.t0 * kRowsBT;
+        l_last = (min(e, b + lp.t1 * kRowsBT) - 1) / a.ps;
+        l_page0 = kv0 / a.ps - 32, l_page = 32;  // (looked up below)
+        l_row = kv0 % a.ps;
       }
-      const int kv0 = l_base + lp.t0 * kRowsBT, pi = kv0 / a.ps;
-      if (pi >= l_page0 + 32) {
-        l_page0 = pi;
-        my_page = pi + lane <= l_last ? dec_page(a, lp.node, pi + lane) : 0;
+      if (l_page >= 32) {
+        l_page0 += l_page;
+        l_page = 0;
+        my_page = l_page0 + lane <= l_last ? dec_page(a, lp.node, l_page0 + lane) : 0;
       }
-      const int page = __shfl_sync(0xffffffffu, my_page, pi - l_page0);
+      const int page = __shfl_sync(0xffffffffu, my_page, l_page);
       const uint32_t s = issued % C::STAGES;
       if (lane == 0) {
         mbar_expect_tx(full + s, C::STAGE);
-        const int row = kv0 - pi * a.ps, ph = page * a.Hkv + lp.hk;
-#pragma unroll
-        for (int pn = 0; pn < NP; ++pn) {
-          tma_load_3d(ring + s * C::STAGE + pn * C::PANEL, &mK, full + s, pn * 64, row, ph);
-          tma_load_3d(ring + s * C::STAGE + (NP + pn) * C::PANEL, &mV, full + s, pn * 64, row, ph);
+        const int ph = page * a.Hkv + lp.hk;
+        uint8_t* dst = ring + s * C::STAGE;
+        if (NP == 1) {
+          tma_load_3d(dst, &mK, full + s, 0, l_row, ph);
+          tma_load_3d(dst + C::PANEL, &mV, full + s, 0, l_row, ph);
+        } else if (a.D == NP * 64) {  // all panels in one box
+          tma_load_4d(dst, &mK, full + s, 0, l_row, 0, ph);
+          tma_load_4d(dst + NP * C::PANEL, &mV, full + s, 0, l_row, 0, ph);
+        } else {
+#pragma unroll 1
+          for (int pn = 0; pn < NP; ++pn) {
+            tma_load_3d(dst + pn * C::PANEL, &mK, full + s, pn * 64, l_row, ph);
+            tma_load_3d(dst + (NP + pn) * C::PANEL, &mV, full + s, pn * 64, l_row, ph);
+          }
         }
       }
+      l_row += kRowsBT;
+      if (l_row == a.ps) l_row = 0, ++l_page;
       ++lp.t0;
       ++issued;
     }
@@ -326,16 +339,19 @@ struct DecSplit {
 template <int NP>
 __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& ct, const DecClass& cr, int* chunk_t,
                                               int* chunk_r, unsigned long long* cost, int sms, int rows_per_sm) {
-#pragma unroll 1
-  for (int i = ct.nitems ? 0 : 1; i < (cr.nitems ? 2 : 1); ++i)
-    dec_scan(a, i ? cr : ct, DecTiling{i ? kRows.r : kTile.r, i ? kRows.t : kTile.t}, i ? chunk_r : chunk_t, ct.nitems && cr.nitems ? cost + i : nullptr, i == 0);
+  const bool both = ct.nitems && cr.nitems;
+  if (both)
+    dec_scan(a, ct, cr, kTile, kRows, chunk_t, chunk_r, cost);
+  else
+    dec_scan(a, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t}, kRows,
+             ct.nitems ? chunk_t : chunk_r, chunk_r, nullptr);
   const int nc = (max(ct.nseg, cr.nseg) + 31) >> 5;
   const int units_t = ct.nitems ? chunk_t[nc] : 0, units_r = cr.nitems ? chunk_r[nc] : 0;
   DecSplit s;
   s.n_tile = units_t > 0 ? sms : 0;
   if (units_t > 0 && units_r > 0) {
-    // a tile unit of up to 128 rows costs an SM about as much as this many units of 16 rows and tokens
-    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f);
+    // a tile unit of 256 rows costs an SM about as much as 20 units of 16 rows and tokens (28 at head_dim 64)
+    const float x = (float)cost[0] * (NP == 1 ? 3.5f : 2.5f);
     s.n_tile = min(max((int)(sms * (x / (x + (float)cost[1]))), 1), sms - 1);
   }
   s.per_t = dec_share(units_t, max(s.n_tile, 1), kTileMinUnits);
@@ -361,16 +377,17 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
   int* chunk = reinterpret_cast<int*>(smem + C::OFF_CHUNK);
   volatile __shared__ int abort_flag;
   __shared__ unsigned long long cost[2];
+  if (threadIdx.x < C::WARPS * C::STAGES) {
+    mbar_init(bars + threadIdx.x, 1);
+    fence_mbar_init();
+  }
   if (threadIdx.x == 0) {
     abort_flag = 0;
     cost[0] = cost[1] = 0;
-#pragma unroll 1
-    for (int i = 0; i < C::WARPS * C::STAGES; ++i) mbar_init(bars + i, 1);
-    fence_mbar_init();
     prefetch_tmap(&mK);
     prefetch_tmap(&mV);
   }
-  __syncthreads();
+  if (beside) __syncthreads();  // (the costs; the scan's barriers publish the rest)
   const DecSplit sp = dec_split<NP>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::WARPS);
   if ((int)blockIdx.x == 0) dec_publish(a, c, kRows, chunk, sp.per_r);
   if ((int)blockIdx.x < (a.sms - sp.n_tile) * C::CTAS)
@@ -849,18 +866,21 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   if (warp == 9) tmem_dealloc(tbase, 512);
 }
 
-// Kc or Vc as a 3-D map (D, page_size, n_pages * Hkv), boxes of 64 columns x `rows` tokens, 128-byte swizzle.
-bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long long heads, int rows) {
+// Kc or Vc as a 3-D map (D, page_size, n_pages * Hkv) with boxes of 64 columns x
+// `rows` tokens, or with `panels` > 1 and D = 64 panels as a 4-D one (64,
+// page_size, panels, n_pages * Hkv) whose boxes hold every column; 128-byte swizzle.
+bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long long heads, int rows, int panels) {
   encode_tiled_fn enc = get_encode_tiled();
   if (!enc) {
     set_error("cuTensorMapEncodeTiled is unavailable from the driver");
     return false;
   }
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)ps, (cuuint64_t)heads};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ps * D * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+  const bool all = panels > 1 && D == panels * 64;
+  cuuint64_t dims[4] = {(cuuint64_t)(all ? 64 : D), (cuuint64_t)ps, (cuuint64_t)(all ? panels : heads), (cuuint64_t)heads};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)(all ? 128 : (size_t)ps * D * 2), (cuuint64_t)ps * D * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)(all ? panels : 1), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, all ? 4 : 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -906,13 +926,13 @@ int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const Dec
   CUtensorMap mK, mV, mKt, mVt;
   cudaError_t e = cudaSuccess;
   const int np = (a.D + 63) / 64;
-  if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, 16) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, 16))
+  if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, 16, np) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, 16, np))
     return PT_ERR_CUDA;
   a.sms = p->sms;
   ProfScope ps(s, tile.nitems ? "decode_tile" : "decode_rows");  // (two kernels that overlap have one scope)
   if (tile.nitems) {
     const int box = std::min(a.ps & -a.ps, kTileBT);  // the largest power of two that divides a page
-    if (!make_tmap_pages(&mKt, a.Kc, a.D, a.ps, heads, box) || !make_tmap_pages(&mVt, a.Vc, a.D, a.ps, heads, box))
+    if (!make_tmap_pages(&mKt, a.Kc, a.D, a.ps, heads, box, 1) || !make_tmap_pages(&mVt, a.Vc, a.D, a.ps, heads, box, 1))
       return PT_ERR_CUDA;
     e = np == 1 ? launch_tile<1>(mKt, mVt, a, tile, rows, box, (int)heads, s)
                 : launch_tile<2>(mKt, mVt, a, tile, rows, box, (int)heads, s);

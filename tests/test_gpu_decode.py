@@ -38,9 +38,9 @@ TREES = {
 }
 
 
-def _run(lens, paths, Hq, Hkv, D, dtype, ps, q_len=1, q_count=None, scale=0.0, seed=0, min_width=0, poison=float("nan")):
+def _run(lens, paths, Hq, Hkv, D, dtype, ps, q_len=1, q_count=None, scale=0.0, seed=0, width=None, poison=float("nan")):
     rng = np.random.default_rng(seed)
-    tables, n_pages = pages_of(lens, ps, rng)
+    tables, n_pages = pages_of(lens, ps, rng, width=width)
     Kc, Vc = cache_of(lens, tables, n_pages, Hkv, ps, D, dtype, seed, poison)
     g = torch.Generator().manual_seed(seed + 1)
     Q = torch.randn(len(paths) * q_len, Hq, D, generator=g).to(dtype)
@@ -63,6 +63,8 @@ def _run(lens, paths, Hq, Hkv, D, dtype, ps, q_len=1, q_count=None, scale=0.0, s
 def test_trees(tree, Hq, Hkv, D, dtype, ps):
     lens, paths = TREES[tree]
     _run(lens, paths, Hq, Hkv, D, dtype, ps, seed=3)
+    if dtype == BF:  # tables wide enough for nodes that many rows read to take the tile kernel
+        _run(lens, paths, Hq, Hkv, D, dtype, ps, seed=3, width=8192 // ps)
 
 
 @pytest.mark.parametrize("D,dtype", [(1, F32), (31, F32), (33, F32), (66, F32), (128, F32), (130, F32), (256, F32), (257, F32), (512, F32),
@@ -77,6 +79,8 @@ def test_head_dims(D, dtype):
 def test_page_sizes(ps, dtype):
     lens, paths = TREES["crowd"]
     _run(lens, paths, 4, 2, 64, dtype, ps, seed=ps)
+    if dtype == BF:
+        _run(lens, paths, 4, 2, 64, dtype, ps, seed=ps, width=-(-8192 // ps))
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 1), (32, 1), (71, 1), (8, 8), (7, 7), (24, 8), (40, 4)])
@@ -84,6 +88,8 @@ def test_page_sizes(ps, dtype):
 def test_head_layouts(Hq, Hkv, dtype):
     lens, paths = TREES["group"]
     _run(lens, paths, Hq, Hkv, 64, dtype, 16, seed=Hq)
+    if dtype == BF:
+        _run(lens, paths, Hq, Hkv, 64, dtype, 16, seed=Hq, width=512)
 
 
 @pytest.mark.parametrize("q_len", [2, 5, 16, 33])
@@ -93,6 +99,8 @@ def test_several_queries(q_len, tree, Hq, Hkv, D, dtype):
     """Rows of a leaf shorter than q_len keep nothing of it at first."""
     lens, paths = TREES[tree]
     _run(lens, paths, Hq, Hkv, D, dtype, 16, q_len=q_len, seed=q_len)
+    if dtype == BF:
+        _run(lens, paths, Hq, Hkv, D, dtype, 16, q_len=q_len, seed=q_len, width=512)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -100,7 +108,7 @@ def test_several_queries(q_len, tree, Hq, Hkv, D, dtype):
 def test_query_counts(dtype, q_len):
     """Samples with fewer queries than q_len, or none: their rows stay."""
     lens, paths = TREES["crowd"]
-    _run(lens, paths, 4, 2, 64, dtype, 16, q_len=q_len, q_count=[(i * 7) % (q_len + 1) for i in range(len(paths))], seed=2)
+    _run(lens, paths, 4, 2, 64, dtype, 16, q_len=q_len, q_count=[(i * 7) % (q_len + 1) for i in range(len(paths))], seed=2, width=512)
     lens, paths = TREES["deep"]
     _run(lens, paths, 4, 2, 64, dtype, 16, q_len=q_len, q_count=[0] * len(paths), seed=2)
 
@@ -111,6 +119,8 @@ def test_what_lies_behind_the_rows(dtype, poison):
     lens, paths = TREES["deep"]
     _run(lens, paths, 4, 2, 64, dtype, 16, seed=1, poison=poison)
     _run(lens, paths, 4, 2, 64, dtype, 16, q_len=3, seed=1, poison=poison)
+    lens, paths = TREES["wide"]
+    _run(lens, paths, 4, 2, 64, dtype, 16, seed=1, poison=poison)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -120,7 +130,7 @@ def test_a_later_drafts_nan_stays_with_it(dtype, Hq, what):
     """A token whose key or value is NaN reaches the queries that keep it only."""
     lens, paths, q_len, ps, D = [50, 40, 21], [[0, 1], [0, 2]], 6, 16, 64
     rng = np.random.default_rng(0)
-    tables, n_pages = pages_of(lens, ps, rng)
+    tables, n_pages = pages_of(lens, ps, rng, width=256)
     Kc, Vc = cache_of(lens, tables, n_pages, 2, ps, D, dtype, 0)
     s = OD.slots_of(tables[1], 40, ps)[37]  # the third draft token of sample 0
     (Kc if what == "K" else Vc)[s // ps, :, s % ps] = float("nan")
@@ -166,7 +176,7 @@ def test_query_rows_between_16_byte_boundaries(extra):
     """A node that many rows read, with query tokens of every alignment allowed."""
     lens, paths = TREES["crowd"]
     Hq, Hkv, D, ps = 4, 2, 64, 16
-    tables, n_pages = pages_of(lens, ps, np.random.default_rng(1))
+    tables, n_pages = pages_of(lens, ps, np.random.default_rng(1), width=512)
     Kc, Vc = cache_of(lens, tables, n_pages, Hkv, ps, D, BF, 1)
     x = torch.randn(len(paths), Hq * D + extra, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
     Q = x.as_strided((len(paths), Hq, D), (Hq * D + extra, D, 1), extra)
@@ -213,7 +223,7 @@ def test_many_nodes():
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_same_result_each_time(dtype):
-    lens, paths = [3000] + [50 + i for i in range(20)], [[0, i] for i in range(1, 21)]
+    lens, paths = [3000] + [50 + i for i in range(20)], [[0, i] for i in range(1, 21)]  # (the prompt: 140 rows)
     tables, n_pages = pages_of(lens, 16, np.random.default_rng(1))
     Kc, Vc = (c.cuda() for c in cache_of(lens, tables, n_pages, 2, 16, 64, dtype, 1))
     Q = torch.randn(20, 14, 64, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
