@@ -506,9 +506,9 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   workspace: at least pt_decode_workspace_bytes(plan, D) bytes, 256-byte
  *   aligned; its contents do not matter before or after.  Calls that share
  *   one must not overlap on the GPU.  The result does not vary between runs.
- *   PT_BF16 with D a multiple of 8 up to 256 and page_size a multiple of 16
- *   runs on tensor cores; other D (multiples of 8 in bf16) up to 512, other
- *   page sizes and PT_F32 on CUDA cores.
+ *   PT_BF16 with D a multiple of 8 up to 512 and page_size a multiple of 16
+ *   runs on tensor cores; other page sizes and PT_F32 (any D up to 512) on
+ *   CUDA cores.
  *   Errors: PT_ERR_INVALID_ARG and PT_ERR_UNSUPPORTED as for pt_attn_fwd,
  *   and for a workspace that is too small, a plan of another device or a bad
  *   stride.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a length

@@ -463,7 +463,7 @@ bool use_tiles(const pt_decodeplan* p, int D, int cap) {
 size_t ws_bytes(const pt_decodeplan* p, int D) {
   size_t n = std::max(class_bytes(p, kDecSimt, D), (size_t)256);
   if (may_tile(p, D)) n = std::max(n, class_bytes(p, kDecRowsFew, D) + class_bytes(p, kDecTile, D));
-  if (D <= 256) n = std::max(n, class_bytes(p, kDecRows, D));
+  n = std::max(n, class_bytes(p, kDecRows, D));
   return n;
 }
 

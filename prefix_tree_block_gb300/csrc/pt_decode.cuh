@@ -349,7 +349,7 @@ namespace pt {
 bool decode_tc_supported(int D, int ps);
 int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile, cudaStream_t s);
 int take_status_decode_tc(cudaStream_t s);
-constexpr int kRowsWarps = 8;
+constexpr int kRowsWarps = 12;  // workers of the rows kernel per SM, at most
 inline int dec_workers(const pt_decodeplan* p, int cls) {
   return cls == kDecSimt ? p->sms * 16 : cls == kDecTile ? p->sms : p->sms * kRowsWarps;
 }

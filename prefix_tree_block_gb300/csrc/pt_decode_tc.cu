@@ -1,5 +1,5 @@
 // pt_decode_tc.cu -- tensor-core kernels of the decoding attention (bf16,
-// head dims up to 256, pages of a multiple of 16 tokens).
+// head dims up to 512, pages of a multiple of 16 tokens).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -48,46 +48,55 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // ---------------------------------------------------------------------------
-// Segments of up to a few rows per kv head: a warp per worker, 16 query rows,
-// 16 tokens a step.
+// Segments of up to a few rows per kv head: 16 query rows and 16 tokens a step,
+// a warp per worker; at head dims over 128, SPLIT = 2 or 4 warps, 128 columns
+// each.
 //
 // A step's work is 32 NP mma for 16 x 128 NP bytes of keys and values: the
 // kernel is bound by memory, and what matters is that every SM keeps enough
-// bytes in flight and that no warp waits for another.  So each warp has its
-// own ring of stages (16 tokens of K and V, 64-column panels, 128-byte
-// swizzle), fills it by TMA itself (a box is 16 tokens of one page and one
-// panel) and computes on what has arrived; nothing is shared between warps.
-// The loads run up to a ring ahead of the arithmetic, across the ends of
-// pieces: a second walk along the worker's units issues them.
+// bytes in flight (more than that only queue: three stages a warp instead of
+// two cost 4% at head_dim 128) and that no warp waits for another.  So each
+// warp has its own ring of stages (16 tokens of K and V, 64-column panels,
+// 128-byte swizzle), fills it by TMA itself (a box is 16 tokens of one page)
+// and computes on what has arrived; nothing but the walk's sums is shared.  The
+// loads run up to a ring ahead of the arithmetic, across the ends of pieces.
 //   S = Q K^T: Q's fragments stay in registers, K's come by ldmatrix.
 //   O += P V: P is the bf16 of S's own registers (the accumulator's layout is
 //   the A operand's), V's fragments come by ldmatrix.trans.
-// The running maximum is followed in steps of 2^8, as in the forward.
+// The warps of a SPLIT worker add up their parts of S through shared memory,
+// each in the same order, and then hold the same P; O's columns stay apart.
+// (16384 units at head_dim 256, 268 MB: 51 us; 60 with one warp for all columns,
+// which has to spill.)  The running maximum is followed in steps of 2^8, as in the forward.
 // ---------------------------------------------------------------------------
-template <int NP>
+template <int NP, int SPLIT>
 struct RowsCfg {
-  static constexpr int WARPS = NP == 4 ? 3 : 4;
-  static constexpr int CTAS = 2;  // per SM
-  static constexpr int STAGES = NP == 1 ? 6 : NP == 2 ? 3 : 2;
+  static constexpr int WARPS = 4, GROUPS = WARPS / SPLIT;  // GROUPS workers a CTA
+  static constexpr int CTAS = NP == 1 ? 3 : 2;             // per SM
+  static constexpr int STAGES = NP == 1 ? 4 : 2;
   static constexpr int PANEL = 16 * 128;            // bytes: 16 tokens x 64 columns
   static constexpr int STAGE = 2 * NP * PANEL;      // K panels, V panels
   static constexpr int RING = STAGES * STAGE;       // a warp's
-  static constexpr int OFF_BAR = WARPS * RING;
-  static constexpr int OFF_PIECE = OFF_BAR + WARPS * STAGES * 8;
+  static constexpr int OFF_X = WARPS * RING;        // parts of S: two of 1 KB a warp
+  static constexpr int OFF_BAR = OFF_X + (SPLIT > 1 ? WARPS * 2048 : 0);
+  static constexpr int NBAR = WARPS * STAGES + (SPLIT > 1 ? GROUPS : 0);
+  static constexpr int OFF_PIECE = OFF_BAR + NBAR * 8;
   static constexpr int OFF_CHUNK = OFF_PIECE + WARPS * 8 * (int)sizeof(DecPiece);
   static constexpr size_t smem(int nseg) { return OFF_CHUNK + 8 * ((size_t)(nseg + 31) / 32 + 1) + 1024; }
 };
 
-// One worker: a warp, with its ring (1024-byte aligned), its barriers
-// (initialised for one arrival) and room for kRowsPieces pieces.
+// One warp of a worker (the sw-th of SPLIT): its ring (1024-byte aligned), its
+// barriers (initialised for one arrival), room for kRowsPieces pieces, and of
+// the worker the room for S's parts and its barrier (SPLIT arrivals).
 constexpr int kRowsPieces = 8;
-template <int NP>
+template <int NP, int SPLIT>
 __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a,
-                                            const DecClass& c, const int* chunk, int per, int worker,
-                                            uint8_t* ring, uint64_t* full, DecPiece* pieces, volatile int* abort_flag) {
-  using C = RowsCfg<NP>;
+                                            const DecClass& c, const int* chunk, int per, int worker, int sw,
+                                            uint8_t* ring, uint64_t* full, DecPiece* pieces, float4* xbuf,
+                                            uint64_t* xbar, volatile int* abort_flag) {
+  using C = RowsCfg<NP, SPLIT>;
   static_assert(C::STAGES + 1 < kRowsPieces, "a piece per stage in flight, and the current one");
   const int lane = threadIdx.x & 31;
+  const int col0 = SPLIT == 1 ? 0 : sw * 128;  // this warp's first column
   const uint32_t ring_u = smem_u32(ring);
   DecWalk walk(a, c, kRows, chunk, worker, per);
   // loads: the piece they are at, its last page, pages l_page0 + lane, and the next tile's page and row in it
@@ -137,14 +146,14 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
         if (NP == 1) {
           tma_load_3d(dst, &mK, full + s, 0, l_row, ph);
           tma_load_3d(dst + C::PANEL, &mV, full + s, 0, l_row, ph);
-        } else if (a.D == NP * 64) {  // all panels in one box
-          tma_load_4d(dst, &mK, full + s, 0, l_row, 0, ph);
-          tma_load_4d(dst + NP * C::PANEL, &mV, full + s, 0, l_row, 0, ph);
+        } else if (a.D % 64 == 0) {  // both panels in one box (behind the last column: zeros)
+          tma_load_4d(dst, &mK, full + s, 0, l_row, col0 >> 6, ph);
+          tma_load_4d(dst + NP * C::PANEL, &mV, full + s, 0, l_row, col0 >> 6, ph);
         } else {
 #pragma unroll 1
           for (int pn = 0; pn < NP; ++pn) {
-            tma_load_3d(dst + pn * C::PANEL, &mK, full + s, pn * 64, l_row, ph);
-            tma_load_3d(dst + (NP + pn) * C::PANEL, &mV, full + s, pn * 64, l_row, ph);
+            tma_load_3d(dst + pn * C::PANEL, &mK, full + s, col0 + pn * 64, l_row, ph);
+            tma_load_3d(dst + (NP + pn) * C::PANEL, &mV, full + s, col0 + pn * 64, l_row, ph);
           }
         }
       }
@@ -177,7 +186,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
         }
 #pragma unroll
         for (int k = 0; k < NP * 4; ++k) {
-          const int col = k * 16 + c2;
+          const int col = col0 + k * 16 + c2;
           q[k][i] = src && col < a.D ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
           q[k][i + 2] = src && col + 8 < a.D ? *reinterpret_cast<const uint32_t*>(src + col + 8) : 0u;
         }
@@ -211,8 +220,33 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = sc[0][n][i] + sc[1][n][i];
+    if constexpr (SPLIT > 1) {
+      // (two buffers in turn: a warp that arrives here for a tile has read the parts of the one before)
+      float4* xb = xbuf + (used & 1) * (SPLIT * 64) + lane;
+      xb[sw * 64] = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+      xb[sw * 64 + 32] = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xbar);
+      ok = mbar_wait(xbar, used & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float4 sum = xb[n * 32];
+#pragma unroll
+        for (int w = 1; w < SPLIT; ++w) {
+          const float4 y = xb[w * 64 + n * 32];
+          sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+        }
+        x[n][0] = sum.x, x[n][1] = sum.y, x[n][2] = sum.z, x[n][3] = sum.w;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[n][i] = (sc[0][n][i] + sc[1][n][i]) * a.scale_log2;
+        x[n][i] *= a.scale_log2;
         if (kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1]) x[n][i] = -INFINITY;
       }
     bool grow = false;
@@ -315,14 +349,15 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       if (r_lo + i * 8 >= rows_left) continue;
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
       const long long row = (long long)slot * kRowsR + r_lo + i * 8;
-      if (c2 == 0) c.lse[row] = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
-      float* dst = c.opart + row * a.D + c2;
+      if (c2 == 0 && sw == 0) c.lse[row] = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+      float* dst = c.opart + row * a.D + col0 + c2;
 #pragma unroll
       for (int k = 0; k < NP * 8; ++k)
-        if (k * 8 < a.D) *reinterpret_cast<float2*>(dst + k * 8) = make_float2(o[k][2 * i] * inv, o[k][2 * i + 1] * inv);
+        if (col0 + k * 8 < a.D) *reinterpret_cast<float2*>(dst + k * 8) = make_float2(o[k][2 * i] * inv, o[k][2 * i + 1] * inv);
     }
   }
   if (!ok) {  // a wait ran out: let the copies in flight land before the block ends
+    *abort_flag = 1;
     for (; used < issued; ++used) mbar_wait_drain(full + used % C::STAGES, (used / C::STAGES) & 1, 20000000);
   }
 }
@@ -359,11 +394,11 @@ __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& 
   return s;
 }
 
-template <int NP>
-__global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
+template <int NP, int SPLIT>
+__global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SPLIT>::CTAS)
     k_decode_rows(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const DecArgs a,
                   const DecClass c, const DecClass ct) {
-  using C = RowsCfg<NP>;
+  using C = RowsCfg<NP, SPLIT>;
   // Beside a tile kernel this one starts when that one has begun (it has then
   // waited for what came before both), runs on the SMs that it leaves, and
   // ends after it, so that waiting for this kernel is waiting for both.
@@ -377,8 +412,8 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
   int* chunk = reinterpret_cast<int*>(smem + C::OFF_CHUNK);
   volatile __shared__ int abort_flag;
   __shared__ unsigned long long cost[2];
-  if (threadIdx.x < C::WARPS * C::STAGES) {
-    mbar_init(bars + threadIdx.x, 1);
+  if (threadIdx.x < C::NBAR) {
+    mbar_init(bars + threadIdx.x, threadIdx.x < C::WARPS * C::STAGES ? 1 : SPLIT);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) {
@@ -388,12 +423,14 @@ __global__ void __launch_bounds__(RowsCfg<NP>::WARPS * 32, RowsCfg<NP>::CTAS)
     prefetch_tmap(&mV);
   }
   if (beside) __syncthreads();  // (the costs; the scan's barriers publish the rest)
-  const DecSplit sp = dec_split<NP>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::WARPS);
+  const DecSplit sp = dec_split<NP>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::GROUPS);
   if ((int)blockIdx.x == 0) dec_publish(a, c, kRows, chunk, sp.per_r);
   if ((int)blockIdx.x < (a.sms - sp.n_tile) * C::CTAS)
-    rows_worker<NP>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::WARPS + warp, smem + warp * C::RING,
-                    bars + warp * C::STAGES, reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE) + warp * kRowsPieces,
-                    &abort_flag);
+    rows_worker<NP, SPLIT>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::GROUPS + warp / SPLIT, warp % SPLIT,
+                           smem + warp * C::RING, bars + warp * C::STAGES,
+                           reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE) + warp * kRowsPieces,
+                           reinterpret_cast<float4*>(smem + C::OFF_X) + (warp / SPLIT) * (SPLIT * 128),
+                           bars + C::WARPS * C::STAGES + warp / SPLIT, &abort_flag);
   if (beside) pdl_wait();
 }
 
@@ -867,18 +904,19 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
 }
 
 // Kc or Vc as a 3-D map (D, page_size, n_pages * Hkv) with boxes of 64 columns x
-// `rows` tokens, or with `panels` > 1 and D = 64 panels as a 4-D one (64,
-// page_size, panels, n_pages * Hkv) whose boxes hold every column; 128-byte swizzle.
-bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long long heads, int rows, int panels) {
+// `rows` tokens, or with `two` and D a multiple of 64 as a 4-D one (64,
+// page_size, D / 64, n_pages * Hkv) with boxes of 128 columns; 128-byte swizzle.
+bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long long heads, int rows, bool two) {
   encode_tiled_fn enc = get_encode_tiled();
   if (!enc) {
     set_error("cuTensorMapEncodeTiled is unavailable from the driver");
     return false;
   }
-  const bool all = panels > 1 && D == panels * 64;
+  const bool all = two && D % 64 == 0;
+  const int panels = D / 64;
   cuuint64_t dims[4] = {(cuuint64_t)(all ? 64 : D), (cuuint64_t)ps, (cuuint64_t)(all ? panels : heads), (cuuint64_t)heads};
   cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)(all ? 128 : (size_t)ps * D * 2), (cuuint64_t)ps * D * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)(all ? panels : 1), 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)(all ? 2 : 1), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, all ? 4 : 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -890,15 +928,17 @@ bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long lon
   return true;
 }
 
-template <int NP>
+template <int NP, int SPLIT>
 cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
                         const DecClass& ct, cudaStream_t s) {
-  using C = RowsCfg<NP>;
+  using C = RowsCfg<NP, SPLIT>;
+  static_assert(C::CTAS * C::GROUPS <= kRowsWarps, "the workspace's slots");
   const size_t smem = C::smem(c.nseg);
-  cudaError_t e = cudaFuncSetAttribute(k_decode_rows<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kernel = k_decode_rows<NP, SPLIT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(k_decode_rows<NP>, dim3(a.sms * C::CTAS), dim3(C::WARPS * 32), smem, s, mK, mV, a, c, ct);
+  return launch_pdl(kernel, dim3(a.sms * C::CTAS), dim3(C::WARPS * 32), smem, s, mK, mV, a, c, ct);
 }
 
 template <int NP>
@@ -910,12 +950,12 @@ cudaError_t launch_tile(const CUtensorMap& mK, const CUtensorMap& mV, const DecA
   if (e != cudaSuccess) return e;
   count_launch();
   return launch_pdl(k_decode_tile<NP>, dim3(a.sms), dim3(C::THREADS), smem, s, mK, mV, a, c, cr,
-                    RowsCfg<NP>::CTAS * RowsCfg<NP>::WARPS, box_rows, heads);
+                    RowsCfg<NP, 1>::CTAS * RowsCfg<NP, 1>::GROUPS, box_rows, heads);
 }
 
 }  // namespace
 
-bool decode_tc_supported(int D, int ps) { return D % 8 == 0 && D <= 256 && ps % 16 == 0; }
+bool decode_tc_supported(int D, int ps) { return D % 8 == 0 && D <= 512 && ps % 16 == 0; }
 
 int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile, cudaStream_t s) {
   const long long heads = (long long)a.n_pages * a.Hkv;
@@ -926,22 +966,22 @@ int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const Dec
   CUtensorMap mK, mV, mKt, mVt;
   cudaError_t e = cudaSuccess;
   const int np = (a.D + 63) / 64;
-  if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, 16, np) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, 16, np))
+  if (!make_tmap_pages(&mK, a.Kc, a.D, a.ps, heads, 16, np > 1) || !make_tmap_pages(&mV, a.Vc, a.D, a.ps, heads, 16, np > 1))
     return PT_ERR_CUDA;
   a.sms = p->sms;
   ProfScope ps(s, tile.nitems ? "decode_tile" : "decode_rows");  // (two kernels that overlap have one scope)
   if (tile.nitems) {
     const int box = std::min(a.ps & -a.ps, kTileBT);  // the largest power of two that divides a page
-    if (!make_tmap_pages(&mKt, a.Kc, a.D, a.ps, heads, box, 1) || !make_tmap_pages(&mVt, a.Vc, a.D, a.ps, heads, box, 1))
+    if (!make_tmap_pages(&mKt, a.Kc, a.D, a.ps, heads, box, false) || !make_tmap_pages(&mVt, a.Vc, a.D, a.ps, heads, box, false))
       return PT_ERR_CUDA;
     e = np == 1 ? launch_tile<1>(mKt, mVt, a, tile, rows, box, (int)heads, s)
                 : launch_tile<2>(mKt, mVt, a, tile, rows, box, (int)heads, s);
   }
   if (e == cudaSuccess && rows.nitems)
-    e = np == 1   ? launch_rows<1>(mK, mV, a, rows, tile, s)
-        : np == 2 ? launch_rows<2>(mK, mV, a, rows, tile, s)
-        : np == 3 ? launch_rows<3>(mK, mV, a, rows, tile, s)
-                  : launch_rows<4>(mK, mV, a, rows, tile, s);
+    e = a.D <= 64    ? launch_rows<1, 1>(mK, mV, a, rows, tile, s)
+        : a.D <= 128 ? launch_rows<2, 1>(mK, mV, a, rows, tile, s)
+        : a.D <= 256 ? launch_rows<2, 2>(mK, mV, a, rows, tile, s)
+                     : launch_rows<2, 4>(mK, mV, a, rows, tile, s);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("pt_attn_decode: launch failed: %s", cudaGetErrorString(e));
