@@ -40,7 +40,8 @@ struct alignas(sizeof(E) * V) VecOf {
 };
 
 // ---------------------------------------------------------------------------
-// CUDA cores: a warp per worker, kSimtR = 4 query rows, 8 tokens a step.
+// CUDA cores: a warp per worker, kSimtR = 4 query rows, 8 tokens a step (4 at
+// head dims over 128).
 //
 // Lanes hold the columns (DL each, VEC of them contiguous), so a token's key
 // is one coalesced load, and four keys against four rows leave 16 partial dot
@@ -60,6 +61,8 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
   if (blockIdx.x == gridDim.x - 1) dec_publish(a, c, kSimt, chunk, per);
   const int lane = threadIdx.x & 31;
   constexpr int R = kSimtR, NV = DL / VEC;
+  constexpr int STEP = DL <= 4 ? 8 : 4;  // tokens, as registers allow
+  constexpr bool EARLY = DL <= 4;        // and whether for their values beside their keys
   using V = VecOf<E, VEC>;
   const E* Qp = static_cast<const E*>(a.Q);
   DecWalk walk(a, c, kSimt, chunk, (int)blockIdx.x * 8 + (threadIdx.x >> 5), per);
@@ -92,35 +95,46 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       }
     }
     float m = -INFINITY, l = 0.f;  // of row my_r, the same on its eight lanes
+    const int end = min(min(b + p.t1 * kSimtBT, e), lim_max);
+    // lane i's row of the cache: token kv0 + i (past the last token: the last again, so that every load may be issued)
+    auto row_of = [&](int kv0) -> long long {
+      const int kv = min(kv0 + (lane & (STEP - 1)), end - 1), pi = kv / a.ps;
+      return (((long long)dec_page(a, p.node, pi) * a.Hkv + p.hk) * a.ps + (kv - pi * a.ps)) * a.D;
+    };
+    long long next = b + p.t0 * kSimtBT < end ? row_of(b + p.t0 * kSimtBT) : 0;
 #pragma unroll 1
-    for (int kv0 = b + p.t0 * kSimtBT, end = min(min(b + p.t1 * kSimtBT, e), lim_max); kv0 < end; kv0 += 8) {
-      // lane i's row of the cache: token kv0 + i (past the last token: the last again, so that every load may be issued)
-      long long off;
-      {
-        const int kv = min(kv0 + (lane & 7), end - 1), pi = kv / a.ps;
-        off = (((long long)dec_page(a, p.node, pi) * a.Hkv + p.hk) * a.ps + (kv - pi * a.ps)) * a.D;
-      }
-      float s[2];
+    for (int kv0 = b + p.t0 * kSimtBT; kv0 < end; kv0 += STEP) {
+      // this step's values are loaded with its keys, and the next step's pages are looked up now
+      const long long off = next;
+      V kk[STEP][NV], vv[EARLY ? STEP : 1][NV];
 #pragma unroll
-      for (int gq = 0; gq < 2; ++gq) {
+      for (int u = 0; u < STEP; ++u) {
+        const long long o = __shfl_sync(0xffffffffu, off, u);
+        const E* kp = static_cast<const E*>(a.Kc) + o;
+        const E* vp = static_cast<const E*>(a.Vc) + o;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int col = (v * 32 + lane) * VEC;
+          kk[u][v] = col < a.D ? *reinterpret_cast<const V*>(kp + col) : V{};
+          if constexpr (EARLY) vv[u][v] = col < a.D ? *reinterpret_cast<const V*>(vp + col) : V{};
+        }
+      }
+      if (kv0 + STEP < end) next = row_of(kv0 + STEP);
+      float s[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int gq = 0; gq < STEP / 4; ++gq) {
         float d[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) d[i] = 0.f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const E* kp = static_cast<const E*>(a.Kc) + __shfl_sync(0xffffffffu, off, gq * 4 + u);
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int col = (v * 32 + lane) * VEC;
-            if (col < a.D) {
-              const V kk = *reinterpret_cast<const V*>(kp + col);
+          for (int v = 0; v < NV; ++v)
 #pragma unroll
-              for (int x = 0; x < VEC; ++x)
+            for (int x = 0; x < VEC; ++x)
 #pragma unroll
-                for (int r = 0; r < R; ++r) d[r * 4 + u] = fmaf(q[r][v * VEC + x], to_f(kk.e[x]), d[r * 4 + u]);
-            }
-          }
-        }
+              for (int r = 0; r < R; ++r)
+                d[r * 4 + u] = fmaf(q[r][v * VEC + x], to_f(kk[gq * 4 + u][v].e[x]), d[r * 4 + u]);
         // 16 sums over 32 lanes: lane l keeps value l >> 1
 #pragma unroll
         for (int h = 8, o = 16; h; h >>= 1, o >>= 1) {
@@ -153,24 +167,22 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
         for (int i = 0; i < DL; ++i) acc[r][i] *= ar;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const E* vp = static_cast<const E*>(a.Vc) + __shfl_sync(0xffffffffu, off, i);
+      for (int i = 0; i < STEP; ++i) {
         float pr[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) pr[r] = __shfl_sync(0xffffffffu, s[i >> 2], r * 8 + (i & 3) * 2);
+        const E* vp = static_cast<const E*>(a.Vc) + (EARLY ? 0 : __shfl_sync(0xffffffffu, off, i));
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const int col = (v * 32 + lane) * VEC;
-          if (col < a.D) {
-            const V vv = *reinterpret_cast<const V*>(vp + col);
+          const V w = EARLY ? vv[EARLY ? i : 0][v] : col < a.D ? *reinterpret_cast<const V*>(vp + col) : V{};
 #pragma unroll
-            for (int x = 0; x < VEC; ++x)
+          for (int x = 0; x < VEC; ++x)
 #pragma unroll
-              for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
-                const float y = fmaf(pr[r], to_f(vv.e[x]), acc[r][v * VEC + x]);
-                acc[r][v * VEC + x] = kv0 + i < lim[r] ? y : acc[r][v * VEC + x];
-              }
-          }
+            for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
+              const float y = fmaf(pr[r], to_f(w.e[x]), acc[r][v * VEC + x]);
+              acc[r][v * VEC + x] = kv0 + i < lim[r] ? y : acc[r][v * VEC + x];
+            }
         }
       }
     }
