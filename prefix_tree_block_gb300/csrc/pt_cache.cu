@@ -424,14 +424,10 @@ extern "C" pt_status pt_cache_tables(const int32_t* held, const int32_t* added, 
   a.counters_out = reinterpret_cast<long long*>(counters_out);
   a.n = n_rows, a.ps = page_size, a.cap = ring_cap, a.max_pages = max_pages, a.max_new = max_new;
   const size_t smem = 12 * (((size_t)n_rows + 31) / 32 + 1);
-  static bool opted[64] = {false};
-  if (smem > 48 * 1024 && dev >= 0 && dev < 64 && !opted[dev]) {
-    if (cudaFuncSetAttribute(k_cache_tables, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * (kTabMaxRows / 32 + 1)) !=
-        cudaSuccess) {
-      set_error("%s: no shared memory for %d rows", who, n_rows);
-      return PT_ERR_CUDA;
-    }
-    opted[dev] = true;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(k_cache_tables, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+                              cudaSuccess) {
+    set_error("%s: no shared memory for %d rows", who, n_rows);
+    return PT_ERR_CUDA;
   }
   // one CTA up to 4096 tokens and 512 rows; then enough for a run or two per warp
   const long long by_new = ((long long)max_new + 4095) / 4096, by_rows = ((long long)n_rows + 511) / 512;

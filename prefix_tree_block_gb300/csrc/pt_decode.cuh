@@ -66,7 +66,8 @@ __host__ __device__ inline long long tile_at(int D, long long slot, int row, int
 }
 inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
 
-constexpr int kItemUnits = 3;  // what an item costs beside its units, in units
+// What an item costs beside its units (see dec_scan).
+constexpr int kRowsItem = 6, kTileItem = 12;
 
 // Which of a node's tokens a class's segment covers.  A class has at most one
 // segment per node, so a segment's number is its node's and its length is read
@@ -198,7 +199,7 @@ __device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, De
 // Exclusive sums of the units over chunks of 32 segments, in shared memory
 // (chunk[nc] = all of them); every thread of the block calls it.  With cost, of
 // two classes, the tile class first; cost[i], zero before, then receives what
-// class i's units cost, kItemUnits for each item among it.
+// class i's units and items cost.
 __device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, const DecClass& c1, DecTiling g0,
                                          DecTiling g1, int* chunk0, int* chunk1, unsigned long long* cost) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -217,7 +218,7 @@ __device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, c
       if (cost) {
         const int rt = (sg.rows() + (1 << g.r) - 1) >> g.r, last = sg.rows() - ((rt - 1) << g.r);
         // (rows: units; tiles: eighths of what a unit of 256 rows costs)
-        unsigned x = u ? (unsigned)((i ? u : 8 * u) + kItemUnits * rt * a.Hkv) : 0u;
+        unsigned x = u ? (unsigned)(i ? u + kRowsItem * rt * a.Hkv : 8 * u + kTileItem * rt * a.Hkv) : 0u;
         if (i == 0 && last <= 1 << (g.r - 1)) x -= 3 * a.Hkv * tiles;
         const unsigned hi = __reduce_add_sync(0xffffffffu, x >> 16), lo = __reduce_add_sync(0xffffffffu, x & 0xffffu);
         if (lane == 0) atomicAdd(cost + i, ((unsigned long long)hi << 16) + lo);

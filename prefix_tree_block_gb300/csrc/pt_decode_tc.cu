@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "pt.h"
@@ -928,6 +929,17 @@ bool make_tmap_pages(CUtensorMap* map, const void* base, int D, int ps, long lon
   return true;
 }
 
+// Lets a kernel use up to `bytes` of shared memory, once per device (a bit each).
+template <class K>
+cudaError_t opt_in_smem(K kernel, size_t bytes, std::atomic<uint64_t>& opted) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (opted.load(std::memory_order_relaxed) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) opted.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
 template <int NP, int SPLIT>
 cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
                         const DecClass& ct, cudaStream_t s) {
@@ -935,8 +947,8 @@ cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecA
   static_assert(C::CTAS * C::GROUPS <= kRowsWarps, "the workspace's slots");
   const size_t smem = C::smem(c.nseg);
   auto kernel = k_decode_rows<NP, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> opted{0};
+  if (cudaError_t e = opt_in_smem(kernel, C::smem(kDecMaxNodes), opted)) return e;
   count_launch();
   return launch_pdl(kernel, dim3(a.sms * C::CTAS), dim3(C::WARPS * 32), smem, s, mK, mV, a, c, ct);
 }
@@ -946,8 +958,8 @@ cudaError_t launch_tile(const CUtensorMap& mK, const CUtensorMap& mV, const DecA
                         const DecClass& cr, int box_rows, int heads, cudaStream_t s) {
   using C = TileCfg<NP>;
   const size_t smem = C::smem(c.nseg);
-  cudaError_t e = cudaFuncSetAttribute(k_decode_tile<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> opted{0};
+  if (cudaError_t e = opt_in_smem(k_decode_tile<NP>, C::smem(kDecMaxNodes), opted)) return e;
   count_launch();
   return launch_pdl(k_decode_tile<NP>, dim3(a.sms), dim3(C::THREADS), smem, s, mK, mV, a, c, cr,
                     RowsCfg<NP, 1>::CTAS * RowsCfg<NP, 1>::GROUPS, box_rows, heads);
