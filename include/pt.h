@@ -510,8 +510,10 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   runs on tensor cores; other page sizes and PT_F32 (any D up to 512) on
  *   CUDA cores.
  *   Errors: PT_ERR_INVALID_ARG and PT_ERR_UNSUPPORTED as for pt_attn_fwd,
- *   and for a workspace that is too small, a plan of another device or a bad
- *   stride.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a length
+ *   PT_ERR_INVALID_ARG also for a workspace that is too small, a plan of
+ *   another device or a bad stride, PT_ERR_UNSUPPORTED when the work items (row
+ *   tiles of 16 query heads' rows, or fewer, times kv heads, over all nodes)
+ *   times the 16-token tiles of a full table row pass 2^31 - 1.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a length
  *   outside [0, max_pages * page_size] or a count outside [0, q_len] (the
  *   nearest is taken), a page id outside [0, n_pages) (page 0 is read).
  * ------------------------------------------------------------------------- */

@@ -776,7 +776,13 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
 #pragma unroll 1
       for (int u = h; u < steps; u += 2, ++sc) {
         const int n_tok = min(tok - (u >> pair) * kTileBT, kTileBT);
-        if (n_tok < kTileBT) {  // clear V's rows behind the last token (both warpgroups of a pair: the same zeros)
+        ok = mbar_wait(s_full + h, sc & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        if (n_tok < kTileBT) {
+          // Clear V's rows behind the last token (both warpgroups of a pair: the same zeros).  Only now: S of this
+          // step being done, the product with the tile that was in this stage before is done too, so the parity
+          // below means this tile.
           const uint32_t x = n + (u >> pair), vs = x % C::VS;
           ok = mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -788,9 +794,6 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
           }
           fence_proxy_async_smem();
         }
-        ok = mbar_wait(s_full + h, sc & 1, abort_flag);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        tc_fence_after();
         if (live) {
           uint32_t sr[128];
           tmem_ld32(sb + 0, sr + 0);

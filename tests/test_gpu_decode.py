@@ -221,6 +221,84 @@ def test_many_nodes():
         _run(lens, paths, 2, 1, 64, dtype, 16, seed=8)
 
 
+@pytest.mark.parametrize("q_len,D", [(16, 128), (16, 64), (17, 128), (5, 128)])
+def test_own_nodes_that_many_rows_read(q_len, D):
+    """Continuations of several tiles, ends inside a tile, more of them than
+    SMs: the tile kernel goes from one item to the next with its rings full.
+    Twice the same."""
+    rng = np.random.default_rng(6)
+    lens = [1000] + [int(x) for x in rng.integers(130, 900, 40)]
+    paths = [[0, i] for i in range(1, 41)]
+    Hq, Hkv, ps = 32, 4, 32
+    tables, n_pages = pages_of(lens, ps, rng, width=512)
+    Kc, Vc = (c.cuda() for c in cache_of(lens, tables, n_pages, Hkv, ps, D, BF, 1))
+    Q = torch.randn(40 * q_len, Hq, D, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
+    plan = pt.decode_plan(len(lens), *csr(paths), Hq, Hkv, q_len)
+    t, n = torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    O, L = pt.attn_decode(Q, Kc, Vc, t, n, plan)
+    for _ in range(4):
+        o, l = pt.attn_decode(Q, Kc, Vc, t, n, plan)
+        assert torch.equal(o, O) and torch.equal(l, L)
+    pt.sync_status()
+    some = [0, 7, 21, 39]  # (the oracle takes its time)
+    rows = torch.tensor([s * q_len + j for s in some for j in range(q_len)])
+    check(O.cpu()[rows], L.cpu()[:, rows], Q.cpu()[rows], Kc.cpu(), Vc.cpu(), tables, lens, [paths[s] for s in some], q_len)
+
+
+def test_samples_that_end_at_one_node():
+    """Only nodes that many rows read: no work for the other kernel."""
+    _run([700], [[0]] * 80, 4, 2, 128, BF, 16, seed=4, width=1024)
+    _run([700], [[0]] * 80, 4, 2, 128, BF, 16, q_len=3, seed=4, width=1024)
+    _run([300, 5], [[0, 1]] * 300, 2, 1, 64, BF, 16, seed=4, width=4096)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_nothing_to_do(dtype):
+    """No samples; tables without a column; as many nodes as there may be."""
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    plan = pt.decode_plan(3, [0], [], 4, 2)
+    O, L = pt.attn_decode(z(0, 4, 64, t=dtype), z(1, 2, 16, 64, t=dtype), z(1, 2, 16, 64, t=dtype), z(3, 2), z(3), plan)
+    assert O.shape == (0, 4, 64) and L.shape == (4, 0)
+    plan = pt.decode_plan(2, [0, 2], [0, 1], 4, 2)
+    O, L = pt.attn_decode(z(1, 4, 64, t=dtype), z(1, 2, 16, 64, t=dtype), z(1, 2, 16, 64, t=dtype), z(2, 0), z(2), plan)
+    pt.sync_status()
+    assert not O.any() and torch.isneginf(L).all()
+    lens = [0] * (1 << 16)
+    lens[5], lens[40000], lens[65535] = 40, 33, 7
+    _run(lens, [[5, 40000], [65535], [40000]], 4, 2, 64, dtype, 16, seed=1)
+
+
+def test_too_much_work_is_refused():
+    """Work items times the tiles of a full table row past 2^31."""
+    n = 1 << 15
+    plan = pt.decode_plan(n, np.arange(n + 1), np.arange(n), 16, 16)
+    t = torch.zeros(n, 1 << 4, dtype=torch.int32, device="cuda")
+    Kc = torch.zeros(1, 16, 1 << 14, 64, dtype=BF, device="cuda")
+    with pytest.raises(pt.PTError) as e:
+        pt.attn_decode(torch.zeros(n, 16, 64, dtype=BF, device="cuda"), Kc, Kc, t, torch.zeros(n, dtype=torch.int32, device="cuda"), plan)
+    assert e.value.status == pt.PT_ERR_UNSUPPORTED
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, over one cache and one plan."""
+    lens, paths = [2500] + [40 + i for i in range(40)], [[0, i] for i in range(1, 41)]
+    tables, n_pages = pages_of(lens, 64, np.random.default_rng(1), width=256)
+    Kc, Vc = (c.cuda() for c in cache_of(lens, tables, n_pages, 2, 64, 128, BF, 1))
+    plan = pt.decode_plan(len(lens), *csr(paths), 16, 2)
+    t, n = torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    Q = [torch.randn(40, 16, 128, generator=torch.Generator().manual_seed(i)).to(BF).cuda() for i in range(2)]
+    want = [pt.attn_decode(q, Kc, Vc, t, n, plan) for q in Q]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        got = [pt.attn_decode(q, Kc, Vc, t, n, plan, stream=s) for q, s in zip(Q, side)]
+    torch.cuda.synchronize()
+    pt.sync_status()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_same_result_each_time(dtype):
     lens, paths = [3000] + [50 + i for i in range(20)], [[0, i] for i in range(1, 21)]  # (the prompt: 140 rows)
