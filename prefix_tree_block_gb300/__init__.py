@@ -587,7 +587,7 @@ def fold_plan(node_lengths, path_ptr, path_nodes, row_len: int, stream=None) -> 
 # The calls below run once per layer and step, next to kernels of a few
 # microseconds, so their Python side is kept short: one attribute or method of
 # a tensor costs about 0.1 us here, an allocation 1.5 us.
-_T = None  # torch, its int32, int64, float32 and bfloat16, and two queries of its CUDA state
+_T = None  # torch, its int32, int64, float32 and bfloat16, a device's current stream, and the current device
 
 
 def _torch():
@@ -598,20 +598,22 @@ def _torch():
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is None:
             raw = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
-        _T = torch, torch.int32, torch.int64, torch.float32, torch.bfloat16, raw
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _T = torch, torch.int32, torch.int64, torch.float32, torch.bfloat16, raw, device
     return _T
 
 
 def _bad(t, name: str, dtype, dev):
     """Raise for a tensor of the cache calls that is not dense, of this dtype
     and on the current device."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or dev < 0:
         raise TypeError(f"{name} must be a contiguous CUDA tensor of {dtype}")
     raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
 
 
 def _need(t, name: str, dtype, shape, dev):
-    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+    """dev: the current device, or -1 when the call's first tensor is not on one."""
+    if t.dtype != dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous():
         _bad(t, name, dtype, dev)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
@@ -640,17 +642,15 @@ def cache_tables(held, added, tables, ring, counters, page_size: int, max_new: i
     [n, max_pages] and ring [cap]; counters int64 [2].  tables and ring change
     in place; returns new lens [n], counters [2], row_ptr [n + 1], and the
     added tokens' slots and position ids (int64 [max_new])."""
-    torch, i32, i64, _, _, _ = _torch()
-    dev = torch.cuda.current_device()
+    _, i32, i64, _, _, _, device = _torch()
     n, cap = held.numel(), ring.numel()
     row = (n,)
+    dev = device() if held.is_cuda else -1
     _need(held, "held", i32, row, dev)
     _need(added, "added", i32, row, dev)
     _need(ring, "ring", i32, (cap,), dev)
     _need(counters, "counters", i64, (2,), dev)
-    if tables.dim() != 2:
-        raise ValueError(f"tables has shape {tuple(tables.shape)}, ({n}, max_pages) expected")
-    width = tables.shape[1]
+    width = tables.shape[1] if tables.dim() == 2 else 0
     _need(tables, "tables", i32, (n, width), dev)
     if start is not None:
         _need(start, "start", i32, row, dev)
@@ -676,7 +676,7 @@ def _cache_shape(Kc, Vc, dtype, dev):
     shape = Kc.shape
     if len(shape) != 4:
         raise ValueError("Kc and Vc are [n_pages, Hkv, page_size, D]")
-    if Kc.dtype != dtype or Kc.get_device() != dev or not Kc.is_contiguous():
+    if Kc.dtype != dtype or Kc.get_device() != dev or dev < 0 or not Kc.is_contiguous():
         _bad(Kc, "Kc", dtype, dev)
     _need(Vc, "Vc", dtype, shape, dev)
     return code, shape
@@ -685,7 +685,7 @@ def _cache_shape(Kc, Vc, dtype, dev):
 def _token_rows(t, name, dtype, T, heads, D, dev):
     """[T, heads, D] tokens whose heads are dense (a slice of a fused
     projection will do); returns the elements between tokens."""
-    if t.dtype != dtype or t.get_device() != dev:
+    if t.dtype != dtype or t.get_device() != dev or dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor [T, heads, head_dim] of {dtype} on the current device")
     if t.shape != (T, heads, D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, ({T}, {heads}, {D}) expected")
@@ -699,8 +699,8 @@ def _token_rows(t, name, dtype, T, heads, D, dev):
 def cache_write(K, V, slots, Kc, Vc, stream=None) -> None:
     """Put tokens' K and V [T, Hkv, D] into their slots (int64 [T], negative:
     passed over) of the cache Kc, Vc [n_pages, Hkv, page_size, D], in place."""
-    torch, _, i64, _, _, _ = _torch()
-    dev = torch.cuda.current_device()
+    i64, device = _torch()[2], _T[6]
+    dev = device() if K.is_cuda else -1
     dtype = K.dtype
     code, (n_pages, Hkv, ps, D) = _cache_shape(Kc, Vc, dtype, dev)
     T = K.shape[0]
@@ -765,17 +765,15 @@ def attn_decode(Q, Kc, Vc, tables, lens, plan: DecodePlan, q_count=None, scale: 
     the samples' newest tokens Q over the cache Kc, Vc [n_pages, Hkv,
     page_size, D], tables [n_nodes, max_pages], lens [n_nodes] (pt_attn_decode).
     With q_count, rows behind a sample's queries keep what O and LSE held."""
-    torch, i32, _, f32, _, _ = _torch()
-    dev = torch.cuda.current_device()
+    torch, i32, _, f32, _, _, device = _torch()
+    dev = device() if Q.is_cuda else -1
     dtype = Q.dtype
     code, (n_pages, Hkv, ps, D) = _cache_shape(Kc, Vc, dtype, dev)
     T, Hq, N = plan.n_rows, plan.Hq, plan.n_nodes
     if Hkv != plan.Hkv:
         raise ValueError(f"the cache has {Hkv} kv heads, the plan {plan.Hkv}")
     qs = _token_rows(Q, "Q", dtype, T, Hq, D, dev)
-    if tables.dim() != 2:
-        raise ValueError(f"tables has shape {tuple(tables.shape)}, ({N}, max_pages) expected")
-    width = tables.shape[1]
+    width = tables.shape[1] if tables.dim() == 2 else 0
     _need(tables, "tables", i32, (N, width), dev)
     _need(lens, "lens", i32, (N,), dev)
     if q_count is not None:
