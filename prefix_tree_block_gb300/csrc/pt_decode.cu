@@ -252,7 +252,8 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
     if (tiles > 0) {
       const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
       two = tile && sg.rows() - (rt << rl) <= kTileR / 2;
-      const unsigned u0 = before + it * tiles, w0 = u0 / (unsigned)per, w1 = (u0 + tiles - 1) / (unsigned)per;
+      const int nu = dec_line(DecTiling{rl, bl, tile ? kTile.k : m.g0.k}, sg.rows(), tiles);
+      const unsigned u0 = before + it * nu, w0 = u0 / (unsigned)per, w1 = (u0 + nu - 1) / (unsigned)per;
       row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
       count = (int)(w1 - w0 + 1) << two;
     }
@@ -736,7 +737,8 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   for (int c = 0; c < kDecClasses; ++c) {
     const bool used = c == kDecSimt ? !tc : c == kDecRows ? tc && !tiles : tiles;
     const int bt = c == kDecSimt ? kSimtBT : c == kDecTile ? kTileBT : kRowsBT;
-    if (used && (long long)plan->cls[c].nitems * ((a.cap + bt - 1) / bt) > INT_MAX) {
+    const long long line = 2ll * ((a.cap + bt - 1) / bt) + 8;  // more than an item's units
+    if (used && plan->cls[c].nitems * line > INT_MAX) {
       set_error("%s: %d work items over tables of %d tokens are out of range", who, plan->cls[c].nitems, a.cap);
       return PT_ERR_UNSUPPORTED;
     }

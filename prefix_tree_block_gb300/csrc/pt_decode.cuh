@@ -3,18 +3,18 @@
 //
 // A segment is a run of one node's cached tokens with the query rows that read
 // it: every q head of every query token of every sample below the node, per kv
-// head (rows = members * q_len * Hq / Hkv).  An item is (segment, tile of R
-// rows, kv head); its units are tiles of BT tokens.  All items' units laid end
-// to end (segments in order, in a segment the row tiles, in a row tile the kv
-// heads) are cut into equal runs, one per worker, wherever the cuts fall: no
-// worker has more than one unit above another, whatever the nodes' lengths,
-// and a prompt that many samples share is read once per row tile.  What a
-// worker computes of an item is a piece.  Worker w and item i have at most one
-// piece in common and both grow along the line, so w + i numbers the pieces
-// without a list: that is the slot of its partial result (each row's
-// normalised output in fp32 and its base-2 log-sum-exp), and a row's pieces
-// are found again from its path's segments alone.  The lengths are read on the
-// device, so a captured graph follows them.
+// head (rows = members * q_len * Hq / Hkv).  An item is (segment, row tile, kv
+// head); its units are its token tiles, and a few more for what beginning and
+// ending it costs.  All items' units laid end to end (segments in order, in a
+// segment the row tiles, in a row tile the kv heads) are cut into equal runs,
+// one per worker, wherever the cuts fall: no worker has more than one unit
+// above another, whatever the nodes' lengths, and a prompt that many samples
+// share is read once per row tile.  What a worker computes of an item is a
+// piece.  Worker w and item i have at most one piece in common and both grow
+// along the line, so w + i numbers the pieces without a list: that is the slot
+// of its partial result (each row's normalised output in fp32 and its base-2
+// log-sum-exp), and a row's pieces are found again from its path's segments
+// alone.  The lengths are read on the device, so a captured graph follows them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,9 +27,10 @@ namespace pt {
 
 constexpr int kDecMaxNodes = 1 << 16;  // 4 or 8 bytes of shared memory per 32 nodes
 
-// Row and token tiles of a class: 2^r rows, 2^t tokens.
+// Row and token tiles of a class: 2^r rows, 2^t tokens; and the units that an
+// item counts beside its tiles', what beginning and ending it costs.
 struct DecTiling {
-  int r, t;
+  int r, t, k;
 };
 
 // The plan's classes: a call uses kDecSimt, or kDecRows, or kDecRowsFew with
@@ -41,9 +42,9 @@ enum : int {
   kDecTile = 3,     // tcgen05: the rest
   kDecClasses = 4
 };
-constexpr DecTiling kSimt = {2, 4};  // a warp per worker
-constexpr DecTiling kRows = {4, 4};  // a warp per worker
-constexpr DecTiling kTile = {8, 7};  // a CTA per worker; an item of up to 128 rows has two partial results
+constexpr DecTiling kSimt = {2, 4, 0};  // a warp per worker
+constexpr DecTiling kRows = {4, 4, 2};  // a warp per worker
+constexpr DecTiling kTile = {8, 7, 4};  // a CTA per worker; an item of up to 128 rows has two partial results
 constexpr int kSimtR = 1 << kSimt.r, kSimtBT = 1 << kSimt.t;
 constexpr int kRowsR = 1 << kRows.r, kRowsBT = 1 << kRows.t;
 constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
@@ -65,9 +66,6 @@ __host__ __device__ inline long long tile_at(int D, long long slot, int row, int
   return ((slot * (D >> 3) + (col >> 3)) * kTileR + row) * 8 + (col & 7);
 }
 inline int dec_r(int cls) { return cls == kDecSimt ? kSimtR : cls == kDecTile ? kTileR : kRowsR; }
-
-// What an item costs beside its units (see dec_scan).
-constexpr int kRowsItem = 6, kTileItem = 12;
 
 // Which of a node's tokens a class's segment covers.  A class has at most one
 // segment per node, so a segment's number is its node's and its length is read
@@ -179,6 +177,15 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
   return v;
 }
 
+// A tile of an item counts 2^wide units: in the tile class twice when the
+// segment has more than half a row tile, which costs twice the time.
+__device__ __forceinline__ int dec_wide(DecTiling g, int rows) { return g.r == kTile.r && rows > kTileR / 2; }
+
+// Units of an item of so many tiles.
+__device__ __forceinline__ int dec_line(DecTiling g, int rows, int tiles) {
+  return tiles > 0 ? (tiles << dec_wide(g, rows)) + g.k : 0;
+}
+
 // Units of segment i, and what it takes to know them: its entry, its length
 // and the tiles of one of its items (0 when its only sample has no queries).
 __device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, DecTiling g, int i, DecSeg& sg, int& raw,
@@ -193,13 +200,13 @@ __device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, De
   dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
   tiles = (e - b + (1 << g.t) - 1) >> g.t;
   if (a.q_count && sg.solo >= 0 && a.q_count[sg.solo] <= 0) tiles = 0;
-  return ((sg.rows() + (1 << g.r) - 1) >> g.r) * a.Hkv * tiles;
+  return ((sg.rows() + (1 << g.r) - 1) >> g.r) * a.Hkv * dec_line(g, sg.rows(), tiles);
 }
 
 // Exclusive sums of the units over chunks of 32 segments, in shared memory
 // (chunk[nc] = all of them); every thread of the block calls it.  With cost, of
-// two classes, the tile class first; cost[i], zero before, then receives what
-// class i's units and items cost.
+// two classes, the tile class first; cost[i], zero before, then receives class
+// i's units.
 __device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, const DecClass& c1, DecTiling g0,
                                          DecTiling g1, int* chunk0, int* chunk1, unsigned long long* cost) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -210,16 +217,13 @@ __device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, c
     for (int i = 0; i < (cost ? 2 : 1); ++i) {
       DecSeg sg;
       int raw, tiles;
-      const DecTiling g = {i ? g1.r : g0.r, i ? g1.t : g0.t};
+      const DecTiling g = {i ? g1.r : g0.r, i ? g1.t : g0.t, i ? g1.k : g0.k};
       const int u = dec_units(a, i ? c1 : c0, g, k * 32 + lane, sg, raw, tiles);
       if (blockIdx.x == 0 && (raw < 0 || raw > a.cap)) record_status(PT_STATUS_INVALID);
       const int sum = __reduce_add_sync(0xffffffffu, u);
       if (lane == 0) (i ? chunk1 : chunk0)[k] = sum;
       if (cost) {
-        const int rt = (sg.rows() + (1 << g.r) - 1) >> g.r, last = sg.rows() - ((rt - 1) << g.r);
-        // (rows: units; tiles: eighths of what a unit of 256 rows costs)
-        unsigned x = u ? (unsigned)(i ? u + kRowsItem * rt * a.Hkv : 8 * u + kTileItem * rt * a.Hkv) : 0u;
-        if (i == 0 && last <= 1 << (g.r - 1)) x -= 3 * a.Hkv * tiles;
+        const unsigned x = u;
         const unsigned hi = __reduce_add_sync(0xffffffffu, x >> 16), lo = __reduce_add_sync(0xffffffffu, x & 0xffffu);
         if (lane == 0) atomicAdd(cost + i, ((unsigned long long)hi << 16) + lo);
       }
@@ -261,7 +265,7 @@ __device__ __forceinline__ void dec_publish(const DecArgs& a, const DecClass& c,
   if (threadIdx.x == 0) c.pref[c.nseg] = per;
 }
 
-// A piece: units [t0, t1) of one item of segment `node`.
+// A piece: tiles [t0, t1) of one item of segment `node`.
 struct DecPiece {
   int node, len, kind, rows, member0;
   int rt, hk;  // row tile and kv head
@@ -314,15 +318,16 @@ struct DecWalk {
     p.kind = (int)((unsigned)rk >> 29);
     p.member0 = __shfl_sync(0xffffffffu, sg.member0, l);
     const int item0 = __shfl_sync(0xffffffffu, sg.item0, l);
-    const int nt = __shfl_sync(0xffffffffu, tiles, l);
+    const int wide = dec_wide(g, p.rows), nu = dec_line(g, p.rows, __shfl_sync(0xffffffffu, tiles, l));
     const int rel = pos - __shfl_sync(0xffffffffu, excl, l);
-    const int it = (int)((unsigned)rel / (unsigned)nt);
-    p.t0 = rel - it * nt;
-    p.t1 = min(nt, p.t0 + (end - pos));
+    const int it = (int)((unsigned)rel / (unsigned)nu), u0 = rel - it * nu, u1 = min(nu, u0 + (end - pos));
+    // (a cut inside a tile leaves it to the piece before, one inside the item's own units gives that an empty piece)
+    p.t0 = (max(u0 - g.k, 0) + wide) >> wide;
+    p.t1 = (max(u1 - g.k, 0) + wide) >> wide;
     p.rt = (int)((unsigned)it / (unsigned)a.Hkv);
     p.hk = it - p.rt * a.Hkv;
     p.slot = w + item0 + it;
-    pos += p.t1 - p.t0;
+    pos += u1 - u0;
     return true;
   }
 };

@@ -124,6 +124,10 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     while (issued - used < C::STAGES) {
       if (lp.t0 >= lp.t1) {
         if (!walk.next(lp)) break;
+        if (lp.t0 == lp.t1) {  // an empty piece: nothing for its rows
+          if (lane < kRowsR && sw == 0) c.lse[(long long)lp.slot * kRowsR + lane] = -INFINITY;
+          continue;
+        }
         if (lane == 0) pieces[found % kRowsPieces] = lp;
         ++found;
         int b, e;
@@ -364,7 +368,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
 }
 
 // The fewest tile units worth a partial result of their own.
-constexpr int kTileMinUnits = 2;
+constexpr int kTileMinUnits = 4;
 
 // How the SMs are divided when a call has both kinds of segments (below): every
 // CTA of both kernels scans both classes and finds the same numbers.
@@ -379,15 +383,15 @@ __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& 
   if (both)
     dec_scan(a, ct, cr, kTile, kRows, chunk_t, chunk_r, cost);
   else
-    dec_scan(a, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t}, kRows,
+    dec_scan(a, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t, ct.nitems ? kTile.k : kRows.k}, kRows,
              ct.nitems ? chunk_t : chunk_r, chunk_r, nullptr);
   const int nc = (max(ct.nseg, cr.nseg) + 31) >> 5;
   const int units_t = ct.nitems ? chunk_t[nc] : 0, units_r = cr.nitems ? chunk_r[nc] : 0;
   DecSplit s;
   s.n_tile = units_t > 0 ? sms : 0;
   if (units_t > 0 && units_r > 0) {
-    // a tile unit of 256 rows costs an SM about as much as 20 units of 16 rows and tokens (28 at head_dim 64)
-    const float x = (float)cost[0] * (NP == 1 ? 3.5f : 2.5f);
+    // (a tile unit of 128 rows costs an SM about as much as 10 units of 16 rows and tokens, 14 at head_dim 64)
+    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f);
     s.n_tile = min(max((int)(sms * (x / (x + (float)cost[1]))), 1), sms - 1);
   }
   s.per_t = dec_share(units_t, max(s.n_tile, 1), kTileMinUnits);
@@ -569,6 +573,11 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
 #pragma unroll 1
     while (true) {
       const bool more = walk.next(p);
+      if (more && p.t0 == p.t1) {  // an empty piece: nothing for its rows
+#pragma unroll 1
+        for (int r = lane; r < kTileR; r += 32) c.lse[(long long)p.slot * kTileR + r] = -INFINITY;
+        continue;
+      }
       if (!more) p.rows = 0;
       if (np >= C::PIECES) ok = mbar_wait(piece_empty + np % C::PIECES, (np / C::PIECES - 1) & 1, abort_flag);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
