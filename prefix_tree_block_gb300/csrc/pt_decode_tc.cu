@@ -247,20 +247,51 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
         x[n][0] = sum.x, x[n][1] = sum.y, x[n][2] = sum.z, x[n][3] = sum.w;
       }
     }
+    int n_mul = kRowsBT, n_any = kRowsBT;  // tokens whose values the product takes; tokens that any row keeps
+    if (kv0 + kRowsBT > lim_min) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[n][i] *= a.scale_log2;
-        if (kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1]) x[n][i] = -INFINITY;
+        for (int i = 0; i < 4; ++i)
+          if (kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1]) x[n][i] = -INFINITY;
+      // Values that no row keeps are cleared: a probability of 0 times what
+      // lies behind the node's tokens must stay 0.  Tokens that some rows keep
+      // and others do not go through the product too unless one is not finite:
+      // then they are cleared as well and added row by row.
+      n_any = min(max(lim_max - kv0, 0), kRowsBT);
+      n_mul = n_any;
+      const int n_all = min(max(lim_min - kv0, 0), kRowsBT);
+      uint8_t* vs = ring + s * C::STAGE + NP * C::PANEL;
+      if (n_all < n_any) {
+        bool odd = false;
+#pragma unroll 1
+        for (int i = n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
+          const uint4 v = *reinterpret_cast<const uint4*>(vs + ((i % (NP * 8)) >> 3) * C::PANEL + (i / (NP * 8)) * 128 +
+                                                          (i & 7) * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+        }
+        if (__any_sync(0xffffffffu, odd)) n_mul = n_all;
       }
+      if (n_mul < n_any) {
+        n_mul = -1 - n_mul;  // (once the probabilities are known)
+      } else if (n_any < kRowsBT) {
+#pragma unroll 1
+        for (int i = n_any * (NP * 8) + lane; i < kRowsBT * (NP * 8); i += 32)
+          *reinterpret_cast<uint4*>(vs + ((i % (NP * 8)) >> 3) * C::PANEL + (i / (NP * 8)) * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();  // before the stage is loaded again
+        __syncwarp();
+      }
+    }
     bool grow = false;
     float ref[2], al[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float mx = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.scale_log2;
       const bool up = mx > m[i] + 8.f;
       const float mn = up ? mx : m[i];
       ref[i] = mn == -INFINITY ? 0.f : mn;
@@ -272,7 +303,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[n][i] = ex2(x[n][i] - ref[i >> 1]);
+      for (int i = 0; i < 4; ++i) x[n][i] = ex2(fmaf(x[n][i], a.scale_log2, -ref[i >> 1]));
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int i = 0; i < NP * 8; ++i) {
@@ -288,59 +319,43 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     pa[1] = pack_bf16(x[0][2], x[0][3]);
     pa[2] = pack_bf16(x[1][0], x[1][1]);
     pa[3] = pack_bf16(x[1][2], x[1][3]);
-    // Values that no row keeps are cleared: a probability of 0 times what lies
-    // behind the node's tokens must stay 0.  Tokens that some rows keep and
-    // others do not go through the product too unless one is not finite: then
-    // they are left out of it and added row by row.
-    uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
-    int n_mul = kRowsBT, n_any = kRowsBT;
-    if (kv0 + kRowsBT > lim_min) {
-      n_any = min(max(lim_max - kv0, 0), kRowsBT);
-      n_mul = n_any;
-      const int n_all = min(max(lim_min - kv0, 0), kRowsBT);
-      if (n_all < n_any) {
-        bool odd = false;
+    if (n_mul < 0) {  // a value that is not finite, kept by some rows only: those tokens row by row, then cleared
+      n_mul = -1 - n_mul;
 #pragma unroll 1
-        for (int i = n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
-          const uint4 v = *reinterpret_cast<const uint4*>(ring + s * C::STAGE + (NP + ((i % (NP * 8)) >> 3)) * C::PANEL +
-                                                          (i / (NP * 8)) * 128 + (i & 7) * 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int n = n_mul; n < n_any; ++n) {
+        float pr[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+        for (int i = 0; i < 2; ++i) {
+          const float even = n & 8 ? x[1][2 * i] : x[0][2 * i], oddc = n & 8 ? x[1][2 * i + 1] : x[0][2 * i + 1];
+          pr[i] = __shfl_sync(0xffffffffu, n & 1 ? oddc : even, (lane & ~3) | ((n & 7) >> 1));
         }
-        if (__any_sync(0xffffffffu, odd)) n_mul = n_all;
+#pragma unroll
+        for (int k = 0; k < NP * 8; ++k) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + s * C::STAGE + (NP + (k >> 3)) * C::PANEL + n * 128 +
+                                                                (((k & 7) ^ (n & 7)) << 4) + (lane & 3) * 4);
+          const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (kv0 + n < lim[i]) {
+              o[k][2 * i] = fmaf(pr[i], v0, o[k][2 * i]);
+              o[k][2 * i + 1] = fmaf(pr[i], v1, o[k][2 * i + 1]);
+            }
+        }
       }
-      // this lane's V elements of a fragment: tokens c2, c2 + 1 (f[0], f[2]) and c2 + 8, c2 + 9 (f[1], f[3])
-      k0 = (c2 < n_mul ? 0xffffu : 0u) | (c2 + 1 < n_mul ? 0xffff0000u : 0u);
-      k1 = (c2 + 8 < n_mul ? 0xffffu : 0u) | (c2 + 9 < n_mul ? 0xffff0000u : 0u);
+      __syncwarp();
+#pragma unroll 1
+      for (int i = n_mul * (NP * 8) + lane; i < kRowsBT * (NP * 8); i += 32)
+        *reinterpret_cast<uint4*>(ring + s * C::STAGE + (NP + ((i % (NP * 8)) >> 3)) * C::PANEL + (i / (NP * 8)) * 128 +
+                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
     }
 #pragma unroll
     for (int k = 0; k < NP * 4; ++k) {
       uint32_t f[4];
       ldsm4t(f, vb + (k >> 2) * C::PANEL + v_row * 128 + ((((k & 3) * 2 + v_cb) ^ (v_row & 7)) << 4));
-      mma16816(o[2 * k], pa, f[0] & k0, f[1] & k1);
-      mma16816(o[2 * k + 1], pa, f[2] & k0, f[3] & k1);
-    }
-#pragma unroll 1
-    for (int n = n_mul; n < n_any; ++n) {
-      float pr[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float even = n & 8 ? x[1][2 * i] : x[0][2 * i], oddc = n & 8 ? x[1][2 * i + 1] : x[0][2 * i + 1];
-        pr[i] = __shfl_sync(0xffffffffu, n & 1 ? oddc : even, (lane & ~3) | ((n & 7) >> 1));
-      }
-#pragma unroll
-      for (int k = 0; k < NP * 8; ++k) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(ring + s * C::STAGE + (NP + (k >> 3)) * C::PANEL + n * 128 +
-                                                              (((k & 7) ^ (n & 7)) << 4) + (lane & 3) * 4);
-        const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (kv0 + n < lim[i]) {
-            o[k][2 * i] = fmaf(pr[i], v0, o[k][2 * i]);
-            o[k][2 * i + 1] = fmaf(pr[i], v1, o[k][2 * i + 1]);
-          }
-      }
+      mma16816(o[2 * k], pa, f[0], f[1]);
+      mma16816(o[2 * k + 1], pa, f[2], f[3]);
     }
     ++used;
     ++t;
