@@ -61,7 +61,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // 128-byte swizzle), fills it by TMA itself (a box is 16 tokens of one page)
 // and computes on what has arrived; nothing but the walk's sums is shared.  The
 // loads run up to a ring ahead of the arithmetic, across the ends of pieces.
-//   S = Q K^T: Q's fragments stay in registers, K's come by ldmatrix.
+// With a piece's first load its query rows are gathered too, so that they are
+// there when the piece begins.
+//   S = Q K^T: both operands' fragments come by ldmatrix.
 //   O += P V: P is the bf16 of S's own registers (the accumulator's layout is
 //   the A operand's), V's fragments come by ldmatrix.trans.
 // The warps of a SPLIT worker add up their parts of S through shared memory,
@@ -71,31 +73,32 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // ---------------------------------------------------------------------------
 template <int NP, int SPLIT>
 struct RowsCfg {
-  static constexpr int WARPS = 4, GROUPS = WARPS / SPLIT;  // GROUPS workers a CTA
-  static constexpr int CTAS = NP == 1 ? 3 : 2;             // per SM
-  static constexpr int STAGES = NP == 1 ? 4 : 2;
-  static constexpr int PANEL = 16 * 128;            // bytes: 16 tokens x 64 columns
+  static constexpr int WARPS = SPLIT == 1 && NP == 2 ? 3 : 4, GROUPS = WARPS / SPLIT;  // GROUPS workers a CTA
+  static constexpr int CTAS = SPLIT == 1 ? 3 : 2;                                      // per SM
+  static constexpr int STAGES = NP == 1 ? 3 : 2;
+  static constexpr int PANEL = 16 * 128;            // bytes: 16 tokens (or rows) x 64 columns
   static constexpr int STAGE = 2 * NP * PANEL;      // K panels, V panels
-  static constexpr int RING = STAGES * STAGE;       // a warp's
+  static constexpr int QBUF = NP * PANEL;           // a piece's query rows
+  static constexpr int RING = STAGES * STAGE + 2 * QBUF;  // a warp's stages, and its rows of two pieces
   static constexpr int OFF_X = WARPS * RING;        // parts of S: two of 1 KB a warp
   static constexpr int OFF_BAR = OFF_X + (SPLIT > 1 ? WARPS * 2048 : 0);
   static constexpr int NBAR = WARPS * STAGES + (SPLIT > 1 ? GROUPS : 0);
-  static constexpr int OFF_PIECE = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_CHUNK = OFF_PIECE + WARPS * 8 * (int)sizeof(DecPiece);
+  static constexpr int OFF_LIM = OFF_BAR + NBAR * 8;  // [warp][piece & 1][row]
+  static constexpr int OFF_PIECE = OFF_LIM + WARPS * 2 * kRowsR * 4;  // [warp][piece & 1]
+  static constexpr int OFF_CHUNK = OFF_PIECE + WARPS * 2 * (int)sizeof(DecPiece);
   static constexpr size_t smem(int nseg) { return OFF_CHUNK + 8 * ((size_t)(nseg + 31) / 32 + 1) + 1024; }
 };
 
 // One warp of a worker (the sw-th of SPLIT): its ring (1024-byte aligned), its
-// barriers (initialised for one arrival), room for kRowsPieces pieces, and of
-// the worker the room for S's parts and its barrier (SPLIT arrivals).
-constexpr int kRowsPieces = 8;
+// barriers (initialised for one arrival), room for two pieces and their rows'
+// limits, and of the worker the room for S's parts and its barrier (SPLIT
+// arrivals).
 template <int NP, int SPLIT>
 __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a,
                                             const DecClass& c, const int* chunk, int per, int worker, int sw,
-                                            uint8_t* ring, uint64_t* full, DecPiece* pieces, float4* xbuf,
+                                            uint8_t* ring, uint64_t* full, DecPiece* pieces, int* lims, float4* xbuf,
                                             uint64_t* xbar, volatile int* abort_flag) {
   using C = RowsCfg<NP, SPLIT>;
-  static_assert(C::STAGES + 1 < kRowsPieces, "a piece per stage in flight, and the current one");
   const int lane = threadIdx.x & 31;
   const int col0 = SPLIT == 1 ? 0 : sw * 128;  // this warp's first column
   const uint32_t ring_u = smem_u32(ring);
@@ -109,7 +112,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
   int t = 0, t1 = 0, kv_base = 0, rows_left = 0, lim_min = 0, lim_max = 0;
   int lim[2] = {0, 0};
   int slot = 0;
-  uint32_t q[NP * 4][4];
+  uint8_t* qbuf = ring + C::STAGES * C::STAGE;
   float o[NP * 8][4], m[2], l[2];
   const int r_lo = lane >> 2, c2 = (lane & 3) * 2;  // this lane's rows r_lo, r_lo + 8; its column pair
   // ldmatrix rows: K (matrices: tokens 0-7 / 8-15 by lane bit 4, columns by bit 3), V transposed (tokens by bit 3,
@@ -123,19 +126,46 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
 #pragma unroll 1
     while (issued - used < C::STAGES) {
       if (lp.t0 >= lp.t1) {
-        if (!walk.next(lp)) break;
+        if (found > at || !walk.next(lp)) break;  // (one piece beside the current: two have room)
         if (lp.t0 == lp.t1) {  // an empty piece: nothing for its rows
           if (lane < kRowsR && sw == 0) c.lse[(long long)lp.slot * kRowsR + lane] = -INFINITY;
           continue;
         }
-        if (lane == 0) pieces[found % kRowsPieces] = lp;
-        ++found;
         int b, e;
         dec_range(a, lp.kind, lp.len, b, e);
         const int kv0 = b + lp.t0 * kRowsBT;
         l_last = (min(e, b + lp.t1 * kRowsBT) - 1) / a.ps;
         l_page0 = kv0 / a.ps - 32, l_page = 32;  // (looked up below)
         l_row = kv0 % a.ps;
+        if (lane == 0) pieces[found & 1] = lp;
+        // the piece's query rows, asynchronously into the buffer that the current piece does not use; lane r looks row r up
+        long long src = -1;
+        if (lane < min(lp.rows - lp.rt * kRowsR, kRowsR)) {
+          const DecRow d = dec_row(a, lp.member0, lp.hk, lp.rt * kRowsR + lane, lp.len);
+          lims[(found & 1) * kRowsR + lane] = d.lim;
+          src = (long long)d.tok * a.q_stride + (long long)d.head * a.D + col0;
+        }
+        constexpr int CPR = NP * 8, RPI = 32 / CPR;  // 16-byte pieces of a row; rows per warp instruction
+        const int ck = lane % CPR, cr = lane / CPR;
+        uint8_t* qb = qbuf + (found & 1) * C::QBUF + (ck >> 3) * C::PANEL;
+#pragma unroll 2
+        for (int i = 0; i < kRowsR; i += RPI) {
+          const long long from = __shfl_sync(0xffffffffu, src, i + cr);
+          const bool in = from >= 0 && col0 + ck * 8 < a.D;
+          const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.Q) + (in ? from + ck * 8 : 0);
+          uint8_t* dst = qb + (i + cr) * 128 + (((ck & 7) ^ ((i + cr) & 7)) << 4);
+          if (a.q_vec) {
+            cp_async16(dst, g, in ? 16 : 0);
+          } else {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(g);
+              v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(dst) = v;
+          }
+        }
+        ++found;
       }
       if (l_page >= 32) {
         l_page0 += l_page;
@@ -170,9 +200,9 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     if (used == issued) break;
     // --- a new piece: its rows
     if (t >= t1) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
-      const DecPiece& p = pieces[at % kRowsPieces];
-      ++at;
+      const DecPiece& p = pieces[at & 1];
       int e;
       dec_range(a, p.kind, p.len, kv_base, e);
       t = p.t0, t1 = p.t1, slot = p.slot;
@@ -180,23 +210,12 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       int own_lo = INT_MAX;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = r_lo + i * 8;
-        const __nv_bfloat16* src = nullptr;
-        lim[i] = 0;
-        if (r < rows_left) {
-          const DecRow d = dec_row(a, p.member0, p.hk, p.rt * kRowsR + r, p.len);
-          lim[i] = d.lim;
-          own_lo = min(own_lo, d.lim);
-          src = static_cast<const __nv_bfloat16*>(a.Q) + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
-        }
-#pragma unroll
-        for (int k = 0; k < NP * 4; ++k) {
-          const int col = col0 + k * 16 + c2;
-          q[k][i] = src && col < a.D ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
-          q[k][i + 2] = src && col + 8 < a.D ? *reinterpret_cast<const uint32_t*>(src + col + 8) : 0u;
-        }
+        const bool row = r_lo + i * 8 < rows_left;
+        lim[i] = row ? lims[(at & 1) * kRowsR + r_lo + i * 8] : 0;
+        if (row) own_lo = min(own_lo, lim[i]);
         m[i] = -INFINITY, l[i] = 0.f;
       }
+      ++at;
       // what all of the rows see, and what any of them does
       lim_min = __reduce_min_sync(0xffffffffu, own_lo);
       lim_max = min(__reduce_max_sync(0xffffffffu, max(lim[0], lim[1])), e);
@@ -209,6 +228,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     const uint32_t kb = ring_u + s * C::STAGE, vb = kb + NP * C::PANEL;
+    const uint32_t qa = ring_u + C::STAGES * C::STAGE + ((at - 1) & 1) * C::QBUF;
     const int kv0 = kv_base + t * kRowsBT;
     // S, in two chains of accumulation a column tile
     float sc[2][2][4];
@@ -216,10 +236,11 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     for (int i = 0; i < 16; ++i) sc[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
 #pragma unroll
     for (int k = 0; k < NP * 4; ++k) {
-      uint32_t f[4];
+      uint32_t f[4], q[4];  // (Q's matrices: rows by lane bit 3, columns by bit 4, as V's)
+      ldsm4(q, qa + (k >> 2) * C::PANEL + v_row * 128 + ((((k & 3) * 2 + v_cb) ^ (v_row & 7)) << 4));
       ldsm4(f, kb + (k >> 2) * C::PANEL + k_row * 128 + ((((k & 3) * 2 + k_cb) ^ (k_row & 7)) << 4));
-      mma16816(sc[k & 1][0], q[k], f[0], f[1]);
-      mma16816(sc[k & 1][1], q[k], f[2], f[3]);
+      mma16816(sc[k & 1][0], q, f[0], f[1]);
+      mma16816(sc[k & 1][1], q, f[2], f[3]);
     }
     float x[2][4];  // [column tile of 8][(row lo: 2 columns), (row hi: 2 columns)]
 #pragma unroll
@@ -448,7 +469,8 @@ __global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SP
   if ((int)blockIdx.x < (a.sms - sp.n_tile) * C::CTAS)
     rows_worker<NP, SPLIT>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::GROUPS + warp / SPLIT, warp % SPLIT,
                            smem + warp * C::RING, bars + warp * C::STAGES,
-                           reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE) + warp * kRowsPieces,
+                           reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE) + warp * 2,
+                           reinterpret_cast<int*>(smem + C::OFF_LIM) + warp * 2 * kRowsR,
                            reinterpret_cast<float4*>(smem + C::OFF_X) + (warp / SPLIT) * (SPLIT * 128),
                            bars + C::WARPS * C::STAGES + warp / SPLIT, &abort_flag);
   if (beside) pdl_wait();
