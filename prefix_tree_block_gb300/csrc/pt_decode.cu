@@ -49,8 +49,10 @@ struct alignas(sizeof(E) * V) VecOf {
 // adds one half of the values to the partner's and keeps the other, 16
 // shuffles for 16 sums where a butterfly for each would take 80, and lane l
 // ends with row l/8, token (l/2) mod 4 of the group.  The softmax then runs on
-// eight lanes a row.  Bound by memory for the four rows of a small group:
-// about 28 instructions a token at head_dim 64, 512 bytes of keys and values.
+// eight lanes a row.  About 28 instructions a token at head_dim 64 for 512
+// bytes of fp32 keys and values.  Documents: 542 MB at head_dim 128, groups of
+// two heads, 118 us (68% of the copy's bandwidth); 136 MB at 64, groups of
+// three, 47 us (43%: bound by issue).
 // ---------------------------------------------------------------------------
 template <class E, int DL, int VEC>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {
@@ -210,9 +212,9 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 // divides the group and a row tile), so the pieces are looked up once for all
 // of them, the path's entries side by side, one per lane.  W warps share a
 // unit, each takes every W-th piece, lanes the columns; several pieces are
-// loaded at a time.  With many rows a unit gets one warp and up to four heads
-// (the lookup's instructions bound it otherwise: 8192 rows took 48 us with four
-// warps for each row); with few, four warps and one head (latency).
+// loaded at a time.  With few rows a unit gets four warps and one head (latency);
+// with many, one warp and, with the most, four heads: the lookup's
+// instructions bound it then.
 // ---------------------------------------------------------------------------
 struct MergeArgs {
   DecArgs d;
@@ -311,6 +313,7 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
 template <class E, int VEC, int NV, int GH, int W>
 __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
   __shared__ float sm_m[W][GH], sm_l[W][GH];
+  static_assert(W == 1 || W == 4, "a CTA is four warps");
   __shared__ VecOf<float, VEC> sm_o[W == 1 ? 1 : W][W == 1 ? 1 : GH][W == 1 ? 1 : NV * 32];
   const DecArgs& a = m.d;
   const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
@@ -491,10 +494,12 @@ cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t sm
   return D % 4 ? go(k_decode_simt<E, 16, 1>) : go(k_decode_simt<E, 16, 4>);
 }
 
-// From this many rows on, a merge unit is four heads on one warp (8192 rows: 14
-// us, 20 with four warps, 48 with four warps for each row); where the group has
-// no multiple of four, one head on one warp from four times as many.
-constexpr int kMergeManyRows = 4096;
+// Rows of a call: below the first number a merge unit is one head on four warps
+// (1024 rows of the 2 x 4096-token batch: the whole call 35 us, 39 with a warp
+// each), from it on one head on one warp (4096 rows: 95 us, 104 with four
+// warps, 99 with four heads a warp), and from the second on four heads on one
+// warp where they divide the group (8192 rows: 57 us, 62 with one head).
+constexpr int kMergeManyRows = 4096, kMergeMostRows = 8192;
 
 template <class E, int GH, int W>
 cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
@@ -511,9 +516,9 @@ cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
 template <class E>
 cudaError_t launch_merge(const MergeArgs& m, cudaStream_t s) {
   const long long rows = (long long)m.n_samples * m.d.q_len * m.d.Hq;
-  const bool heads = m.d.g % 4 == 0 && m.d.D <= 256 && rows >= kMergeManyRows;
+  const bool heads = m.d.g % 4 == 0 && m.d.D <= 256 && rows >= kMergeMostRows;
   if (heads) return launch_merge<E, 4, 1>(m, s);
-  return rows < 4 * kMergeManyRows ? launch_merge<E, 1, 4>(m, s) : launch_merge<E, 1, 1>(m, s);
+  return rows < kMergeManyRows ? launch_merge<E, 1, 4>(m, s) : launch_merge<E, 1, 1>(m, s);
 }
 
 }  // namespace

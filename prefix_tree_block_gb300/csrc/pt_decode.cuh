@@ -42,7 +42,7 @@ enum : int {
   kDecTile = 3,     // tcgen05: the rest
   kDecClasses = 4
 };
-constexpr DecTiling kSimt = {2, 4, 0};  // a warp per worker
+constexpr DecTiling kSimt = {2, 4, 1};  // a warp per worker
 constexpr DecTiling kRows = {4, 4, 2};  // a warp per worker
 constexpr DecTiling kTile = {8, 7, 4};  // a CTA per worker; an item of up to 128 rows has two partial results
 constexpr int kSimtR = 1 << kSimt.r, kSimtBT = 1 << kSimt.t;
@@ -54,12 +54,12 @@ constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
 // both kernels then start later than the one alone.  128 tokens of an item take
 // an SM about 0.9 us for each tile of 16 rows, or 1.1 us for 128 rows and 2.2
 // for 256; kTileMinGain is in such us, over the tokens of a full table row.
-// Two prompts of 1024 tokens, 64 samples, 32 q heads over 8: 55 us on rows
-// alone, 36 with tiles; a depth-3 tree of 1024 + 512 tokens, 16 samples, 16 q
-// heads over 4: 16 and 20 us; two prompts of 4096 tokens, 16 samples, 32 over
-// 8: 39 and 40.
+// 32 q heads over 8, head_dim 128, us on rows alone and with tiles: two prompts
+// of 1024 tokens, 64 samples (gain 1560) 35 and 41; of 4096 tokens, 16 samples
+// (1280) 35 and 40; four of 4096, 16 samples (2560) 47 and 43; two of 2048, 64
+// samples (3120) 52 and 42; two of 32768, 64 samples 629 and 168.
 constexpr int kTileMinRows = 33, kTileMaxD = 128;
-constexpr float kTileMinGain = 1500.f;
+constexpr float kTileMinGain = 2000.f;
 // Element (row, column) of a tile-class partial result: groups of 8 columns, in
 // each the rows one after another (D is a multiple of 8 there).
 __host__ __device__ inline long long tile_at(int D, long long slot, int row, int col) {

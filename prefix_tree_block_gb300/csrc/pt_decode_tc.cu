@@ -53,29 +53,34 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // a warp per worker; at head dims over 128, SPLIT = 2 or 4 warps, 128 columns
 // each.
 //
-// A step's work is 32 NP mma for 16 x 128 NP bytes of keys and values: the
+// A step's work is 32 NP mma for 16 x 256 NP bytes of keys and values: the
 // kernel is bound by memory, and what matters is that every SM keeps enough
-// bytes in flight (more than that only queue: three stages a warp instead of
-// two cost 4% at head_dim 128) and that no warp waits for another.  So each
-// warp has its own ring of stages (16 tokens of K and V, 64-column panels,
-// 128-byte swizzle), fills it by TMA itself (a box is 16 tokens of one page)
-// and computes on what has arrived; nothing but the walk's sums is shared.  The
-// loads run up to a ring ahead of the arithmetic, across the ends of pieces.
+// bytes in flight (three stages a warp instead of two, which leaves fewer
+// workers, cost 1% to 12% at head_dim 128) and that no warp waits for another.
+// So each warp has its own ring of stages (16 tokens of K and V, 64-column
+// panels, 128-byte swizzle), fills it by TMA itself (a box is 16 tokens of one
+// page) and computes on what has arrived; nothing but the walk's sums is
+// shared.  The loads run up to a ring ahead of the arithmetic, across the ends
+// of pieces.
 // With a piece's first load its query rows are gathered too, so that they are
 // there when the piece begins.
 //   S = Q K^T: both operands' fragments come by ldmatrix.
 //   O += P V: P is the bf16 of S's own registers (the accumulator's layout is
 //   the A operand's), V's fragments come by ldmatrix.trans.
+// P's rounding to bf16 (up to 2^-8 of each weight, as in the forward) is what
+// the tensor cores' operands cost; sums, maxima, O and the partial results are fp32.
 // The warps of a SPLIT worker add up their parts of S through shared memory,
 // each in the same order, and then hold the same P; O's columns stay apart.
-// (16384 units at head_dim 256, 268 MB: 51 us; 60 with one warp for all columns,
-// which has to spill.)  The running maximum is followed in steps of 2^8, as in the forward.
+// The running maximum is followed in steps of 2^8, as in the forward.
+// Documents read once: 1.07 GB at head_dim 128 173 us (91% of the copy's
+// bandwidth), 268 MB at 256 51 us (78%; 60 us with one warp for all columns,
+// which has to spill), 134 MB at 64 in pages of 16 tokens 32 us (62%).
 // ---------------------------------------------------------------------------
 template <int NP, int SPLIT>
 struct RowsCfg {
   static constexpr int WARPS = SPLIT == 1 && NP == 2 ? 3 : 4, GROUPS = WARPS / SPLIT;  // GROUPS workers a CTA
   static constexpr int CTAS = SPLIT == 1 ? 3 : 2;                                      // per SM
-  static constexpr int STAGES = NP == 1 ? 3 : 2;
+  static constexpr int STAGES = 2;
   static constexpr int PANEL = 16 * 128;            // bytes: 16 tokens (or rows) x 64 columns
   static constexpr int STAGE = 2 * NP * PANEL;      // K panels, V panels
   static constexpr int QBUF = NP * PANEL;           // a piece's query rows
@@ -496,6 +501,12 @@ __global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SP
 // step u belongs to warpgroup u & 1 and tile u >> pair.  S of step u is issued
 // after PV of step u - 2 of the same warpgroup, so the commit of S(u) also says
 // that O may be rescaled.  Warps without rows only keep the barriers moving.
+// 943 MB of prompts and continuations, two prompts of 32768 tokens under 64
+// samples of 512 to 2048 more, 32 q heads over 8: 169 us for the call (82% of
+// the copy's bandwidth), 629 on rows alone; drafts of 16 tokens behind 32
+// continuations of prompts of 4096, 16 q heads over 4, where 64 rows read every
+// token of a continuation and 1024 a prompt: 56 us, 131 on rows alone.
+// P is rounded to bf16 as above.
 // Tokens behind the segment's last are zero-filled by TMA where a whole box
 // lies behind it; inside a box the threads clear V's rows, so that nothing
 // stored there reaches O.
