@@ -1645,10 +1645,6 @@ struct DqpBars {
   uint64_t acc_full, acc_free, mma_done;
 };
 
-// 64-bit shared-memory descriptor plus a byte offset that keeps the address
-// below 256 KB (no carry out of the 14-bit start-address field).
-__device__ __forceinline__ uint64_t sdesc_add(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
-
 template <int D>
 __global__ void __launch_bounds__(DqpCfg<D>::THREADS, 1)
     k_bwd_dq_pipe(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mdO,

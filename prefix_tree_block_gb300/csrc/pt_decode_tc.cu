@@ -683,20 +683,28 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     __syncwarp();
   };
 
-  const auto mma_role = [&]() {
+  const auto mma_role = [&]() {  // lane 0
     constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
     constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
-    const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
-    DecPiece p;
-    uint32_t n = 0, it = 0;       // tiles before this piece; pieces
-    uint32_t pc[2] = {0, 0};      // PV steps per warpgroup
-    uint32_t oc[2] = {0, 0};      // pieces in which the warpgroup had steps
+    // (each product's descriptors by an addition: built anew, what issues them would take longer than they do)
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t dK = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+    const uint64_t dV = sdesc_sw128(smem_u32(smem + C::OFF_V), C::PANEL, 1024);
+    uint32_t n = 0, it = 0;   // tiles before this piece; pieces
+    uint32_t pc[2] = {0, 0};  // PV steps per warpgroup
+    uint32_t oc[2] = {0, 0};  // pieces in which the warpgroup had steps
     bool ok = true;
 #pragma unroll 1
-    while (ok && get_piece(p, it)) {
-      const int pair = p.rows - p.rt * kTileR > kTileR / 2 ? 1 : 0;
-      const int tiles = p.t1 - p.t0, steps = tiles << pair;
-      ok = __all_sync(0xffffffffu, mbar_wait(q_full, it & 1, abort_flag));
+    while (ok) {
+      const uint32_t pi = it % C::PIECES;
+      if (!mbar_wait(piece_full + pi, (it / C::PIECES) & 1, abort_flag)) break;
+      const int left = pieces[pi].rows - pieces[pi].rt * kTileR, tiles = pieces[pi].t1 - pieces[pi].t0;
+      const bool end = pieces[pi].rows <= 0;
+      mbar_arrive(piece_empty + pi);
+      if (end) break;
+      const int pair = left > kTileR / 2 ? 1 : 0, steps = tiles << pair;
+      ok = mbar_wait(q_full, it & 1, abort_flag);
+      tc_fence_after();
 #pragma unroll 1
       for (int u0 = 0; u0 < steps + 2 && ok; u0 += 2) {
 #pragma unroll
@@ -704,39 +712,34 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
           const int u = u0 + h;
           if (u >= 2 && u < steps + 2) {  // PV of step u - 2
             const uint32_t x = n + ((u - 2) >> pair), vs = x % C::VS;
+            const uint64_t dv = sdesc_add(dV, vs * C::TILE);
             ok = mbar_wait(p_full + h, pc[h] & 1, abort_flag) && mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
             if (u < 4 && oc[h] > 0) ok = ok && mbar_wait(o_free + h, (oc[h] - 1) & 1, abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tbase + C::TM_O + h * D, tbase + C::TM_S + h * 128 + kk * 8,
-                       sdesc_sw128(sV + vs * C::TILE + kk * 2048, C::PANEL, 1024), IDESC_PV, u >= 4 || kk > 0);
-              if (!pair || h == 1) mma_commit(v_empty + vs);
-              if (u >= steps) mma_commit(o_full + h);  // the warpgroup's last
-            }
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tbase + C::TM_O + h * D, tbase + C::TM_S + h * 128 + kk * 8, sdesc_add(dv, kk * 2048), IDESC_PV,
+                     u >= 4 || kk > 0);
+            if (!pair || h == 1) mma_commit(v_empty + vs);
+            if (u >= steps) mma_commit(o_full + h);  // the warpgroup's last
             ++pc[h];
           }
           if (u < steps) {
             const uint32_t x = n + (u >> pair), ks = x % C::KS;
+            const uint64_t dq = sdesc_add(dQ, pair ? h * C::TILE : 0), dk = sdesc_add(dK, ks * C::TILE);
             ok = mbar_wait(k_full + ks, (x / C::KS) & 1, abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t qa = sQ + (pair ? h * C::TILE : 0);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
-                mma_ss(tbase + C::TM_S + h * 128, sdesc_sw128(qa + off, 16, 1024),
-                       sdesc_sw128(sK + ks * C::TILE + off, 16, 1024), IDESC_S, kk > 0);
-              }
-              mma_commit(s_full + h);
-              if (!pair || h == 1) mma_commit(k_empty + ks);
-              if (u == steps - 1) mma_commit(q_empty);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
+              mma_ss(tbase + C::TM_S + h * 128, sdesc_add(dq, off), sdesc_add(dk, off), IDESC_S, kk > 0);
             }
+            mma_commit(s_full + h);
+            if (!pair || h == 1) mma_commit(k_empty + ks);
+            if (u == steps - 1) mma_commit(q_empty);
           }
-          __syncwarp();
         }
       }
       n += tiles;
@@ -744,11 +747,8 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
       if (steps > 0) ++oc[0];
       if (steps > 1) ++oc[1];
     }
-    if (lane == 0) {
-      mma_commit(done);
-      mbar_wait_drain(done, 0, 200000000);
-    }
-    __syncwarp();
+    mma_commit(done);
+    mbar_wait_drain(done, 0, 200000000);
   };
 
   // Gathers an item's query rows into the Q tiles, warp w of every `nw`: 16-byte
@@ -950,9 +950,10 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     regs_dec<C::REG_CTRL>();
     if (warp == 8)
       producer_role();
-    else if (warp == 9)
-      mma_role();
-    else
+    else if (warp == 9) {
+      if (lane == 0) mma_role();
+      __syncwarp();
+    } else
       query_role();
   } else {
     regs_inc<C::REG_SOFTMAX>();

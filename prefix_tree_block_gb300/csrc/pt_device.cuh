@@ -263,6 +263,10 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// 64-bit shared-memory descriptor plus a byte offset that keeps the address
+// below 256 KB (no carry out of the 14-bit start-address field).
+__device__ __forceinline__ uint64_t sdesc_add(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 // TMEM loads/stores, 32 lanes x 32 bits, 32 consecutive columns per call.
 // Thread i of a warp reads lane (lane base of the warp's sub-partition + i).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
