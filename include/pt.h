@@ -513,8 +513,8 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   PT_ERR_INVALID_ARG also for a workspace that is too small, a plan of
  *   another device or a bad stride, PT_ERR_UNSUPPORTED when the work items (row
  *   tiles of 16 query heads' rows, or fewer, times kv heads, over all nodes)
- *   times the 16-token tiles of a full table row pass 2^31 - 1.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a length
- *   outside [0, max_pages * page_size] or a count outside [0, q_len] (the
+ *   times the 16-token tiles of a full table row pass 2^31 - 1.  On the device
+ *   (pt_sync_status), PT_ERR_INVALID_ARG: a length outside [0, max_pages * page_size] or a count outside [0, q_len] (the
  *   nearest is taken), a page id outside [0, n_pages) (page 0 is read).
  * ------------------------------------------------------------------------- */
 typedef struct pt_decodeplan pt_decodeplan;

@@ -57,7 +57,7 @@ constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
 // 32 q heads over 8, head_dim 128, us on rows alone and with tiles: two prompts
 // of 1024 tokens, 64 samples (gain 1560) 35 and 41; of 4096 tokens, 16 samples
 // (1280) 35 and 40; four of 4096, 16 samples (2560) 47 and 43; two of 2048, 64
-// samples (3120) 52 and 42; two of 32768, 64 samples 629 and 168.
+// samples (3120) 52 and 41; two of 32768, 64 samples 629 and 165.
 constexpr int kTileMinRows = 33, kTileMaxD = 128;
 constexpr float kTileMinGain = 2000.f;
 // Element (row, column) of a tile-class partial result: groups of 8 columns, in
