@@ -514,8 +514,9 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   another device or a bad stride, PT_ERR_UNSUPPORTED when the work items (row
  *   tiles of 16 query heads' rows, or fewer, times kv heads, over all nodes)
  *   times the 16-token tiles of a full table row pass 2^31 - 1.  On the device
- *   (pt_sync_status), PT_ERR_INVALID_ARG: a length outside [0, max_pages * page_size] or a count outside [0, q_len] (the
- *   nearest is taken), a page id outside [0, n_pages) (page 0 is read).
+ *   (pt_sync_status), PT_ERR_INVALID_ARG: a length outside [0, max_pages *
+ *   page_size] or a count outside [0, q_len] (the nearest is taken), a page id
+ *   outside [0, n_pages) (page 0 is read).
  * ------------------------------------------------------------------------- */
 typedef struct pt_decodeplan pt_decodeplan;
 pt_status pt_cache_tables(const int32_t* held, const int32_t* added, const int32_t* start, int32_t n_rows,

@@ -21,7 +21,7 @@ def lib():
 def _tables(lib, **kw):
     buf = np.zeros(1 << 12, np.int64)
     p = buf.ctypes.data
-    a = dict(held=p, added=p + 512, start=None, n=4, ps=16, tables=p + 1024, mp=4, ring=p + 2048, cap=8, ctr=p + 2560, lens=p + 3072,
+    a = dict(held=p, added=p + 512, start=None, n=4, ps=16, tables=p + 1024, mp=4, ring=p + 2048, cap=8, ctr=p + 2560, lens=p + 16384,
              row_ptr=p + 3584, slots=p + 4096, pos=p + 8192, new=32, out=p + 12288)
     a.update(kw)
     return lib.pt_cache_tables(*a.values(), None)
