@@ -64,7 +64,7 @@ def test_trees(tree, Hq, Hkv, D, dtype, ps):
     lens, paths = TREES[tree]
     _run(lens, paths, Hq, Hkv, D, dtype, ps, seed=3)
     if dtype == BF:  # tables wide enough for nodes that many rows read to take the tile kernel
-        _run(lens, paths, Hq, Hkv, D, dtype, ps, seed=3, width=8192 // ps)
+        _run(lens, paths, Hq, Hkv, D, dtype, ps, seed=3, width=65536 // ps)
 
 
 @pytest.mark.parametrize("D,dtype", [(1, F32), (31, F32), (33, F32), (66, F32), (128, F32), (130, F32), (256, F32), (257, F32), (512, F32),
@@ -80,7 +80,7 @@ def test_page_sizes(ps, dtype):
     lens, paths = TREES["crowd"]
     _run(lens, paths, 4, 2, 64, dtype, ps, seed=ps)
     if dtype == BF:
-        _run(lens, paths, 4, 2, 64, dtype, ps, seed=ps, width=-(-8192 // ps))
+        _run(lens, paths, 4, 2, 64, dtype, ps, seed=ps, width=-(-65536 // ps))
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 1), (32, 1), (71, 1), (8, 8), (7, 7), (24, 8), (40, 4)])
@@ -89,7 +89,7 @@ def test_head_layouts(Hq, Hkv, dtype):
     lens, paths = TREES["group"]
     _run(lens, paths, Hq, Hkv, 64, dtype, 16, seed=Hq)
     if dtype == BF:
-        _run(lens, paths, Hq, Hkv, 64, dtype, 16, seed=Hq, width=512)
+        _run(lens, paths, Hq, Hkv, 64, dtype, 16, seed=Hq, width=4096)
 
 
 @pytest.mark.parametrize("q_len", [2, 5, 16, 33])
@@ -100,7 +100,7 @@ def test_several_queries(q_len, tree, Hq, Hkv, D, dtype):
     lens, paths = TREES[tree]
     _run(lens, paths, Hq, Hkv, D, dtype, 16, q_len=q_len, seed=q_len)
     if dtype == BF:
-        _run(lens, paths, Hq, Hkv, D, dtype, 16, q_len=q_len, seed=q_len, width=512)
+        _run(lens, paths, Hq, Hkv, D, dtype, 16, q_len=q_len, seed=q_len, width=4096)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -108,7 +108,7 @@ def test_several_queries(q_len, tree, Hq, Hkv, D, dtype):
 def test_query_counts(dtype, q_len):
     """Samples with fewer queries than q_len, or none: their rows stay."""
     lens, paths = TREES["crowd"]
-    _run(lens, paths, 4, 2, 64, dtype, 16, q_len=q_len, q_count=[(i * 7) % (q_len + 1) for i in range(len(paths))], seed=2, width=512)
+    _run(lens, paths, 4, 2, 64, dtype, 16, q_len=q_len, q_count=[(i * 7) % (q_len + 1) for i in range(len(paths))], seed=2, width=4096)
     lens, paths = TREES["deep"]
     _run(lens, paths, 4, 2, 64, dtype, 16, q_len=q_len, q_count=[0] * len(paths), seed=2)
 
@@ -130,7 +130,7 @@ def test_a_later_drafts_nan_stays_with_it(dtype, Hq, what):
     """A token whose key or value is NaN reaches the queries that keep it only."""
     lens, paths, q_len, ps, D = [50, 40, 21], [[0, 1], [0, 2]], 6, 16, 64
     rng = np.random.default_rng(0)
-    tables, n_pages = pages_of(lens, ps, rng, width=256)
+    tables, n_pages = pages_of(lens, ps, rng, width=2048)
     Kc, Vc = cache_of(lens, tables, n_pages, 2, ps, D, dtype, 0)
     s = OD.slots_of(tables[1], 40, ps)[37]  # the third draft token of sample 0
     (Kc if what == "K" else Vc)[s // ps, :, s % ps] = float("nan")
@@ -176,7 +176,7 @@ def test_query_rows_between_16_byte_boundaries(extra):
     """A node that many rows read, with query tokens of every alignment allowed."""
     lens, paths = TREES["crowd"]
     Hq, Hkv, D, ps = 4, 2, 64, 16
-    tables, n_pages = pages_of(lens, ps, np.random.default_rng(1), width=512)
+    tables, n_pages = pages_of(lens, ps, np.random.default_rng(1), width=4096)
     Kc, Vc = cache_of(lens, tables, n_pages, Hkv, ps, D, BF, 1)
     x = torch.randn(len(paths), Hq * D + extra, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
     Q = x.as_strided((len(paths), Hq, D), (Hq * D + extra, D, 1), extra)
@@ -230,7 +230,7 @@ def test_own_nodes_that_many_rows_read(q_len, D):
     lens = [1000] + [int(x) for x in rng.integers(130, 900, 40)]
     paths = [[0, i] for i in range(1, 41)]
     Hq, Hkv, ps = 32, 4, 32
-    tables, n_pages = pages_of(lens, ps, rng, width=512)
+    tables, n_pages = pages_of(lens, ps, rng, width=4096)
     Kc, Vc = (c.cuda() for c in cache_of(lens, tables, n_pages, Hkv, ps, D, BF, 1))
     Q = torch.randn(40 * q_len, Hq, D, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
     plan = pt.decode_plan(len(lens), *csr(paths), Hq, Hkv, q_len)
@@ -247,9 +247,9 @@ def test_own_nodes_that_many_rows_read(q_len, D):
 
 def test_samples_that_end_at_one_node():
     """Only nodes that many rows read: no work for the other kernel."""
-    _run([700], [[0]] * 80, 4, 2, 128, BF, 16, seed=4, width=1024)
-    _run([700], [[0]] * 80, 4, 2, 128, BF, 16, q_len=3, seed=4, width=1024)
-    _run([300, 5], [[0, 1]] * 300, 2, 1, 64, BF, 16, seed=4, width=4096)
+    _run([700], [[0]] * 80, 4, 2, 128, BF, 16, seed=4, width=8192)
+    _run([700], [[0]] * 80, 4, 2, 128, BF, 16, q_len=3, seed=4, width=8192)
+    _run([300, 5], [[0, 1]] * 300, 2, 1, 64, BF, 16, seed=4, width=32768)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -282,7 +282,7 @@ def test_too_much_work_is_refused():
 def test_two_calls_at_once():
     """Two streams, each with its own workspace, over one cache and one plan."""
     lens, paths = [2500] + [40 + i for i in range(40)], [[0, i] for i in range(1, 41)]
-    tables, n_pages = pages_of(lens, 64, np.random.default_rng(1), width=256)
+    tables, n_pages = pages_of(lens, 64, np.random.default_rng(1), width=2048)
     Kc, Vc = (c.cuda() for c in cache_of(lens, tables, n_pages, 2, 64, 128, BF, 1))
     plan = pt.decode_plan(len(lens), *csr(paths), 16, 2)
     t, n = torch.from_numpy(tables).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
