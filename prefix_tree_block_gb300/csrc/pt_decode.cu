@@ -233,28 +233,29 @@ struct MergeAcc {
   int turn;  // pieces so far, modulo the warps
 };
 
-// The pieces of up to 32 path entries in one class (lane i: node, its segment
-// and length, the sample's place among the node's).
-template <int VEC, int NV, int GH, int W>
-__device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int node, const DecSeg& sg, int raw, int mem,
+// The pieces of as many path entries as the lanes hold, one per lane: node, its
+// segment and length, the sample's place among the node's.  With TWO classes the
+// upper half of the lanes holds the same entries in the tile class (both in one
+// pass: 16-token drafts 56.1 -> 54.0 us, 32768-token prompts 165.6 -> 163.4).
+template <int VEC, int NV, int GH, int W, bool TWO>
+__device__ __forceinline__ void merge_pieces(const MergeArgs& m, int node, const DecSeg& sg, int raw, int mem,
                                             int j, int hk, int h0, int warp, int lane, MergeAcc<VEC, NV, GH>& s) {
   using V = VecOf<float, VEC>;
   const DecArgs& a = m.d;
-  const int* pref = tile ? m.c1.pref : m.c0.pref;
-  const float* lse = tile ? m.c1.lse : m.c0.lse;
-  const float* opart = tile ? m.c1.opart : m.c0.opart;
-  const int rl = tile ? kTile.r : m.g0.r, bl = tile ? kTile.t : m.g0.t;
+  const bool mine = TWO && lane >= 16;  // this lane's entry is of the tile class
+  const int* pref = mine ? m.c1.pref : m.c0.pref;
   int count = 0, two = 0;
   int row0 = 0;  // the row in the first piece, over all slots
   if (sg.rows_kind) {
+    const int rl = mine ? kTile.r : m.g0.r, bl = mine ? kTile.t : m.g0.t;
     const int before = pref[node], per = pref[m.c0.nseg];
     int b, e;
     dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
     const int tiles = (e - b + (1 << bl) - 1) >> bl;
     if (tiles > 0) {
       const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
-      two = tile && sg.rows() - (rt << rl) <= kTileR / 2;
-      const int nu = dec_line(DecTiling{rl, bl, tile ? kTile.k : m.g0.k}, sg.rows(), tiles);
+      two = mine && sg.rows() - (rt << rl) <= kTileR / 2;
+      const int nu = dec_line(DecTiling{rl, bl, mine ? kTile.k : m.g0.k}, sg.rows(), tiles);
       const unsigned u0 = before + it * nu, w0 = u0 / (unsigned)per, w1 = (u0 + nu - 1) / (unsigned)per;
       row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
       count = (int)(w1 - w0 + 1) << two;
@@ -267,8 +268,6 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
     if (lane >= o) incl += u;
   }
   const int excl = incl - count, total = __shfl_sync(0xffffffffu, incl, 31);
-  // a row's columns: groups of 8, far apart in the tile class and side by side in the others
-  const int row_step = tile ? 8 : a.D, col_step = tile ? kTileR * 8 : 8;
   constexpr int U = GH * NV * VEC > 8 ? 2 : 4;  // pieces in flight
 #pragma unroll 1
   for (int x0 = W == 1 ? 0 : (warp - s.turn) & (W - 1); x0 < total; x0 += W * U) {
@@ -279,9 +278,13 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
       const int x = min(x0 + W * u, total - 1);
       const int l = 31 - __clz(__ballot_sync(0xffffffffu, excl <= x));
       const int y = x - __shfl_sync(0xffffffffu, excl, l), tw = __shfl_sync(0xffffffffu, two, l);
+      const bool tile = TWO && l >= 16;
+      const int rl = tile ? kTile.r : m.g0.r;
+      // a row's columns: groups of 8, far apart in the tile class and side by side in the others
+      const int row_step = tile ? 8 : a.D, col_step = tile ? kTileR * 8 : 8;
       const int at = __shfl_sync(0xffffffffu, row0, l) + ((y >> tw) << rl) + (y & tw) * (kTileR / 2);
       const bool in = x0 + W * u < total;
-      const float* src = opart + (long long)(at >> rl) * (a.D << rl) + (at & ((1 << rl) - 1)) * row_step;
+      const float* src = (tile ? m.c1.opart : m.c0.opart) + (long long)(at >> rl) * (a.D << rl) + (at & ((1 << rl) - 1)) * row_step;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = (i * 32 + lane) * VEC;
@@ -290,7 +293,7 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
         for (int h = 0; h < GH; ++h) o[u][h][i] = in && col < a.D ? *reinterpret_cast<const V*>(from + h * row_step) : V{};
       }
 #pragma unroll
-      for (int h = 0; h < GH; ++h) ls[u][h] = in ? lse[at + h] : -INFINITY;
+      for (int h = 0; h < GH; ++h) ls[u][h] = in ? (tile ? m.c1.lse : m.c0.lse)[at + h] : -INFINITY;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -310,8 +313,13 @@ __device__ __forceinline__ void merge_class(const MergeArgs& m, bool tile, int n
   s.turn = (s.turn + total) & (W - 1);
 }
 
-template <class E, int VEC, int NV, int GH, int W>
-__global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
+// CTAs per SM: said so that the loads of a round get registers of their own
+// (without it the compiler saves some and one round becomes several: documents
+// at head_dim 256 17.5 -> 16.6 us, GRPO batch 12.3 -> 11.6).
+constexpr int merge_ctas(int floats) { return floats <= 4 ? 7 : floats <= 8 ? 4 : 1; }
+
+template <class E, int VEC, int NV, int GH, int W, bool TWO>
+__global__ void __launch_bounds__(128, merge_ctas(GH* NV* VEC)) k_decode_merge(const MergeArgs m) {
   __shared__ float sm_m[W][GH], sm_l[W][GH];
   static_assert(W == 1 || W == 4, "a CTA is four warps");
   __shared__ VecOf<float, VEC> sm_o[W == 1 ? 1 : W][W == 1 ? 1 : GH][W == 1 ? 1 : NV * 32];
@@ -328,15 +336,18 @@ __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
   // launched after all that came before them had ended.
   const int k0 = m.path_ptr[s], k1 = m.path_ptr[s + 1];
   int2 en = make_int2(0, 0);
-  DecSeg sg[2] = {DecSeg{0, 0, 0, -1}, DecSeg{0, 0, 0, -1}};
+  DecSeg sg = DecSeg{0, 0, 0, -1};
   int raw = 0;
+  constexpr int AT_ONCE = TWO ? 16 : 32;  // path entries
+  const DecSeg* segs = TWO && lane >= 16 ? m.c1.seg : m.c0.seg;
+  const bool any = !TWO || (lane >= 16 ? m.c1.nitems : m.c0.nitems) > 0;
   auto look = [&](int k) {
-    sg[0].rows_kind = sg[1].rows_kind = 0;
-    if (k + lane < k1) {
-      en = m.path_ent[k + lane];
+    sg.rows_kind = 0;
+    const int at = k + (TWO ? lane & 15 : lane);
+    if (at < k1) {
+      en = m.path_ent[at];
       raw = a.lens[en.x];
-      if (m.c0.nitems) sg[0] = load_seg(m.c0.seg + en.x);
-      if (m.c1.nitems) sg[1] = load_seg(m.c1.seg + en.x);
+      if (any) sg = load_seg(segs + en.x);
     }
   };
   look(k0);
@@ -358,10 +369,8 @@ __global__ void __launch_bounds__(128) k_decode_merge(const MergeArgs m) {
   }
 #pragma unroll 1
   for (int k = k0;;) {
-#pragma unroll 1
-    for (int cls = m.c0.nitems ? 0 : 1; cls < (m.c1.nitems ? 2 : 1); ++cls)
-      merge_class<VEC, NV, GH, W>(m, cls == 1, en.x, cls ? sg[1] : sg[0], raw, en.y, j, hk, h0, warp, lane, r);
-    k += 32;
+    merge_pieces<VEC, NV, GH, W, TWO>(m, en.x, sg, raw, en.y, j, hk, h0, warp, lane, r);
+    k += AT_ONCE;
     if (k >= k1) break;
     look(k);
   }
@@ -501,24 +510,29 @@ cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t sm
 // warp where they divide the group (8192 rows: 57 us, 62 with one head).
 constexpr int kMergeManyRows = 4096, kMergeMostRows = 8192;
 
-template <class E, int GH, int W>
+template <class E, int GH, int W, bool TWO>
 cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
   m.units = m.n_samples * m.d.q_len * (m.d.Hq / GH);
   const int grid = W == 1 ? (m.units + 3) / 4 : m.units, D = m.d.D;
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(128), 0, s, m); };
-  if (D <= 32) return go(k_decode_merge<E, 1, 1, GH, W>);
-  if (D <= 64) return D % 2 ? go(k_decode_merge<E, 1, 2, GH, W>) : go(k_decode_merge<E, 2, 1, GH, W>);
-  if (D <= 128) return D % 4 ? go(k_decode_merge<E, 1, 4, GH, W>) : go(k_decode_merge<E, 4, 1, GH, W>);
-  if (D <= 256) return D % 4 ? go(k_decode_merge<E, 1, 8, GH, W>) : go(k_decode_merge<E, 4, 2, GH, W>);
-  return D % 4 ? go(k_decode_merge<E, 1, 16, GH, W>) : go(k_decode_merge<E, 4, 4, GH, W>);
+  if (D <= 32) return go(k_decode_merge<E, 1, 1, GH, W, TWO>);
+  if constexpr (TWO) {  // (bf16 up to kTileMaxD, a multiple of 8)
+    if (D <= 64) return go(k_decode_merge<E, 2, 1, GH, W, TWO>);
+    return go(k_decode_merge<E, 4, 1, GH, W, TWO>);
+  } else {
+    if (D <= 64) return D % 2 ? go(k_decode_merge<E, 1, 2, GH, W, TWO>) : go(k_decode_merge<E, 2, 1, GH, W, TWO>);
+    if (D <= 128) return D % 4 ? go(k_decode_merge<E, 1, 4, GH, W, TWO>) : go(k_decode_merge<E, 4, 1, GH, W, TWO>);
+    if (D <= 256) return D % 4 ? go(k_decode_merge<E, 1, 8, GH, W, TWO>) : go(k_decode_merge<E, 4, 2, GH, W, TWO>);
+    return D % 4 ? go(k_decode_merge<E, 1, 16, GH, W, TWO>) : go(k_decode_merge<E, 4, 4, GH, W, TWO>);
+  }
 }
 
-template <class E>
+template <class E, bool TWO>
 cudaError_t launch_merge(const MergeArgs& m, cudaStream_t s) {
   const long long rows = (long long)m.n_samples * m.d.q_len * m.d.Hq;
   const bool heads = m.d.g % 4 == 0 && m.d.D <= 256 && rows >= kMergeMostRows;
-  if (heads) return launch_merge<E, 4, 1>(m, s);
-  return rows < kMergeManyRows ? launch_merge<E, 1, 4>(m, s) : launch_merge<E, 1, 1>(m, s);
+  if (heads) return launch_merge<E, 4, 1, TWO>(m, s);
+  return rows < kMergeManyRows ? launch_merge<E, 1, 4, TWO>(m, s) : launch_merge<E, 1, 1, TWO>(m, s);
 }
 
 }  // namespace
@@ -778,7 +792,9 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   m.path_ent = plan->path_ent;
   {
     ProfScope ps(stream, "decode_merge");
-    e = dtype == PT_BF16 ? launch_merge<__nv_bfloat16>(m, stream) : launch_merge<float>(m, stream);
+    e = dtype == PT_F32   ? launch_merge<float, false>(m, stream)
+        : m.c1.nitems ? launch_merge<__nv_bfloat16, true>(m, stream)
+                      : launch_merge<__nv_bfloat16, false>(m, stream);
     count_launch();
   }
   return (pt_status)launch_status(who, e);
