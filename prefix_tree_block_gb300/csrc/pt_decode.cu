@@ -504,11 +504,12 @@ cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t sm
 }
 
 // Rows of a call: below the first number a merge unit is one head on four warps
-// (1024 rows of the 2 x 4096-token batch: the whole call 35 us, 39 with a warp
-// each), from it on one head on one warp (4096 rows: 95 us, 104 with four
-// warps, 99 with four heads a warp), and from the second on four heads on one
-// warp where they divide the group (8192 rows: 57 us, 62 with one head).
-constexpr int kMergeManyRows = 4096, kMergeMostRows = 8192;
+// (1024 rows of the 2 x 4096-token batch: the whole call 34.6 us, 38.4 with a
+// warp each), from it on one head on one warp (2048 rows of four such prompts:
+// 39.1 us, 40.1 with four warps; 4096 rows: 86 us, 89 with four heads a warp),
+// and from the second on four heads on one warp where they divide the group
+// (8192 rows: 53.5 us, 55.9 with two heads).
+constexpr int kMergeManyRows = 2048, kMergeMostRows = 8192;
 
 template <class E, int GH, int W, bool TWO>
 cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
