@@ -14,6 +14,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 #include <vector>
 
 #include "pt.h"
@@ -51,8 +52,10 @@ struct alignas(sizeof(E) * V) VecOf {
 // ends with row l/8, token (l/2) mod 4 of the group.  The softmax then runs on
 // eight lanes a row.  About 28 instructions a token at head_dim 64 for 512
 // bytes of fp32 keys and values.  Documents: 542 MB at head_dim 128, groups of
-// two heads, 118 us (68% of the copy's bandwidth); 136 MB at 64, groups of
-// three, 47 us (43%: bound by issue).
+// two heads, 114 us (70% of the copy's bandwidth); 136 MB at 64, groups of
+// three, 47 us (43%: latency and issue).  Every four rows read a node again: seven
+// prompts of 7909 tokens under 62 samples, 124 rows a kv head, take 1167 us,
+// 12 TB/s out of L2.
 // ---------------------------------------------------------------------------
 template <class E, int DL, int VEC>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
     int b, e;
     dec_range(a, p.kind, p.len, b, e);
     float q[R][DL], acc[R][DL];
-    int lim_max = 0, my_lim = 0;
+    int lim_max = 0, lim_min = INT_MAX, my_lim = 0;  // (the least of the rows there are)
     int lim[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -85,6 +88,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       if (row < p.rows) {
         const DecRow d = dec_row(a, p.member0, p.hk, row, p.len);
         lim[r] = d.lim;
+        lim_min = min(lim_min, d.lim);
         src = Qp + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
       }
       lim_max = max(lim_max, lim[r]);
@@ -155,38 +159,46 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
       const float mn = fmaxf(m, mt), ref = mn == -INFINITY ? 0.f : mn;
-      const float al = ex2(m - ref);
+      const float al = mn == m ? 1.f : ex2(m - ref);
       m = mn;
       s[0] = ex2(s[0] - ref), s[1] = ex2(s[1] - ref);
       float sum = s[0] + s[1];
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       l = fmaf(l, al, sum);
+      if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float ar = __shfl_sync(0xffffffffu, al, r * 8);
+        for (int r = 0; r < R; ++r) {
+          const float ar = __shfl_sync(0xffffffffu, al, r * 8);
 #pragma unroll
-        for (int i = 0; i < DL; ++i) acc[r][i] *= ar;
-      }
-#pragma unroll
-      for (int i = 0; i < STEP; ++i) {
-        float pr[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) pr[r] = __shfl_sync(0xffffffffu, s[i >> 2], r * 8 + (i & 3) * 2);
-        const E* vp = static_cast<const E*>(a.Vc) + (EARLY ? 0 : __shfl_sync(0xffffffffu, off, i));
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int col = (v * 32 + lane) * VEC;
-          const V w = EARLY ? vv[EARLY ? i : 0][v] : col < a.D ? *reinterpret_cast<const V*>(vp + col) : V{};
-#pragma unroll
-          for (int x = 0; x < VEC; ++x)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
-              const float y = fmaf(pr[r], to_f(w.e[x]), acc[r][v * VEC + x]);
-              acc[r][v * VEC + x] = kv0 + i < lim[r] ? y : acc[r][v * VEC + x];
-            }
+          for (int i = 0; i < DL; ++i) acc[r][i] *= ar;
         }
       }
+      auto add_values = [&](auto masked) {
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+          float pr[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) pr[r] = __shfl_sync(0xffffffffu, s[i >> 2], r * 8 + (i & 3) * 2);
+          const E* vp = static_cast<const E*>(a.Vc) + (EARLY ? 0 : __shfl_sync(0xffffffffu, off, i));
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int col = (v * 32 + lane) * VEC;
+            const V w = EARLY ? vv[EARLY ? i : 0][v] : col < a.D ? *reinterpret_cast<const V*>(vp + col) : V{};
+#pragma unroll
+            for (int x = 0; x < VEC; ++x)
+#pragma unroll
+              for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
+                const float y = fmaf(pr[r], to_f(w.e[x]), acc[r][v * VEC + x]);
+                acc[r][v * VEC + x] = !masked || kv0 + i < lim[r] ? y : acc[r][v * VEC + x];
+              }
+          }
+        }
+      };
+      if (kv0 + STEP <= lim_min)  // every row sees all of them: half the instructions
+        add_values(std::false_type{});
+      else
+        add_values(std::true_type{});
     }
     // the piece's partial result
 #pragma unroll
