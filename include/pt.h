@@ -468,9 +468,9 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   PT_ERR_NOMEM when the ring runs out: the rows behind get no page, their
  *   tokens slot -1, and lens counts what fits in the pages they have.
  *   Errors on the host: PT_ERR_INVALID_ARG for NULL pointers, negative sizes,
- *   page_size or ring_cap below 1, max_new above 2^30, n_rows * max_pages
- *   above 2^31 - 1, or overlapping arrays; PT_ERR_UNSUPPORTED above 262144
- *   rows.
+ *   page_size or ring_cap below 1, ring_cap or max_new above 2^30, n_rows *
+ *   max_pages above 2^31 - 1, max_pages * page_size above 2^30 - 1, or
+ *   overlapping arrays; PT_ERR_UNSUPPORTED above 262144 rows.
  *
  * pt_cache_write: K and V [T, Hkv, D] (device, dtype; tokens k_stride and
  *   v_stride elements apart, a token's heads dense) into the slots
@@ -511,9 +511,10 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   CUDA cores.
  *   Errors: PT_ERR_INVALID_ARG and PT_ERR_UNSUPPORTED as for pt_attn_fwd,
  *   PT_ERR_INVALID_ARG also for a workspace that is too small, a plan of
- *   another device or a bad stride, PT_ERR_UNSUPPORTED when the work items (row
- *   tiles of 16 query heads' rows, or fewer, times kv heads, over all nodes)
- *   times the 16-token tiles of a full table row pass 2^31 - 1.  On the device
+ *   another device, a bad stride or max_pages * page_size above 2^30 - 1,
+ *   PT_ERR_UNSUPPORTED when the work items (row tiles of 16 query heads' rows,
+ *   or fewer, times kv heads, over all nodes) times the 16-token tiles of a
+ *   full table row pass 2^31 - 1.  On the device
  *   (pt_sync_status), PT_ERR_INVALID_ARG: a length outside [0, max_pages *
  *   page_size] or a count outside [0, q_len] (the nearest is taken), a page id
  *   outside [0, n_pages) (page 0 is read).

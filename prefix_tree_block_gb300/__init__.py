@@ -644,6 +644,8 @@ def cache_tables(held, added, tables, ring, counters, page_size: int, max_new: i
     added tokens' slots and position ids (int64 [max_new])."""
     _, i32, i64, _, _, _, device = _torch()
     n, cap = held.numel(), ring.numel()
+    if cap > 1 << 30:
+        raise ValueError(f"a ring of {cap} ids is out of range")
     row = (n,)
     dev = device() if held.is_cuda else -1
     _need(held, "held", i32, row, dev)

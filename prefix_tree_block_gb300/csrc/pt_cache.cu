@@ -27,6 +27,9 @@ namespace {
 constexpr int kTabWarps = 32;
 constexpr int kTabMaxRows = 1 << 18;  // 12 bytes of shared memory per 32 rows
 constexpr int kTabMaxNew = 1 << 30;
+// Ids of a ring: a place in it plus a count of pages below its size fits in 32
+// bits, and no page of it lies behind the sums' clamp.
+constexpr int kTabMaxRing = 1 << 30;
 
 // What a row does in this step, from its lengths.
 struct RowMove {
@@ -381,7 +384,7 @@ extern "C" pt_status pt_cache_tables(const int32_t* held, const int32_t* added, 
                                      int64_t* slots, int64_t* positions, int32_t max_new, int64_t* counters_out,
                                      cudaStream_t stream) {
   static const char* who = "pt_cache_tables";
-  if (n_rows < 0 || max_pages < 0 || max_new < 0 || ring_cap < 1 || page_size < 1) {
+  if (n_rows < 0 || max_pages < 0 || max_new < 0 || ring_cap < 1 || ring_cap > kTabMaxRing || page_size < 1) {
     set_error("%s: n_rows = %d, max_pages = %d, max_new = %d, ring_cap = %d or page_size = %d out of range", who,
               n_rows, max_pages, max_new, ring_cap, page_size);
     return PT_ERR_INVALID_ARG;
