@@ -403,7 +403,7 @@ extern "C" pt_status pt_cache_tables(const int32_t* held, const int32_t* added, 
     set_error("%s: a pointer is NULL", who);
     return PT_ERR_INVALID_ARG;
   }
-  // every CTA reads the inputs while others write the outputs
+  // every CTA reads the inputs while others write the outputs, and different warps write different outputs
   const size_t nb = (size_t)n_rows * 4;
   const struct {
     const void* p;
@@ -415,6 +415,12 @@ extern "C" pt_status pt_cache_tables(const int32_t* held, const int32_t* added, 
     for (const auto& o : out)
       if (overlap(i.p, i.n, o.p, o.n)) {
         set_error("%s: an output overlaps an input", who);
+        return PT_ERR_INVALID_ARG;
+      }
+  for (const auto& x : out)
+    for (const auto& y : out)
+      if (&x < &y && overlap(x.p, x.n, y.p, y.n)) {
+        set_error("%s: two outputs overlap", who);
         return PT_ERR_INVALID_ARG;
       }
   int dev = 0;

@@ -37,3 +37,19 @@ def test_binding_refuses_a_ring_whose_size_does_not_fit():
     ring = torch.zeros(1, dtype=torch.int32).expand((1 << 32) + 8)  # would reach the library as 8
     with pytest.raises(ValueError, match="ring"):
         pt.cache_tables(i, i, i.view(4, 1), ring, torch.zeros(2, dtype=torch.int64), 16, 4)
+
+
+OUT = ("tables", "ring", "lens", "row_ptr", "slots", "pos", "out")  # tables and ring change in place
+
+
+@pytest.mark.parametrize("a,b", [(a, b) for i, a in enumerate(OUT) for b in OUT[i + 1:]])
+def test_outputs_over_each_other(lib, a, b):
+    assert tables_call(lib, **{a: FAR[b]}) == pt.PT_ERR_INVALID_ARG
+    assert b"overlap" in lib.pt_last_error()
+
+
+def test_an_outputs_last_byte_counts(lib):
+    assert tables_call(lib, lens=FAR["slots"] + 32 * 8 - 1) == pt.PT_ERR_INVALID_ARG
+    assert b"overlap" in lib.pt_last_error()
+    assert tables_call(lib, slots=FAR["ring"] - 32 * 8 + 1) == pt.PT_ERR_INVALID_ARG
+    assert b"overlap" in lib.pt_last_error()
