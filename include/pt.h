@@ -462,9 +462,10 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   stay, so the call may be repeated with the same ones.
  *   Errors on the device (pt_sync_status): PT_ERR_INVALID_ARG for a row with
  *   held or held + added outside [0, max_pages * page_size] (it is left as it
- *   is), for more than max_new added tokens (those behind have no slot), for
- *   counters that are no ring of at most ring_cap entries, for more pages
- *   given back than the ring has room for, and for a freed id below 0;
+ *   is), for more than max_new added tokens (those behind have no slot;
+ *   row_ptr counts on, up to 2^30 + 1), for counters that are no ring of at
+ *   most ring_cap entries, for more pages given back than the ring has room
+ *   for, and for a freed id below 0;
  *   PT_ERR_NOMEM when the ring runs out: the rows behind get no page, their
  *   tokens slot -1, and lens counts what fits in the pages they have.
  *   Errors on the host: PT_ERR_INVALID_ARG for NULL pointers, negative sizes,

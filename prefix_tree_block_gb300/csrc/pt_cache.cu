@@ -66,6 +66,20 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
   return v;
 }
 
+// Tokens before each of a chunk's rows, `before` those of the chunks before it;
+// none above kTabMaxNew + 1, where 32 rows may hold more than 2^31.
+__device__ __forceinline__ int tokens_before(int before, int grow, int lane) {
+  constexpr unsigned top = (unsigned)kTabMaxNew + 1;
+  unsigned s = min((unsigned)grow, top);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s = min(s + u, top);
+  }
+  const unsigned excl = __shfl_up_sync(0xffffffffu, s, 1);
+  return (int)min((unsigned)before + (lane ? excl : 0u), top);
+}
+
 // The lane whose half-open run [start of lane, start of lane + 1) holds x:
 // the last lane with excl <= x (runs of length zero are passed over).
 __device__ __forceinline__ int lane_of(int excl, int x) {
@@ -153,7 +167,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
     const long long g = ((long long)__reduce_add_sync(0xffffffffu, m.grow >> 16) << 16) +
                         __reduce_add_sync(0xffffffffu, m.grow & 0xffff);
     const int t = __reduce_add_sync(0xffffffffu, m.take), b = __reduce_add_sync(0xffffffffu, m.back);
-    if (lane == 0) c_new[c] = (int)min(g, (long long)kTabMaxNew), c_take[c] = t, c_back[c] = b;
+    if (lane == 0) c_new[c] = (int)min(g, (long long)kTabMaxNew + 1), c_take[c] = t, c_back[c] = b;
   }
   __syncthreads();
   if (warp < 3) {  // exclusive scan of one of the three sums (tokens stop at kTabMaxNew + 1, over any max_new)
@@ -196,7 +210,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
   for (int c = blockIdx.x + gridDim.x * warp; c < nc; c += gridDim.x * kTabWarps) {
     const int i = c * 32 + lane;
     const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
-    const int e_new = c_new[c] + warp_incl_scan(m.grow, lane) - m.grow;
+    const int e_new = tokens_before(c_new[c], m.grow, lane);
     const int e_take = warp_incl_scan(m.take, lane) - m.take;
     if (i < a.n) {
       a.row_ptr[i] = e_new;
@@ -257,7 +271,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
       const int i = c * 32 + lane;
       const RowMove m = row_move(i < a.n ? a.held[i] : 0, i < a.n ? a.added[i] : 0, a.ps, most);
       const int st = a.start && i < a.n ? a.start[i] : 0;
-      const int e_new = c_new[c] + warp_incl_scan(m.grow, lane) - m.grow;
+      const int e_new = tokens_before(c_new[c], m.grow, lane);
       const int e_take = c_take[c] + warp_incl_scan(m.take, lane) - m.take;
 #pragma unroll 1
       for (int x = x0; x < x1; x += 32 * U) {
@@ -271,8 +285,7 @@ __global__ void __launch_bounds__(kTabWarps * 32) k_cache_tables(const TabArgs a
           const int pi = tok[u] / a.ps;
           rest[u] = tok[u] - pi * a.ps;
           page[u] = -1;
-          if (tok[u] < 0 || pi >= a.max_pages) {  // only when the rows' tokens together pass kTabMaxNew
-          } else if (pi < p0) {
+          if (pi < p0) {
             page[u] = a.tables[(size_t)(c * 32 + l) * a.max_pages + pi];
           } else if (et + pi - p0 < avail) {
             const int r = h0 + et + pi - p0;
