@@ -537,12 +537,13 @@ pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void* Kc, const 
                          const int32_t* lens, const int32_t* q_count, float scale, const pt_decodeplan* plan, void* O,
                          float* LSE, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Synchronise the stream, then return and clear the device status word:
- * PT_ERR_TIMEOUT if an in-kernel wait ran out since the last check,
- * PT_ERR_INVALID_ARG if a device-side check of a block map (see
- * pt_build_blockmap_tree and pt_build_blockmap_seg) or of the cache calls'
- * lengths, slots and pages failed, PT_ERR_NOMEM if a cache ran out of pages,
- * PT_ERR_CUDA if the stream reported an error, else PT_OK. */
+/* Synchronise the stream, then return and clear the device status words:
+ * PT_ERR_CUDA if the stream reported an error, PT_ERR_TIMEOUT if an in-kernel
+ * wait ran out since the last check, PT_ERR_INVALID_ARG if a device-side check
+ * of a block map (see pt_build_blockmap_tree and pt_build_blockmap_seg) or of
+ * the cache calls' lengths, slots and pages failed, PT_ERR_NOMEM if a cache
+ * ran out of pages, else PT_OK.  When several of these happened the first in
+ * this order is returned, and pt_last_error names them all. */
 pt_status pt_sync_status(cudaStream_t stream);
 
 /* Message for the last failing call on this thread ("" if none). */
@@ -559,6 +560,15 @@ uint64_t pt_launch_count(void);
  * stream returns PT_ERR_TIMEOUT.  Meant for tests of error reporting; the
  * pages have no counterpart. */
 pt_status pt_debug_wait_timeout(cudaStream_t stream);
+
+/* Failure-path check on the host alone: what pt_sync_status returns, and the
+ * message it leaves, when the device status words of the units block map,
+ * forward, backward, CUDA-core attention, fold, cache and decoding hold these
+ * (the first n of them; the rest 0).  Bits of a word: 1 a check failed, 2 out
+ * of pages, 4 a wait ran out; below 0: it could not be read.
+ * PT_ERR_INVALID_ARG also for n outside [0, 7] or NULL words with n > 0.
+ * Meant for tests; the pages have no counterpart. */
+pt_status pt_debug_status(const int32_t* words, int32_t n);
 
 /* Builds the work lists pt_attn_bwd_noalloc needs for block map bm and head
  * layout (Hq, Hkv, D): the kv-major items packed onto the SMs (no column is

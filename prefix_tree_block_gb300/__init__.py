@@ -85,6 +85,7 @@ def load_library(path: Optional[str] = None):
             "pt_attn_bwd": [vp, vp, vp, vp, vp, vp, ctypes.c_int, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp],
             "pt_sync_status": [vp],
             "pt_debug_wait_timeout": [vp],
+            "pt_debug_status": [vp, i32],
             "pt_debug_exp2": [vp, vp, i64, i32, vp],
             "pt_debug_pack_dkdv": [vp, i32, i32, i32, i32, i32, i32, vp, i64, vp, i32p, i32p, i32p],
             "pt_debug_pack_dq": [vp, i32, i32, i32, vp, i64, vp, i32p, i32p, i32p],
@@ -388,7 +389,8 @@ def attn_bwd_noalloc(dO, Q, K, V, O, LSE, bm: BlockMap, scale: float = 0.0, dQ=N
 
 
 def sync_status(stream=None):
-    """Synchronise and raise PTError if an in-kernel wait timed out."""
+    """Synchronise and raise PTError if an in-kernel wait timed out, a
+    device-side check failed or a cache ran out of pages since the last call."""
     _check(load_library().pt_sync_status(ctypes.c_void_p(_stream(stream))))
 
 

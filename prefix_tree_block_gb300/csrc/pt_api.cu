@@ -223,6 +223,49 @@ size_t partial_slots(int T, int Hq) {
   return std::min<size_t>(256, 2 * cols);
 }
 
+// The status of a set of units' device status words, worst first: a wait that
+// ran out leaves outputs undefined, a failed check says that an input was bad,
+// a cache without pages can be given more.
+pt_status status_of(const int32_t* words, int32_t n) {
+  static const char* unit[] = {"block map", "forward", "backward", "CUDA-core attention", "fold", "cache", "decoding"};
+  static const struct {
+    int bit;
+    pt_status status;
+    const char* what;
+  } kinds[] = {{PT_STATUS_TIMEOUT, PT_ERR_TIMEOUT, "a bounded in-kernel wait ran out"},
+               {PT_STATUS_INVALID, PT_ERR_INVALID_ARG, "a device-side check failed"},
+               {PT_STATUS_NOMEM, PT_ERR_NOMEM, "out of free pages"}};
+  char text[512] = "";
+  size_t len = 0;
+  auto add = [&](const char* x, const char* y = "") {
+    len = std::min(len + (size_t)snprintf(text + len, sizeof(text) - len, "%s%s", x, y), sizeof(text) - 1);
+  };
+  pt_status worst = PT_OK;
+  bool maps = false, caches = false;  // which checks
+  for (int i = 0; i < n; ++i)
+    if (words[i] < 0) {
+      set_error("pt_sync_status: could not read the device status word of the %s kernels", unit[i]);
+      return PT_ERR_CUDA;
+    }
+  for (const auto& k : kinds) {
+    bool any = false;
+    for (int i = 0; i < n; ++i) {
+      if (!(words[i] & k.bit)) continue;
+      if (!any) add(worst == PT_OK ? "" : "; ", k.what);
+      add(any ? ", " : ": ", unit[i]);
+      any = true;
+      if (worst == PT_OK) worst = k.status;
+      if (k.bit == PT_STATUS_INVALID) (i < 5 ? maps : caches) = true;
+    }
+  }
+  if (maps)
+    add("; a map's checks: a listed tile that keeps nothing, kept pairs missing from the lists, more partial tiles than "
+        "the lists' bound");
+  if (caches) add("; a cache's checks: a length, count, slot, page id or ring counter out of range");
+  if (worst != PT_OK) set_error("%s", text);
+  return worst;
+}
+
 }  // namespace
 
 extern "C" {
@@ -416,48 +459,18 @@ pt_status pt_sync_status(cudaStream_t stream) {
     set_error("pt_sync_status: %s", cudaGetErrorString(e));
     return PT_ERR_CUDA;
   }
-  int worst = 0;
-  int codes[] = {pt::take_status_blockmap(stream), pt::take_status_fwd(stream), pt::take_status_bwd(stream),
-                 pt::take_status_simt(stream), pt::take_status_fold(stream)};
-  const int cache[] = {pt::take_status_cache(stream), pt::take_status_decode(stream)};
-  for (int c : codes) {
-    if (c < 0) {
-      set_error("pt_sync_status: could not read the device status word");
-      return PT_ERR_CUDA;
-    }
-    if (c && !worst) worst = c;
-  }
-  int cached = 0;
-  for (int c : cache) {
-    if (c < 0) {
-      set_error("pt_sync_status: could not read the device status word");
-      return PT_ERR_CUDA;
-    }
-    if (c && !cached) cached = c;
-  }
-  if (worst == PT_STATUS_TIMEOUT || (!worst && cached == PT_STATUS_TIMEOUT)) {
-    set_error("a bounded in-kernel wait ran out");
-    return PT_ERR_TIMEOUT;
-  }
-  if (worst == PT_STATUS_INVALID) {
-    set_error("a device-side check of a block map's lists or labels failed (a listed tile that keeps nothing, "
-              "kept pairs missing from the lists, or more partial tiles than the lists' bound)");
+  const int32_t words[] = {pt::take_status_blockmap(stream), pt::take_status_fwd(stream),   pt::take_status_bwd(stream),
+                           pt::take_status_simt(stream),     pt::take_status_fold(stream),  pt::take_status_cache(stream),
+                           pt::take_status_decode(stream)};
+  return status_of(words, 7);
+}
+
+pt_status pt_debug_status(const int32_t* words, int32_t n) {
+  if (n < 0 || n > 7 || (n > 0 && !words)) {
+    set_error("pt_debug_status: %d words", n);
     return PT_ERR_INVALID_ARG;
   }
-  if (!worst && cached == PT_STATUS_NOMEM) {
-    set_error("the cache ran out of free pages");
-    return PT_ERR_NOMEM;
-  }
-  if (!worst && cached == PT_STATUS_INVALID) {
-    set_error("a device-side check of the cache calls failed (a length, count, slot, page id or ring counter out of range)");
-    return PT_ERR_INVALID_ARG;
-  }
-  if (!worst) worst = cached;
-  if (worst) {
-    set_error("device status %d", worst);
-    return PT_ERR_CUDA;
-  }
-  return PT_OK;
+  return status_of(words, n);
 }
 
 const char* pt_last_error(void) { return pt::g_err_ptr(); }

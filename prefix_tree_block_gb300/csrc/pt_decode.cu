@@ -24,7 +24,7 @@
 namespace pt {
 int take_status_decode(cudaStream_t s) {
   const int a = take_status_here(s), b = take_status_decode_tc(s);
-  return a < 0 || b < 0 ? -1 : a ? a : b;
+  return a < 0 || b < 0 ? -1 : a | b;
 }
 }  // namespace pt
 

@@ -23,7 +23,7 @@ static __device__ int g_status;
 // no correct launch in this library comes close.
 constexpr long long kWaitLimitCycles = 2000000000LL;
 
-__device__ __forceinline__ void record_status(int code) { atomicCAS(&g_status, 0, code); }
+__device__ __forceinline__ void record_status(int bit) { atomicOr(&g_status, bit); }
 
 // Host side: read and clear this unit's status word (synchronises the stream).
 static inline int take_status_here(cudaStream_t s) {

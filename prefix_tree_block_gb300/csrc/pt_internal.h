@@ -6,10 +6,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#define PT_STATUS_OK 0
+// Bits of a unit's device status word.
 #define PT_STATUS_INVALID 1
+#define PT_STATUS_NOMEM 2
 #define PT_STATUS_TIMEOUT 4
-#define PT_STATUS_NOMEM 5
 
 // Kinds of a (q tile, kv block) pair in the block map.
 #define PT_KIND_EMPTY 0
