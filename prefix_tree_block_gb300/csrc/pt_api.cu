@@ -261,7 +261,7 @@ pt_status status_of(const int32_t* words, int32_t n) {
   if (maps)
     add("; a map's checks: a listed tile that keeps nothing, kept pairs missing from the lists, more partial tiles than "
         "the lists' bound");
-  if (caches) add("; a cache's checks: a length, count, slot, page id or ring counter out of range");
+  if (caches) add("; the pages' checks: a length, count, slot, page id or ring counter out of range");
   if (worst != PT_OK) set_error("%s", text);
   return worst;
 }
