@@ -584,13 +584,15 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
     set_error("%s: path_ptr[0] must be 0", who);
     return PT_ERR_INVALID_ARG;
   }
-  std::vector<int32_t> np(N + 1, 0), leaf(std::max(S, 1), 0), seen(std::max(N, 1), -1);
-  std::vector<uint8_t> is_leaf(std::max(N, 1), 0);
-  for (int s = 0; s < S; ++s) {
+  // (all of path_ptr before any node: path_nodes holds path_ptr[S] of them, so a later entry may be the smaller)
+  for (int s = 0; s < S; ++s)
     if (path_ptr[s + 1] <= path_ptr[s]) {
       set_error("%s: sample path %d is empty", who, s);
       return PT_ERR_INVALID_ARG;
     }
+  std::vector<int32_t> np(N + 1, 0), leaf(std::max(S, 1), 0), seen(std::max(N, 1), -1);
+  std::vector<uint8_t> is_leaf(std::max(N, 1), 0);
+  for (int s = 0; s < S; ++s) {
     for (int k = path_ptr[s]; k < path_ptr[s + 1]; ++k) {
       const int n = path_nodes[k];
       if (n < 0 || n >= N) {
