@@ -509,10 +509,16 @@ cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t sm
   const int D = a.D;
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(256), smem, s, a, c); };
   if (D <= 32) return go(k_decode_simt<E, 1, 1>);
-  if (D <= 64) return D % 2 ? go(k_decode_simt<E, 2, 1>) : go(k_decode_simt<E, 2, 2>);
-  if (D <= 128) return D % 4 ? go(k_decode_simt<E, 4, 1>) : go(k_decode_simt<E, 4, 4>);
-  if (D <= 256) return D % 4 ? go(k_decode_simt<E, 8, 1>) : go(k_decode_simt<E, 8, 4>);
-  return D % 4 ? go(k_decode_simt<E, 16, 1>) : go(k_decode_simt<E, 16, 4>);
+  if constexpr (sizeof(E) == 4) {  // (bf16 head dims are multiples of 8)
+    if (D % (D <= 64 ? 2 : 4)) {
+      if (D <= 64) return go(k_decode_simt<E, 2, 1>);
+      if (D <= 128) return go(k_decode_simt<E, 4, 1>);
+      return D <= 256 ? go(k_decode_simt<E, 8, 1>) : go(k_decode_simt<E, 16, 1>);
+    }
+  }
+  if (D <= 64) return go(k_decode_simt<E, 2, 2>);
+  if (D <= 128) return go(k_decode_simt<E, 4, 4>);
+  return D <= 256 ? go(k_decode_simt<E, 8, 4>) : go(k_decode_simt<E, 16, 4>);
 }
 
 // Rows of a call: below the first number a merge unit is one head on four warps
@@ -529,15 +535,22 @@ cudaError_t launch_merge(MergeArgs m, cudaStream_t s) {
   const int grid = W == 1 ? (m.units + 3) / 4 : m.units, D = m.d.D;
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(128), 0, s, m); };
   if (D <= 32) return go(k_decode_merge<E, 1, 1, GH, W, TWO>);
-  if constexpr (TWO) {  // (bf16 up to kTileMaxD, a multiple of 8)
-    if (D <= 64) return go(k_decode_merge<E, 2, 1, GH, W, TWO>);
-    return go(k_decode_merge<E, 4, 1, GH, W, TWO>);
-  } else {
-    if (D <= 64) return D % 2 ? go(k_decode_merge<E, 1, 2, GH, W, TWO>) : go(k_decode_merge<E, 2, 1, GH, W, TWO>);
-    if (D <= 128) return D % 4 ? go(k_decode_merge<E, 1, 4, GH, W, TWO>) : go(k_decode_merge<E, 4, 1, GH, W, TWO>);
-    if (D <= 256) return D % 4 ? go(k_decode_merge<E, 1, 8, GH, W, TWO>) : go(k_decode_merge<E, 4, 2, GH, W, TWO>);
-    return D % 4 ? go(k_decode_merge<E, 1, 16, GH, W, TWO>) : go(k_decode_merge<E, 4, 4, GH, W, TWO>);
+  if constexpr (sizeof(E) == 4) {  // (bf16 head dims are multiples of 8)
+    if (D % (D <= 64 ? 2 : 4)) {
+      if (D <= 64) return go(k_decode_merge<E, 1, 2, GH, W, TWO>);
+      if (D <= 128) return go(k_decode_merge<E, 1, 4, GH, W, TWO>);
+      if constexpr (GH == 1)
+        if (D > 256) return go(k_decode_merge<E, 1, 16, GH, W, TWO>);
+      return go(k_decode_merge<E, 1, 8, GH, W, TWO>);
+    }
   }
+  if (D <= 64) return go(k_decode_merge<E, 2, 1, GH, W, TWO>);
+  if constexpr (!TWO) {  // (tiles: up to kTileMaxD; several heads to a warp: up to 256)
+    if constexpr (GH == 1)
+      if (D > 256) return go(k_decode_merge<E, 4, 4, GH, W, TWO>);
+    if (D > 128) return go(k_decode_merge<E, 4, 2, GH, W, TWO>);
+  }
+  return go(k_decode_merge<E, 4, 1, GH, W, TWO>);
 }
 
 template <class E, bool TWO>
