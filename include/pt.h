@@ -509,7 +509,17 @@ pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t 
  *   one must not overlap on the GPU.  The result does not vary between runs.
  *   PT_BF16 with D a multiple of 8 up to 512 and page_size a multiple of 16
  *   runs on tensor cores; other page sizes and PT_F32 (any D up to 512) on
- *   CUDA cores.
+ *   CUDA cores.  Probabilities are rounded to bf16 for the product with V on
+ *   tensor cores, as in pt_attn_fwd; everything else is fp32 up to O's own
+ *   rounding.
+ *   What a call costs depends on more than the lengths.  Whether nodes that
+ *   many rows read get a kernel of their own is decided from max_pages *
+ *   page_size, for the lengths are known on the device only: tables much wider
+ *   than the nodes are long can cost a short call 3 to 8 us.  Rows behind
+ *   q_count take the time of masked ones, so a plan of the samples that are
+ *   left is faster than counts of 0 for many that have ended.  q_len is meant
+ *   for tokens and drafts; turns of many hundred tokens are computed, but far
+ *   below the rate of pt_attn_fwd.
  *   Errors: PT_ERR_INVALID_ARG and PT_ERR_UNSUPPORTED as for pt_attn_fwd,
  *   PT_ERR_INVALID_ARG also for a workspace that is too small, a plan of
  *   another device, a bad stride or max_pages * page_size above 2^30 - 1,

@@ -53,9 +53,12 @@ struct alignas(sizeof(E) * V) VecOf {
 // eight lanes a row.  About 28 instructions a token at head_dim 64 for 512
 // bytes of fp32 keys and values.  Documents: 542 MB at head_dim 128, groups of
 // two heads, 114 us (70% of the copy's bandwidth); 136 MB at 64, groups of
-// three, 47 us (43%: latency and issue).  Every four rows read a node again: seven
-// prompts of 7909 tokens under 62 samples, 124 rows a kv head, take 1167 us,
-// 12 TB/s out of L2.
+// three, 47 us (43%: latency and issue); bf16 in pages of 24 tokens, 69 MB at
+// 128, groups of four, 40 us (25%: issue).  Every four rows read a node again:
+// seven prompts of 7909 tokens, each under 62 samples (8 q heads over 4, head_dim
+// 128: 227 MB, 124 rows a kv head), take 1155 us, 6 TB/s out of L2.  Head dims 65
+// to 256 spill 40 to 60 bytes a thread, those from 65 to 127 that 4 does not
+// divide 256: 128 registers, for two CTAs on an SM, are a little short.
 // ---------------------------------------------------------------------------
 template <class E, int DL, int VEC>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {

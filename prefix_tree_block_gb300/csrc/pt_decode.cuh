@@ -55,9 +55,11 @@ constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
 // an SM about 0.9 us for each tile of 16 rows, or 1.1 us for 128 rows and 2.2
 // for 256; kTileMinGain is in such us, over the tokens of a full table row.
 // 32 q heads over 8, head_dim 128, us on rows alone and with tiles: two prompts
-// of 1024 tokens, 64 samples (gain 1560) 35 and 41; of 4096 tokens, 16 samples
-// (1280) 35 and 40; four of 4096, 16 samples (2560) 47 and 43; two of 2048, 64
-// samples (3120) 52 and 41; two of 32768, 64 samples 629 and 165.
+// of 1024 tokens, 64 samples (gain 1560) 35 and 39; of 4096 tokens, 16 samples
+// (1280) 35 and 38; four of 4096, 16 samples (2560) 46 and 39; two of 2048, 64
+// samples (3120) 49 and 40; two of 32768, 64 samples 631 and 168.
+// The host does not know the lengths, so a table that is much wider than its
+// nodes are long counts as if they were: see pt_attn_decode.
 constexpr int kTileMinRows = 33, kTileMaxD = 128;
 constexpr float kTileMinGain = 2000.f;
 // Element (row, column) of a tile-class partial result: groups of 8 columns, in

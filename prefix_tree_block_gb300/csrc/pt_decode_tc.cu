@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SP
 // samples of 512 to 2048 more, 32 q heads over 8: 165 us for the call (84% of
 // the copy's bandwidth), 629 on rows alone; drafts of 16 tokens behind 32
 // continuations of prompts of 4096, 16 q heads over 4, where 64 rows read every
-// token of a continuation and 1024 a prompt: 56 us, 131 on rows alone.
+// token of a continuation and 1024 a prompt: 54 us, 130 on rows alone.
 // A step of 256 x 128 takes 2.1 us, 60% of the tensor pipe's rate: one thread
 // issues its 32 products at 50 ns each.  P is rounded to bf16 as above.
 // Tokens behind the segment's last are zero-filled by TMA where a whole box
