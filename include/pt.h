@@ -403,6 +403,13 @@ void pt_hoststep_free(pt_hoststep* h);
  * pt_fold_positions: pos[t] = the position of token t in the rows that hold
  *   it (int64 [T], the RoPE position ids): a completion's positions continue
  *   from its prompt's.
+ * pt_fold_successors: which tokens follow which, as lists by the token before
+ *   (int32, device): succ[succ_ptr[t] .. succ_ptr[t + 1]) are the flat tokens
+ *   that follow token t in some rollout, ascending: the next one of its node,
+ *   or behind a node's last token the first ones of the nodes below it (of
+ *   those with tokens).  succ_ptr [T + 1]; succ [T] ends with the tokens that
+ *   follow none.  These are pt_token_logprobs' row_ptr and index for the flat
+ *   layout: row t of the logits scores the tokens that follow t.
  * pt_fold_mismatches: *count (device, one unsigned 64-bit counter, zeroed by
  *   the call) = the number of rollout entries whose bytes differ from the
  *   entry pt_fold keeps for their token; 0 when the rollouts really share
@@ -424,6 +431,7 @@ pt_status pt_unfold(const pt_foldplan* plan, const void* flat, int64_t row_bytes
 pt_status pt_unfold_grad(const pt_foldplan* plan, const void* droll, pt_dtype dtype, int64_t width, void* dflat,
                          cudaStream_t stream);
 pt_status pt_fold_positions(const pt_foldplan* plan, int64_t* pos, cudaStream_t stream);
+pt_status pt_fold_successors(const pt_foldplan* plan, int32_t* succ_ptr, int32_t* succ, cudaStream_t stream);
 pt_status pt_fold_mismatches(const pt_foldplan* plan, const void* roll, int64_t row_bytes, unsigned long long* count,
                              cudaStream_t stream);
 
@@ -547,11 +555,146 @@ pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void* Kc, const 
                          const int32_t* lens, const int32_t* q_count, float scale, const pt_decodeplan* plan, void* O,
                          float* LSE, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Trees of drafted tokens over the cache.
+ *
+ * The pages verify nothing: this is the rollout decoding above for samples
+ * whose q_len query tokens are a tree of guesses instead of a run.  A sample's
+ * drafts 0 .. q_count - 1 are the last tokens of its own node, parents before
+ * children; each sees the path's other nodes, its own node's tokens before
+ * the drafts, its ancestors among the drafts and itself.
+ *
+ * pt_draft_tree: parents [n_samples * q_len] (device int32): the draft above
+ *   draft j of the sample, in [-1, j); -1: the last token before the drafts.
+ *   Writes mask [n_samples * q_len][ceil(q_len / 32)] (device int32): bit i % 32
+ *   of word i / 32 of row j says that draft j sees draft i; and with positions
+ *   (device int64 [n_samples * q_len], or NULL) the drafts' position ids:
+ *   start[leaf] (device int32 [n_nodes], or NULL: 0) + lens[leaf] - q_count +
+ *   the drafts above, so that two drafts at one depth have one position.  Rows
+ *   behind q_count (as pt_attn_decode takes it) are 0 in both.  q_len up to
+ *   256 (else PT_ERR_UNSUPPORTED).  On the device (pt_sync_status),
+ *   PT_ERR_INVALID_ARG: a parent outside [-1, j) (-1 is taken), a count outside
+ *   [0, q_len] (the nearest is taken).
+ * pt_attn_decode_drafts: pt_attn_decode with such a mask in the place of "up to
+ *   itself".  A draft sees itself whatever its own bit says; bits behind
+ *   q_count are not looked at.  Any q_len that pt_attn_decode takes.  What a
+ *   row's mask hides, NaN and infinities included, has no part in its result.
+ *   draft_mask must not be NULL; everything else is as there.
+ * pt_cache_keep: after the verification, the accepted drafts' keys and values
+ *   move together: of each sample, draft kept[i] becomes draft i.  kept
+ *   [n_samples][q_len] (device int32): ascending draft numbers below q_count
+ *   (a path of the tree read from its root), ended by a negative one or the
+ *   row's end.  Kc and Vc (one layer's cache) change in place; lens still counts
+ *   all drafts, and pt_cache_tables takes the others back (added = accepted -
+ *   q_count).  The places behind the accepted ones keep what they had.  q_len
+ *   up to 256.  Errors: PT_ERR_INVALID_ARG as pt_cache_write, and for a plan in
+ *   which two samples end at one node.  On the device, PT_ERR_INVALID_ARG, and
+ *   the sample's rows stay as they are: numbers out of order or out of range, a
+ *   length below q_count or above the table's, a page id outside [0, n_pages).
+ * ------------------------------------------------------------------------- */
+pt_status pt_draft_tree(const int32_t* parents, const int32_t* lens, const int32_t* q_count, const int32_t* start,
+                        const pt_decodeplan* plan, int32_t* mask, int64_t* positions, cudaStream_t stream);
+pt_status pt_attn_decode_drafts(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, pt_dtype dtype,
+                                int32_t D, int32_t n_pages, int32_t page_size, const int32_t* tables,
+                                int32_t max_pages, const int32_t* lens, const int32_t* q_count,
+                                const int32_t* draft_mask, float scale, const pt_decodeplan* plan, void* O, float* LSE,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+pt_status pt_cache_keep(const int32_t* kept, const int32_t* q_count, const int32_t* lens, const int32_t* tables,
+                        int32_t max_pages, pt_dtype dtype, int32_t D, void* Kc, void* Vc, int32_t n_pages,
+                        int32_t page_size, const pt_decodeplan* plan, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pt_rotary -- rotary positions of one or several axes.
+ *
+ * Passage: "cp=1 shared-prefix prefix-tree attention for rollouts", PR
+ * description: position ids continue from the prompt's.  The ids come from
+ * pt_fold_positions, pt_cache_tables or pt_draft_tree (one axis), or from the
+ * caller (time, height and width of images and video, up to 4 axes).
+ *
+ * X [T, H, D] and Y [T, H, D] (device, dtype; tokens x_stride and y_stride
+ * elements apart, heads dense, so a slice of a fused projection will do).  Pair
+ * i < rot_dim / 2 of every head is turned by the angle positions[axis(i)][t] *
+ * inv_freq[i] (by its negative with inverse != 0, which is the inverse and the
+ * gradient of the call): (a, b) -> (a cos - b sin, b cos + a sin).  Pair i is
+ * columns i and rot_dim / 2 + i, or with interleaved != 0 columns 2i and 2i + 1.
+ * Columns behind rot_dim are copied.  positions [n_axes][T] (device int64, any
+ * sign); sections [n_axes] (host): pairs of each axis, in order, rot_dim / 2 in
+ * all (NULL with one axis).  inv_freq [rot_dim / 2] (device fp32).
+ * The angle is taken modulo a turn in 64-bit integers, so far positions lose
+ * nothing (|inv_freq| up to 2^20; not finite or beyond 2^31: NaN); sines,
+ * cosines and products are fp32, with one rounding to dtype.
+ * Y may be X (same strides) or not overlap it.  Any alignment to the element;
+ * 16-byte rows, strides and addresses are the fast ones.
+ * Errors: PT_ERR_INVALID_ARG for a bad dtype, sizes, strides, sections, overlap
+ * or pointers, an odd rot_dim or one above D; PT_ERR_UNSUPPORTED for more than
+ * 4 axes or rot_dim above 1024.
+ * ------------------------------------------------------------------------- */
+pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, int32_t H, int32_t D,
+                    const int64_t* positions, const float* inv_freq, int32_t rot_dim, const int32_t* sections,
+                    int32_t n_axes, int32_t interleaved, int32_t inverse, void* Y, int64_t y_stride,
+                    cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pt_token_logprobs -- log probabilities of given tokens under rows of logits,
+ * the rows' entropy, and their most likely tokens; and the gradient.
+ *
+ * Passage: "cp=1 shared-prefix prefix-tree attention for rollouts", PR
+ * description: a prompt is encoded once for all its completions.  Its last row
+ * of logits is then scored against the first token of each of them, so a row has
+ * any number of tokens here.
+ *
+ * logits [R, V] (device, dtype; rows row_stride elements apart).  With z =
+ * scale * logits (scale: the inverse of a sampling temperature):
+ *   LSE[r] = ln sum_v exp z[r, v];  logp of token t under row r = z[r,
+ *   targets[t]] - LSE[r];  entropy[r] = -sum_v p ln p, p = exp(z - LSE).
+ * targets [N] (device int64): token ids; a negative one is not scored (logp 0,
+ * no gradient).  Row r scores tokens index[row_ptr[r]] .. index[row_ptr[r + 1] -
+ * 1] (device int32; index NULL: the entries' own numbers; row_ptr NULL: token r,
+ * N = R).  The entries from row_ptr[R] on belong to no row: logp 0.  logp [N],
+ * LSE [R], entropy [R] (or NULL): fp32.  An index that names a token twice gets
+ * one of the two rows' logp.
+ * top_k > 0: top_ids [R, top_k] (int64) and top_logp [R, top_k] (fp32) are the
+ * largest logits' tokens, descending, equal ones by the lower id.
+ * Infinities: a logit of -inf is a token that cannot be chosen; a row of nothing
+ * else has LSE = -inf, entropy 0 and logp -inf.  A row with a NaN or +inf has
+ * LSE, entropy and logp NaN (a NaN counts as -inf among the alternatives).
+ * logp is taken from the row's maximum, so large logits cost it nothing; LSE
+ * is one fp32 number, and what it was rounded by (2^-24 of it) is an error of
+ * every ln p in the backward.
+ *
+ * pt_token_logprobs_bwd: dlogits [R, V] (dtype; rows d_stride elements apart) =
+ * scale * (sum over the row's tokens of dlogp[t] (1[v = targets[t]] - p) -
+ * dentropy[r] p (ln p + entropy[r])), from dlogp [N] and dentropy [R] (fp32, the
+ * latter NULL for none), LSE and entropy as the forward wrote them (entropy may
+ * be NULL without dentropy).  Every row is written; rows without weight (LSE =
+ * -inf) get the tokens' own part only.  dlogits may be logits (same stride) or
+ * not overlap it.  Sums are fp32 in a fixed order, rounded once to dtype, so
+ * both calls repeat bit for bit.
+ *
+ * Any V up to 2^30, stride and alignment to the element (rows whose gradient
+ * does not start as their logits do modulo 16 bytes are stored by elements).
+ * Errors: PT_ERR_INVALID_ARG for a bad dtype, sizes (V < 1, N != R without
+ * row_ptr), strides, a scale outside [1e-30, 1e30], top_k outside [0, V],
+ * overlap or NULL pointers; PT_ERR_UNSUPPORTED for top_k above 64, V above 2^30
+ * or R above 2^28 - 1.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a
+ * target of V or more (not scored), a row_ptr that decreases or passes N (the
+ * row scores nothing), an index outside [0, N) (passed over).
+ * ------------------------------------------------------------------------- */
+pt_status pt_token_logprobs(const void* logits, int64_t row_stride, pt_dtype dtype, int32_t R, int32_t V,
+                            const int64_t* targets, const int32_t* row_ptr, const int32_t* index, int32_t N,
+                            float scale, int32_t top_k, float* logp, float* LSE, float* entropy, float* top_logp,
+                            int64_t* top_ids, cudaStream_t stream);
+pt_status pt_token_logprobs_bwd(const float* dlogp, const float* dentropy, const void* logits, int64_t row_stride,
+                                pt_dtype dtype, int32_t R, int32_t V, const int64_t* targets, const int32_t* row_ptr,
+                                const int32_t* index, int32_t N, float scale, const float* LSE, const float* entropy,
+                                void* dlogits, int64_t d_stride, cudaStream_t stream);
+
 /* Synchronise the stream, then return and clear the device status words:
  * PT_ERR_CUDA if the stream reported an error, PT_ERR_TIMEOUT if an in-kernel
  * wait ran out since the last check, PT_ERR_INVALID_ARG if a device-side check
- * of a block map (see pt_build_blockmap_tree and pt_build_blockmap_seg) or of
- * the cache calls' lengths, slots and pages failed, PT_ERR_NOMEM if a cache
+ * of a block map (see pt_build_blockmap_tree and pt_build_blockmap_seg), of
+ * the cache calls' lengths, slots and pages, of trees of drafts or of scored
+ * tokens failed, PT_ERR_NOMEM if a cache
  * ran out of pages, else PT_OK.  When several of these happened the first in
  * this order is returned, and pt_last_error names them all. */
 pt_status pt_sync_status(cudaStream_t stream);
@@ -690,9 +833,10 @@ pt_status pt_debug_exp2(const float* x, float* y, int64_t n, int32_t method, cud
  * "bwd_dq", "bwd_simt",
  * "blockmap_classify" (tile classes, list sizes, orders),
  * "blockmap_lists" (lists and masks), and the fold calls' "fold_plan",
- * "fold", "unfold", "unfold_grad", "fold_positions", "fold_mismatches",
- * and the cache and decoding calls' "cache_tables", "cache_write",
- * "decode_simt", "decode_rows", "decode_tile", "decode_merge".  pt_profile_reset drops every record
+ * "fold", "unfold", "unfold_grad", "fold_positions", "fold_successors",
+ * "fold_mismatches", and the cache and decoding calls' "cache_tables", "cache_write",
+ * "decode_simt", "decode_rows", "decode_tile", "decode_merge", "draft_tree",
+ * "cache_keep", "rotary", "token_logprobs", "token_logprobs_bwd".  pt_profile_reset drops every record
  * (its events go back to the pool once they have completed). */
 void pt_profile_enable(int on);
 pt_status pt_profile_read(const char* kernel, int64_t* launches, double* total_ms);

@@ -20,7 +20,8 @@ __all__ = [
     "build_blockmap_draft",
     "attn_fwd", "attn_bwd", "bwd_workspace_bytes", "sync_status", "launch_count", "LIB_PATH",
     "profile_enable", "profile_read", "profile_reset", "attn_bwd_noalloc", "FoldPlan", "fold_plan",
-    "cache_tables", "cache_write", "DecodePlan", "decode_plan", "attn_decode",
+    "cache_tables", "cache_write", "DecodePlan", "decode_plan", "attn_decode", "draft_tree", "cache_keep", "rotary",
+    "token_logprobs", "token_logprobs_bwd",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpt.so")
@@ -104,6 +105,7 @@ def load_library(path: Optional[str] = None):
             "pt_unfold": [vp, vp, i64, vp, vp],
             "pt_unfold_grad": [vp, vp, ctypes.c_int, i64, vp, vp],
             "pt_fold_positions": [vp, vp, vp],
+            "pt_fold_successors": [vp, vp, vp, vp],
             "pt_fold_mismatches": [vp, vp, i64, vp, vp],
             "pt_debug_pool_usage": [i32, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)],
             "pt_cache_tables": [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp],
@@ -111,6 +113,13 @@ def load_library(path: Optional[str] = None):
             "pt_decode_plan": [i32, vp, vp, i32, i32, i32, i32, vp, pp],
             "pt_attn_decode": [vp, i64, vp, vp, ctypes.c_int, i32, i32, i32, vp, i32, vp, vp, f32, vp, vp, vp, vp, sz,
                                vp],
+            "pt_attn_decode_drafts": [vp, i64, vp, vp, ctypes.c_int, i32, i32, i32, vp, i32, vp, vp, vp, f32, vp, vp, vp,
+                                      vp, sz, vp],
+            "pt_draft_tree": [vp, vp, vp, vp, vp, vp, vp, vp],
+            "pt_cache_keep": [vp, vp, vp, vp, i32, ctypes.c_int, i32, vp, vp, i32, i32, vp, vp],
+            "pt_rotary": [vp, i64, ctypes.c_int, i32, i32, i32, vp, vp, i32, vp, i32, i32, i32, vp, i64, vp],
+            "pt_token_logprobs": [vp, i64, ctypes.c_int, i32, i32, vp, vp, vp, i32, f32, i32, vp, vp, vp, vp, vp, vp],
+            "pt_token_logprobs_bwd": [vp, vp, vp, i64, ctypes.c_int, i32, i32, vp, vp, vp, i32, f32, vp, vp, vp, i64, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -559,6 +568,16 @@ class FoldPlan:
         _check(self._lib.pt_fold_positions(self._h, _ptr(out), ctypes.c_void_p(_stream(stream))))
         return out
 
+    def successors(self, device=None, stream=None) -> Tuple:
+        """Which flat tokens follow which: succ_ptr [T + 1] and succ [T] (int32),
+        the row_ptr and index of token_logprobs for the flat layout."""
+        import torch
+
+        device = device or torch.device("cuda")
+        ptr, succ = _empty((self.T + 1,), torch.int32, device), _empty((self.T,), torch.int32, device)
+        _check(self._lib.pt_fold_successors(self._h, _ptr(ptr), _ptr(succ), ctypes.c_void_p(_stream(stream))))
+        return ptr, succ
+
     def mismatches(self, roll, stream=None) -> int:
         """Rollout entries whose bytes differ from the entry the fold keeps (synchronises)."""
         import torch
@@ -764,11 +783,13 @@ def decode_plan(n_nodes: int, path_ptr, path_nodes, Hq: int, Hkv: int, q_len: in
 
 
 def attn_decode(Q, Kc, Vc, tables, lens, plan: DecodePlan, q_count=None, scale: float = 0.0, O=None, LSE=None,
-                workspace=None, stream=None) -> Tuple:
+                workspace=None, stream=None, draft_mask=None) -> Tuple:
     """O [n_samples * q_len, Hq, D] and LSE [Hq, n_samples * q_len] (fp32) of
     the samples' newest tokens Q over the cache Kc, Vc [n_pages, Hkv,
     page_size, D], tables [n_nodes, max_pages], lens [n_nodes] (pt_attn_decode).
-    With q_count, rows behind a sample's queries keep what O and LSE held."""
+    With q_count, rows behind a sample's queries keep what O and LSE held.
+    draft_mask [n_samples * q_len, ceil(q_len / 32)] (int32, as draft_tree gives
+    it): the queries are a tree of drafts (pt_attn_decode_drafts)."""
     torch, i32, _, f32, _, _, device = _torch()
     dev = device() if Q.is_cuda else -1
     dtype = Q.dtype
@@ -798,11 +819,193 @@ def attn_decode(Q, Kc, Vc, tables, lens, plan: DecodePlan, q_count=None, scale: 
         held.append(workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor on the current device")
-    rc = load_library().pt_attn_decode(
+    call, masked = load_library().pt_attn_decode, ()
+    if draft_mask is not None:
+        _need(draft_mask, "draft_mask", i32, (T, (plan.q_len + 31) // 32), dev)
+        call, masked = _lib.pt_attn_decode_drafts, (draft_mask.data_ptr(),)
+    rc = call(
         Q.data_ptr(), qs, Kc.data_ptr(), Vc.data_ptr(), code, D, n_pages, ps, tables.data_ptr(), width,
-        lens.data_ptr(), None if q_count is None else q_count.data_ptr(), scale, plan.handle, O.data_ptr(),
+        lens.data_ptr(), None if q_count is None else q_count.data_ptr(), *masked, scale, plan.handle, O.data_ptr(),
         LSE.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _launch_stream(stream, dev, *held))
     if rc:
         _check(rc)
     return O, LSE
+
+
+def draft_tree(parents, lens, plan: DecodePlan, q_count=None, start=None, stream=None) -> Tuple:
+    """Trees of drafts (pt_draft_tree): parents [n_samples * q_len] (CUDA int32,
+    the draft above each, or -1) become draft_mask [n_samples * q_len, ceil(q_len
+    / 32)] (int32) for attn_decode, and the drafts' position ids (int64
+    [n_samples * q_len]) from lens and start (int32 [n_nodes])."""
+    _, i32, i64, _, _, _, device = _torch()
+    dev = device() if parents.is_cuda else -1
+    n, N = plan.n_rows, plan.n_nodes
+    _need(parents, "parents", i32, (n,), dev)
+    _need(lens, "lens", i32, (N,), dev)
+    if q_count is not None:
+        _need(q_count, "q_count", i32, (plan.n_samples,), dev)
+    if start is not None:
+        _need(start, "start", i32, (N,), dev)
+    mask, positions = _out((n, (plan.q_len + 31) // 32), i32, parents), _out((n,), i64, parents)
+    rc = load_library().pt_draft_tree(
+        parents.data_ptr(), lens.data_ptr(), None if q_count is None else q_count.data_ptr(),
+        None if start is None else start.data_ptr(), plan.handle, mask.data_ptr(), positions.data_ptr(),
+        _launch_stream(stream, dev, mask, positions))
+    if rc:
+        _check(rc)
+    return mask, positions
+
+
+def cache_keep(kept, Kc, Vc, tables, lens, plan: DecodePlan, q_count=None, stream=None) -> None:
+    """Move the accepted drafts' keys and values together (pt_cache_keep): of
+    each sample, draft kept[s, i] (CUDA int32 [n_samples, q_len], ascending, ended
+    by a negative one) becomes draft i of its own node, in place in Kc and Vc."""
+    _, i32, _, _, _, _, device = _torch()
+    dev = device() if kept.is_cuda else -1
+    code, (n_pages, Hkv, ps, D) = _cache_shape(Kc, Vc, Kc.dtype, dev)
+    if Hkv != plan.Hkv:
+        raise ValueError(f"the cache has {Hkv} kv heads, the plan {plan.Hkv}")
+    _need(kept, "kept", i32, (plan.n_samples, plan.q_len), dev)
+    width = tables.shape[1] if tables.dim() == 2 else 0
+    _need(tables, "tables", i32, (plan.n_nodes, width), dev)
+    _need(lens, "lens", i32, (plan.n_nodes,), dev)
+    if q_count is not None:
+        _need(q_count, "q_count", i32, (plan.n_samples,), dev)
+    rc = load_library().pt_cache_keep(
+        kept.data_ptr(), None if q_count is None else q_count.data_ptr(), lens.data_ptr(), tables.data_ptr(), width,
+        code, D, Kc.data_ptr(), Vc.data_ptr(), n_pages, ps, plan.handle, _launch_stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def _code(dtype) -> int:
+    code = PT_BF16 if dtype == _T[4] else PT_F32 if dtype == _T[3] else None
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def rotary(X, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False, out=None,
+           stream=None):
+    """X [T, H, D] with its pairs of columns turned by position (pt_rotary).
+    positions: CUDA int64 [T], or [axes, T] with sections, the pairs of each axis;
+    inv_freq: fp32 [rot_dim / 2].  inverse gives the inverse, which is also the
+    gradient.  X and out may be slices of a fused projection; out may be X."""
+    _, _, i64, f32, _, _, device = _torch()
+    dev = device() if X.is_cuda else -1
+    if X.dim() != 3:
+        raise ValueError("X is [T, H, head_dim]")
+    T, H, D = X.shape
+    code = _code(X.dtype)
+    xs = _token_rows(X, "X", X.dtype, T, H, D, dev)
+    axes = 1 if sections is None else len(sections)
+    _need(positions, "positions", i64, (T,) if positions.dim() == 1 and axes == 1 else (axes, T), dev)
+    half = inv_freq.numel()
+    _need(inv_freq, "inv_freq", f32, (half,), dev)
+    held = ()
+    if out is None:
+        out = _out((T, H, D), X.dtype, X)
+        held, ys = (out,), H * D
+    else:
+        ys = _token_rows(out, "out", X.dtype, T, H, D, dev)
+    if T == 1:  # (a token has no neighbour: one stride for both, whatever the slices')
+        xs = ys = H * D
+    pairs = None if sections is None else (ctypes.c_int32 * max(axes, 1))(*sections)
+    rc = load_library().pt_rotary(X.data_ptr(), xs, code, T, H, D, positions.data_ptr(), inv_freq.data_ptr(), 2 * half,
+                                  pairs, axes, interleaved, inverse, out.data_ptr(), ys,
+                                  _launch_stream(stream, dev, *held))
+    if rc:
+        _check(rc)
+    return out
+
+
+def _logit_rows(t, name, dtype, shape, dev) -> int:
+    """[R, V] rows of dense elements; returns the elements between rows."""
+    if t.dtype != dtype or t.get_device() != dev or dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor [rows, vocabulary] of {dtype} on the current device")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
+    R, V = shape
+    s, d = t.stride()
+    if R and V and ((d != 1 and V > 1) or (s < V and R > 1)):
+        raise ValueError(f"{name}: the logits of a row must be dense and rows must not overlap")
+    return s if R > 1 else V
+
+
+def _entries(targets, row_ptr, index, R, dev):
+    """The checked tokens of the rows: (N, pointers of targets, row_ptr and index)."""
+    i32, i64 = _T[1], _T[2]
+    N = targets.numel()
+    _need(targets, "targets", i64, (N,), dev)
+    if row_ptr is not None:
+        _need(row_ptr, "row_ptr", i32, (R + 1,), dev)
+    elif N != R:
+        raise ValueError(f"{N} targets for {R} rows need a row_ptr")
+    if index is not None:
+        _need(index, "index", i32, (N,), dev)
+    return N, targets.data_ptr(), None if row_ptr is None else row_ptr.data_ptr(), None if index is None else index.data_ptr()
+
+
+def token_logprobs(logits, targets, row_ptr=None, index=None, top_k: int = 0, entropy: bool = False,
+                   scale: float = 1.0, stream=None) -> Tuple:
+    """Log probabilities of given tokens (pt_token_logprobs): logits [R, V],
+    targets int64 [N] (negative: not scored).  Row r scores token r, or tokens
+    index[row_ptr[r]:row_ptr[r + 1]] (int32; FoldPlan.successors gives both for a
+    tree).  Returns logp [N], LSE [R], entropy [R] or None, and the top_k most
+    likely tokens' log probabilities and ids [R, top_k] or None."""
+    _, _, i64, f32, _, _, device = _torch()
+    dev = device() if logits.is_cuda else -1
+    if logits.dim() != 2:
+        raise ValueError("logits is [rows, vocabulary]")
+    R, V = logits.shape
+    code = _code(logits.dtype)
+    rs = _logit_rows(logits, "logits", logits.dtype, (R, V), dev)
+    N, *entries = _entries(targets, row_ptr, index, R, dev)
+    logp, lse = _out((N,), f32, logits), _out((R,), f32, logits)
+    H = _out((R,), f32, logits) if entropy else None
+    top = _out((R, top_k), f32, logits) if top_k > 0 else None
+    ids = _out((R, top_k), i64, logits) if top_k > 0 else None
+    held = [t for t in (logp, lse, H, top, ids) if t is not None]
+    rc = load_library().pt_token_logprobs(
+        logits.data_ptr(), rs, code, R, V, *entries, N, scale, top_k, logp.data_ptr(), lse.data_ptr(),
+        H.data_ptr() if entropy else None, top.data_ptr() if top_k > 0 else None, ids.data_ptr() if top_k > 0 else None,
+        _launch_stream(stream, dev, *held))
+    if rc:
+        _check(rc)
+    return logp, lse, H, top, ids
+
+
+def token_logprobs_bwd(dlogp, logits, targets, lse, row_ptr=None, index=None, dentropy=None, entropy=None,
+                       scale: float = 1.0, dlogits=None, stream=None):
+    """dlogits [R, V] from dlogp [N] and, with the forward's entropy, dentropy
+    [R] (pt_token_logprobs_bwd); lse and entropy as token_logprobs returned them.
+    dlogits may be logits."""
+    _, _, _, f32, _, _, device = _torch()
+    dev = device() if logits.is_cuda else -1
+    if logits.dim() != 2:
+        raise ValueError("logits is [rows, vocabulary]")
+    R, V = logits.shape
+    code = _code(logits.dtype)
+    rs = _logit_rows(logits, "logits", logits.dtype, (R, V), dev)
+    N, *entries = _entries(targets, row_ptr, index, R, dev)
+    _need(dlogp, "dlogp", f32, (N,), dev)
+    _need(lse, "lse", f32, (R,), dev)
+    if dentropy is not None:
+        if entropy is None:
+            raise ValueError("dentropy needs the forward's entropy")
+        _need(dentropy, "dentropy", f32, (R,), dev)
+        _need(entropy, "entropy", f32, (R,), dev)
+    held = ()
+    if dlogits is None:
+        dlogits = _out((R, V), logits.dtype, logits)
+        held, ds = (dlogits,), V
+    else:
+        ds = _logit_rows(dlogits, "dlogits", logits.dtype, (R, V), dev)
+    rc = load_library().pt_token_logprobs_bwd(
+        dlogp.data_ptr(), None if dentropy is None else dentropy.data_ptr(), logits.data_ptr(), rs, code, R, V, *entries,
+        N, scale, lse.data_ptr(), None if entropy is None else entropy.data_ptr(), dlogits.data_ptr(), ds,
+        _launch_stream(stream, dev, *held))
+    if rc:
+        _check(rc)
+    return dlogits

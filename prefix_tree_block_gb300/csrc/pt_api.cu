@@ -227,7 +227,8 @@ size_t partial_slots(int T, int Hq) {
 // ran out leaves outputs undefined, a failed check says that an input was bad,
 // a cache without pages can be given more.
 pt_status status_of(const int32_t* words, int32_t n) {
-  static const char* unit[] = {"block map", "forward", "backward", "CUDA-core attention", "fold", "cache", "decoding"};
+  static const char* unit[] = {"block map", "forward", "backward", "CUDA-core attention", "fold", "cache", "decoding",
+                               "token log probability"};
   static const struct {
     int bit;
     pt_status status;
@@ -241,7 +242,7 @@ pt_status status_of(const int32_t* words, int32_t n) {
     len = std::min(len + (size_t)snprintf(text + len, sizeof(text) - len, "%s%s", x, y), sizeof(text) - 1);
   };
   pt_status worst = PT_OK;
-  bool maps = false, caches = false;  // which checks
+  bool maps = false, caches = false, tokens = false;  // which checks
   for (int i = 0; i < n; ++i)
     if (words[i] < 0) {
       set_error("pt_sync_status: could not read the device status word of the %s kernels", unit[i]);
@@ -255,13 +256,14 @@ pt_status status_of(const int32_t* words, int32_t n) {
       add(any ? ", " : ": ", unit[i]);
       any = true;
       if (worst == PT_OK) worst = k.status;
-      if (k.bit == PT_STATUS_INVALID) (i < 5 ? maps : caches) = true;
+      if (k.bit == PT_STATUS_INVALID) (i < 5 ? maps : i < 7 ? caches : tokens) = true;
     }
   }
   if (maps)
     add("; a map's checks: a listed tile that keeps nothing, kept pairs missing from the lists, more partial tiles than "
         "the lists' bound");
-  if (caches) add("; the pages' checks: a length, count, slot, page id or ring counter out of range");
+  if (caches) add("; the pages' checks: a length, count, slot, page id, ring counter, parent or kept draft out of range");
+  if (tokens) add("; the tokens' checks: a target, row_ptr or index out of range");
   if (worst != PT_OK) set_error("%s", text);
   return worst;
 }
@@ -461,8 +463,8 @@ pt_status pt_sync_status(cudaStream_t stream) {
   }
   const int32_t words[] = {pt::take_status_blockmap(stream), pt::take_status_fwd(stream),   pt::take_status_bwd(stream),
                            pt::take_status_simt(stream),     pt::take_status_fold(stream),  pt::take_status_cache(stream),
-                           pt::take_status_decode(stream)};
-  return status_of(words, 7);
+                           pt::take_status_decode(stream), pt::take_status_logprobs(stream)};
+  return status_of(words, 8);
 }
 
 pt_status pt_debug_status(const int32_t* words, int32_t n) {

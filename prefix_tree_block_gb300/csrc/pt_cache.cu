@@ -17,7 +17,11 @@
 #include "pt_internal.h"
 
 namespace pt {
-int take_status_cache(cudaStream_t s) { return take_status_here(s); }
+int take_status_drafts(cudaStream_t s);  // pt_drafts.cu
+int take_status_cache(cudaStream_t s) {
+  const int a = take_status_here(s), b = take_status_drafts(s);
+  return a < 0 || b < 0 ? -1 : a | b;
+}
 }  // namespace pt
 
 using namespace pt;

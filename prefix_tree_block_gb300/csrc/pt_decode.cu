@@ -60,7 +60,7 @@ struct alignas(sizeof(E) * V) VecOf {
 // to 256 spill 40 to 60 bytes a thread, those from 65 to 127 that 4 does not
 // divide 256: 128 registers, for two CTAs on an SM, are a little short.
 // ---------------------------------------------------------------------------
-template <class E, int DL, int VEC>
+template <class E, int DL, int VEC, bool TREE>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {
   pdl_wait();
   extern __shared__ int chunk[];
@@ -83,15 +83,24 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
     float q[R][DL], acc[R][DL];
     int lim_max = 0, lim_min = INT_MAX, my_lim = 0;  // (the least of the rows there are)
     int lim[R];
+    int my_lo = 0, my_mask = -1;  // TREE: what the row sees in any case, and its mask's row
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = p.rt * R + r;
       lim[r] = 0;
       const E* src = nullptr;
       if (row < p.rows) {
-        const DecRow d = dec_row(a, p.member0, p.hk, row, p.len);
+        DecRow d;
+        if constexpr (TREE) {
+          const DecTreeRow tr = dec_tree_row(a, p.member0, p.hk, row, p.len);
+          d = tr.d;
+          lim_min = min(lim_min, tr.lo);
+          if (r == my_r) my_lo = tr.lo, my_mask = tr.mask_row;
+        } else {
+          d = dec_row(a, p.member0, p.hk, row, p.len);
+          lim_min = min(lim_min, d.lim);
+        }
         lim[r] = d.lim;
-        lim_min = min(lim_min, d.lim);
         src = Qp + (long long)d.tok * a.q_stride + (long long)d.head * a.D;
       }
       lim_max = max(lim_max, lim[r]);
@@ -130,6 +139,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       }
       if (kv0 + STEP < end) next = row_of(kv0 + STEP);
       float s[2] = {-INFINITY, -INFINITY};
+      int hidden = 0;  // TREE: which of the two the row does not see
 #pragma unroll
       for (int gq = 0; gq < STEP / 4; ++gq) {
         float d[16];
@@ -156,7 +166,10 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
         }
         d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
         const int kv = kv0 + gq * 4 + ((lane >> 1) & 3);
-        s[gq] = kv < end && kv < my_lim ? d[0] : -INFINITY;
+        bool sees = kv < end && kv < my_lim;
+        if (TREE && sees && kv >= my_lo) sees = dec_sees16(a, my_lo, my_lim, my_mask, kv) & 1u;
+        s[gq] = sees ? d[0] : -INFINITY;
+        if (TREE && !sees) hidden |= 1 << gq;
       }
       float mt = fmaxf(s[0], s[1]);
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
@@ -177,6 +190,10 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
           for (int i = 0; i < DL; ++i) acc[r][i] *= ar;
         }
       }
+      if constexpr (TREE) {  // (weights are not negative: below 0 says that the token is not seen)
+        if (hidden & 1) s[0] = -1.f;
+        if (hidden & 2) s[1] = -1.f;
+      }
       auto add_values = [&](auto masked) {
 #pragma unroll
         for (int i = 0; i < STEP; ++i) {
@@ -193,7 +210,8 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 #pragma unroll
               for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
                 const float y = fmaf(pr[r], to_f(w.e[x]), acc[r][v * VEC + x]);
-                acc[r][v * VEC + x] = !masked || kv0 + i < lim[r] ? y : acc[r][v * VEC + x];
+                const bool sees = !masked || (TREE ? !(pr[r] < 0.f) : kv0 + i < lim[r]);
+                acc[r][v * VEC + x] = sees ? y : acc[r][v * VEC + x];
               }
           }
         }
@@ -507,21 +525,21 @@ size_t ws_bytes(const pt_decodeplan* p, int D) {
   return n;
 }
 
-template <class E>
+template <class E, bool TREE>
 cudaError_t launch_simt(const DecArgs& a, const DecClass& c, int grid, size_t smem, cudaStream_t s) {
   const int D = a.D;
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(256), smem, s, a, c); };
-  if (D <= 32) return go(k_decode_simt<E, 1, 1>);
+  if (D <= 32) return go(k_decode_simt<E, 1, 1, TREE>);
   if constexpr (sizeof(E) == 4) {  // (bf16 head dims are multiples of 8)
     if (D % (D <= 64 ? 2 : 4)) {
-      if (D <= 64) return go(k_decode_simt<E, 2, 1>);
-      if (D <= 128) return go(k_decode_simt<E, 4, 1>);
-      return D <= 256 ? go(k_decode_simt<E, 8, 1>) : go(k_decode_simt<E, 16, 1>);
+      if (D <= 64) return go(k_decode_simt<E, 2, 1, TREE>);
+      if (D <= 128) return go(k_decode_simt<E, 4, 1, TREE>);
+      return D <= 256 ? go(k_decode_simt<E, 8, 1, TREE>) : go(k_decode_simt<E, 16, 1, TREE>);
     }
   }
-  if (D <= 64) return go(k_decode_simt<E, 2, 2>);
-  if (D <= 128) return go(k_decode_simt<E, 4, 4>);
-  return D <= 256 ? go(k_decode_simt<E, 8, 4>) : go(k_decode_simt<E, 16, 4>);
+  if (D <= 64) return go(k_decode_simt<E, 2, 2, TREE>);
+  if (D <= 128) return go(k_decode_simt<E, 4, 4, TREE>);
+  return D <= 256 ? go(k_decode_simt<E, 8, 4, TREE>) : go(k_decode_simt<E, 16, 4, TREE>);
 }
 
 // Rows of a call: below the first number a merge unit is one head on four warps
@@ -608,6 +626,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
     }
   std::vector<int32_t> np(N + 1, 0), leaf(std::max(S, 1), 0), seen(std::max(N, 1), -1);
   std::vector<uint8_t> is_leaf(std::max(N, 1), 0);
+  bool own_leaves = true;
   for (int s = 0; s < S; ++s) {
     for (int k = path_ptr[s]; k < path_ptr[s + 1]; ++k) {
       const int n = path_nodes[k];
@@ -623,6 +642,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
       ++np[n + 1];
     }
     leaf[s] = path_nodes[path_ptr[s + 1] - 1];
+    own_leaves &= !is_leaf[leaf[s]];
     is_leaf[leaf[s]] = 1;
   }
   for (int i = 0; i < N; ++i) np[i + 1] += np[i];
@@ -688,7 +708,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
   p->device = dev;
   p->sms = num_sms(dev);
   p->stream = stream;
-  p->N = N, p->S = S, p->Hq = Hq, p->Hkv = Hkv, p->q_len = q_len, p->tile_gain = (float)tile_gain;
+  p->N = N, p->S = S, p->Hq = Hq, p->Hkv = Hkv, p->q_len = q_len, p->own_leaves = own_leaves, p->tile_gain = (float)tile_gain;
   int rc = pool_alloc(&p->mem, host.size(), dev, stream);
   if (rc) {
     delete p;
@@ -724,12 +744,13 @@ extern "C" size_t pt_decode_workspace_bytes(const pt_decodeplan* p, int32_t D) {
   return ws_bytes(p, D);
 }
 
-extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, pt_dtype dtype,
-                                    int32_t D, int32_t n_pages, int32_t page_size, const int32_t* tables,
-                                    int32_t max_pages, const int32_t* lens, const int32_t* q_count, float scale,
-                                    const pt_decodeplan* plan, void* O, float* LSE, void* workspace,
-                                    size_t workspace_bytes, cudaStream_t stream) {
-  static const char* who = "pt_attn_decode";
+namespace {
+
+pt_status attn_decode(const char* who, const void* Q, int64_t q_stride, const void* Kc, const void* Vc, pt_dtype dtype,
+                      int32_t D, int32_t n_pages, int32_t page_size, const int32_t* tables, int32_t max_pages,
+                      const int32_t* lens, const int32_t* q_count, const int32_t* mask, float scale,
+                      const pt_decodeplan* plan, void* O, float* LSE, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
   if (!plan) {
     set_error("%s: plan is NULL", who);
     return PT_ERR_INVALID_ARG;
@@ -782,6 +803,9 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
   a.q_len = plan->q_len, a.Hq = plan->Hq, a.Hkv = plan->Hkv, a.g = plan->Hq / plan->Hkv, a.D = D;
   a.ps = page_size, a.max_pages = max_pages, a.n_pages = n_pages, a.cap = max_pages * page_size;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.mask = plan->q_len > 1 ? reinterpret_cast<const unsigned*>(mask) : nullptr;  // (one query sees itself in any case)
+  a.mask_w = (plan->q_len + 31) / 32;
+  a.first_seen = a.mask ? 0 : 1;
   const bool tc = dtype == PT_BF16 && decode_tc_supported(D, page_size);
   const bool tiles = tc && use_tiles(plan, D, max_pages * page_size);
   for (int c = 0; c < kDecClasses; ++c) {
@@ -813,8 +837,13 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
     a.min_units = 2;
     const size_t smem = 4 * (((size_t)m.c0.nseg + 31) / 32 + 1);
     ProfScope ps(stream, "decode_simt");
-    e = dtype == PT_BF16 ? launch_simt<__nv_bfloat16>(a, m.c0, a.workers / 8, smem, stream)
-                         : launch_simt<float>(a, m.c0, a.workers / 8, smem, stream);
+    const int grid = a.workers / 8;
+    if (a.mask)
+      e = dtype == PT_BF16 ? launch_simt<__nv_bfloat16, true>(a, m.c0, grid, smem, stream)
+                           : launch_simt<float, true>(a, m.c0, grid, smem, stream);
+    else
+      e = dtype == PT_BF16 ? launch_simt<__nv_bfloat16, false>(a, m.c0, grid, smem, stream)
+                           : launch_simt<float, false>(a, m.c0, grid, smem, stream);
     count_launch();
     if (int rc = launch_status(who, e)) return (pt_status)rc;
   }
@@ -829,4 +858,30 @@ extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void*
     count_launch();
   }
   return (pt_status)launch_status(who, e);
+}
+
+}  // namespace
+
+extern "C" pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, pt_dtype dtype,
+                                    int32_t D, int32_t n_pages, int32_t page_size, const int32_t* tables,
+                                    int32_t max_pages, const int32_t* lens, const int32_t* q_count, float scale,
+                                    const pt_decodeplan* plan, void* O, float* LSE, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  return attn_decode("pt_attn_decode", Q, q_stride, Kc, Vc, dtype, D, n_pages, page_size, tables, max_pages, lens,
+                     q_count, nullptr, scale, plan, O, LSE, workspace, workspace_bytes, stream);
+}
+
+extern "C" pt_status pt_attn_decode_drafts(const void* Q, int64_t q_stride, const void* Kc, const void* Vc,
+                                           pt_dtype dtype, int32_t D, int32_t n_pages, int32_t page_size,
+                                           const int32_t* tables, int32_t max_pages, const int32_t* lens,
+                                           const int32_t* q_count, const int32_t* draft_mask, float scale,
+                                           const pt_decodeplan* plan, void* O, float* LSE, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream) {
+  static const char* who = "pt_attn_decode_drafts";
+  if (!draft_mask) {
+    set_error("%s: draft_mask is NULL", who);
+    return PT_ERR_INVALID_ARG;
+  }
+  return attn_decode(who, Q, q_stride, Kc, Vc, dtype, D, n_pages, page_size, tables, max_pages, lens, q_count,
+                     draft_mask, scale, plan, O, LSE, workspace, workspace_bytes, stream);
 }

@@ -113,6 +113,9 @@ struct DecArgs {
   int sms;
   int workers, min_units;  // CUDA cores
   int q_vec;           // Q's rows start on 16-byte boundaries
+  const unsigned* mask;  // [n_samples * q_len][mask_w] which drafts a query sees, or NULL: those up to itself
+  int mask_w;
+  int first_seen;        // queries of a sample that all of them see: 1, or 0 with masks
   float scale_log2;
 };
 
@@ -126,7 +129,7 @@ __device__ __forceinline__ int dec_clamp(const DecArgs& a, int len) { return min
 
 // Tokens [b, e) of a node of len tokens.
 __device__ __forceinline__ void dec_range(const DecArgs& a, int kind, int len, int& b, int& e) {
-  const int body = max(len - a.q_len + 1, 0) & ~15;
+  const int body = max(len - a.q_len + a.first_seen, 0) & ~15;
   b = kind == kSegTail ? body : 0;
   e = kind == kSegBody ? body : len;
 }
@@ -151,6 +154,43 @@ __device__ __forceinline__ DecRow dec_row(const DecArgs& a, int member0, int hk,
   const int cnt = dec_count(a, s);
   d.lim = j >= cnt ? 0 : mb < 0 ? len - cnt + j + 1 : len;
   return d;
+}
+
+// The same for trees of drafts: the row sees tokens below lo, of those from lo to
+// lim the ones that its mask's bits say, and itself.
+struct DecTreeRow {
+  DecRow d;
+  int lo;
+  int mask_row;  // -1: no token in question
+};
+__device__ __forceinline__ DecTreeRow dec_tree_row(const DecArgs& a, int member0, int hk, int r, int len) {
+  DecTreeRow t;
+  t.d = dec_row(a, member0, hk, r, len);
+  t.lo = t.d.lim;
+  t.mask_row = -1;
+  const int m = (int)((unsigned)r / (unsigned)(a.g * a.q_len));
+  if (a.member[member0 + m] < 0 && t.d.lim > 0) {  // (a limit of 0: a row behind the count, or in front of the first token)
+    t.lo = len - dec_count(a, t.d.tok / a.q_len);
+    t.d.lim = len;
+    t.mask_row = t.d.tok;
+  }
+  return t;
+}
+
+// Which of 16 tokens from kv0 a row sees (bit i: token kv0 + i).
+__device__ __forceinline__ unsigned dec_sees16(const DecArgs& a, int lo, int lim, int mask_row, int kv0) {
+  const auto below = [&](int x) { return x >= 16 ? 0xffffu : x <= 0 ? 0u : (1u << x) - 1u; };
+  unsigned b = below(lo - kv0);
+  const int t = kv0 - lo;  // the first of them is draft t
+  if (mask_row >= 0 && t > -16) {
+    const unsigned* m = a.mask + (long long)mask_row * a.mask_w;
+    const int w = max(t, 0) >> 5;
+    const unsigned m0 = w < a.mask_w ? m[w] : 0u, m1 = w + 1 < a.mask_w ? m[w + 1] : 0u;
+    b |= t >= 0 ? __funnelshift_r(m0, m1, t & 31) : m0 << -t;
+    const int self = mask_row % a.q_len - t;
+    if (self >= 0 && self < 16) b |= 1u << self;
+  }
+  return b & below(lim - kv0);
 }
 
 // Page that holds the node's tokens from pi * page_size (an entry out of range
@@ -342,6 +382,7 @@ struct pt_decodeplan {
   cudaStream_t stream;  // the build stream; memory goes back to the pool in its order
   void* mem;            // one pool allocation for every array below
   int32_t N, S, Hq, Hkv, q_len;
+  bool own_leaves;      // no two samples end at one node
   float tile_gain;      // what the tile kernel saves per 128 tokens of every node that it takes
   int32_t* member;
   struct Class {

@@ -76,7 +76,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // bandwidth), 268 MB at 256 51 us (78%; 60 us with one warp for all columns,
 // which has to spill), 134 MB at 64 in pages of 16 tokens 32 us (62%).
 // ---------------------------------------------------------------------------
-template <int NP, int SPLIT>
+template <int NP, int SPLIT, bool TREE = false>
 struct RowsCfg {
   static constexpr int WARPS = SPLIT == 1 && NP == 2 ? 3 : 4, GROUPS = WARPS / SPLIT;  // GROUPS workers a CTA
   static constexpr int CTAS = SPLIT == 1 ? 3 : 2;                                      // per SM
@@ -88,8 +88,9 @@ struct RowsCfg {
   static constexpr int OFF_X = WARPS * RING;        // parts of S: two of 1 KB a warp
   static constexpr int OFF_BAR = OFF_X + (SPLIT > 1 ? WARPS * 2048 : 0);
   static constexpr int NBAR = WARPS * STAGES + (SPLIT > 1 ? GROUPS : 0);
-  static constexpr int OFF_LIM = OFF_BAR + NBAR * 8;  // [warp][piece & 1][row]
-  static constexpr int OFF_PIECE = OFF_LIM + WARPS * 2 * kRowsR * 4;  // [warp][piece & 1]
+  static constexpr int LIMS = 2 * kRowsR * (TREE ? 3 : 1);  // [piece & 1][row] limits; with trees, then what all see, then mask rows
+  static constexpr int OFF_LIM = OFF_BAR + NBAR * 8;       // [warp]
+  static constexpr int OFF_PIECE = OFF_LIM + WARPS * LIMS * 4;  // [warp][piece & 1]
   static constexpr int OFF_CHUNK = OFF_PIECE + WARPS * 2 * (int)sizeof(DecPiece);
   static constexpr size_t smem(int nseg) { return OFF_CHUNK + 8 * ((size_t)(nseg + 31) / 32 + 1) + 1024; }
 };
@@ -98,12 +99,12 @@ struct RowsCfg {
 // barriers (initialised for one arrival), room for two pieces and their rows'
 // limits, and of the worker the room for S's parts and its barrier (SPLIT
 // arrivals).
-template <int NP, int SPLIT>
+template <int NP, int SPLIT, bool TREE>
 __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a,
                                             const DecClass& c, const int* chunk, int per, int worker, int sw,
                                             uint8_t* ring, uint64_t* full, DecPiece* pieces, int* lims, float4* xbuf,
                                             uint64_t* xbar, volatile int* abort_flag) {
-  using C = RowsCfg<NP, SPLIT>;
+  using C = RowsCfg<NP, SPLIT, TREE>;
   const int lane = threadIdx.x & 31;
   const int col0 = SPLIT == 1 ? 0 : sw * 128;  // this warp's first column
   const uint32_t ring_u = smem_u32(ring);
@@ -116,6 +117,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
   // the current piece
   int t = 0, t1 = 0, kv_base = 0, rows_left = 0, lim_min = 0, lim_max = 0;
   int lim[2] = {0, 0};
+  int lo[2] = {0, 0}, mask_row[2] = {-1, -1};  // TREE
   int slot = 0;
   uint8_t* qbuf = ring + C::STAGES * C::STAGE;
   float o[NP * 8][4], m[2], l[2];
@@ -146,7 +148,15 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
         // the piece's query rows, asynchronously into the buffer that the current piece does not use; lane r looks row r up
         long long src = -1;
         if (lane < min(lp.rows - lp.rt * kRowsR, kRowsR)) {
-          const DecRow d = dec_row(a, lp.member0, lp.hk, lp.rt * kRowsR + lane, lp.len);
+          DecRow d;
+          if constexpr (TREE) {
+            const DecTreeRow tr = dec_tree_row(a, lp.member0, lp.hk, lp.rt * kRowsR + lane, lp.len);
+            lims[(2 + (found & 1)) * kRowsR + lane] = tr.lo;
+            lims[(4 + (found & 1)) * kRowsR + lane] = tr.mask_row;
+            d = tr.d;
+          } else {
+            d = dec_row(a, lp.member0, lp.hk, lp.rt * kRowsR + lane, lp.len);
+          }
           lims[(found & 1) * kRowsR + lane] = d.lim;
           src = (long long)d.tok * a.q_stride + (long long)d.head * a.D + col0;
         }
@@ -217,7 +227,11 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       for (int i = 0; i < 2; ++i) {
         const bool row = r_lo + i * 8 < rows_left;
         lim[i] = row ? lims[(at & 1) * kRowsR + r_lo + i * 8] : 0;
-        if (row) own_lo = min(own_lo, lim[i]);
+        if constexpr (TREE) {
+          lo[i] = row ? lims[(2 + (at & 1)) * kRowsR + r_lo + i * 8] : 0;
+          mask_row[i] = row ? lims[(4 + (at & 1)) * kRowsR + r_lo + i * 8] : -1;
+        }
+        if (row) own_lo = min(own_lo, TREE ? lo[i] : lim[i]);
         m[i] = -INFINITY, l[i] = 0.f;
       }
       ++at;
@@ -274,12 +288,18 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       }
     }
     int n_mul = kRowsBT, n_any = kRowsBT;  // tokens whose values the product takes; tokens that any row keeps
+    unsigned sees[2] = {0, 0};             // TREE: the tile's tokens that this lane's rows keep
     if (kv0 + kRowsBT > lim_min) {
+      if constexpr (TREE) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sees[i] = dec_sees16(a, lo[i], lim[i], mask_row[i], kv0);
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1]) x[n][i] = -INFINITY;
+          if (TREE ? !(sees[i >> 1] >> (n * 8 + c2 + (i & 1)) & 1u) : kv0 + n * 8 + c2 + (i & 1) >= lim[i >> 1])
+            x[n][i] = -INFINITY;
       // Values that no row keeps are cleared: a probability of 0 times what
       // lies behind the node's tokens must stay 0.  Tokens that some rows keep
       // and others do not go through the product too unless one is not finite:
@@ -362,7 +382,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
           const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (kv0 + n < lim[i]) {
+            if (TREE ? sees[i] >> n & 1u : kv0 + n < lim[i]) {
               o[k][2 * i] = fmaf(pr[i], v0, o[k][2 * i]);
               o[k][2 * i + 1] = fmaf(pr[i], v1, o[k][2 * i + 1]);
             }
@@ -440,11 +460,11 @@ __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& 
   return s;
 }
 
-template <int NP, int SPLIT>
+template <int NP, int SPLIT, bool TREE>
 __global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SPLIT>::CTAS)
     k_decode_rows(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const DecArgs a,
                   const DecClass c, const DecClass ct) {
-  using C = RowsCfg<NP, SPLIT>;
+  using C = RowsCfg<NP, SPLIT, TREE>;
   // Beside a tile kernel this one starts when that one has begun (it has then
   // waited for what came before both), runs on the SMs that it leaves, and
   // ends after it, so that waiting for this kernel is waiting for both.
@@ -472,10 +492,10 @@ __global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SP
   const DecSplit sp = dec_split<NP>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::GROUPS);
   if ((int)blockIdx.x == 0) dec_publish(a, c, kRows, chunk, sp.per_r);
   if ((int)blockIdx.x < (a.sms - sp.n_tile) * C::CTAS)
-    rows_worker<NP, SPLIT>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::GROUPS + warp / SPLIT, warp % SPLIT,
+    rows_worker<NP, SPLIT, TREE>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::GROUPS + warp / SPLIT, warp % SPLIT,
                            smem + warp * C::RING, bars + warp * C::STAGES,
                            reinterpret_cast<DecPiece*>(smem + C::OFF_PIECE) + warp * 2,
-                           reinterpret_cast<int*>(smem + C::OFF_LIM) + warp * 2 * kRowsR,
+                           reinterpret_cast<int*>(smem + C::OFF_LIM) + warp * C::LIMS,
                            reinterpret_cast<float4*>(smem + C::OFF_X) + (warp / SPLIT) * (SPLIT * 128),
                            bars + C::WARPS * C::STAGES + warp / SPLIT, &abort_flag);
   if (beside) pdl_wait();
@@ -1002,17 +1022,25 @@ cudaError_t opt_in_smem(K kernel, size_t bytes, std::atomic<uint64_t>& opted) {
   return e;
 }
 
-template <int NP, int SPLIT>
+template <int NP, int SPLIT, bool TREE>
 cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
                         const DecClass& ct, cudaStream_t s) {
-  using C = RowsCfg<NP, SPLIT>;
+  using C = RowsCfg<NP, SPLIT, TREE>;
   static_assert(C::CTAS * C::GROUPS <= kRowsWarps, "the workspace's slots");
   const size_t smem = C::smem(c.nseg);
-  auto kernel = k_decode_rows<NP, SPLIT>;
+  auto kernel = k_decode_rows<NP, SPLIT, TREE>;
   static std::atomic<uint64_t> opted{0};
   if (cudaError_t e = opt_in_smem(kernel, C::smem(kDecMaxNodes), opted)) return e;
   count_launch();
   return launch_pdl(kernel, dim3(a.sms * C::CTAS), dim3(C::WARPS * 32), smem, s, mK, mV, a, c, ct);
+}
+
+template <bool TREE>
+cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
+                        const DecClass& ct, cudaStream_t s) {
+  if (a.D <= 64) return launch_rows<1, 1, TREE>(mK, mV, a, c, ct, s);
+  if (a.D <= 128) return launch_rows<2, 1, TREE>(mK, mV, a, c, ct, s);
+  return a.D <= 256 ? launch_rows<2, 2, TREE>(mK, mV, a, c, ct, s) : launch_rows<2, 4, TREE>(mK, mV, a, c, ct, s);
 }
 
 template <int NP>
@@ -1052,10 +1080,7 @@ int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const Dec
                 : launch_tile<2>(mKt, mVt, a, tile, rows, box, (int)heads, s);
   }
   if (e == cudaSuccess && rows.nitems)
-    e = a.D <= 64    ? launch_rows<1, 1>(mK, mV, a, rows, tile, s)
-        : a.D <= 128 ? launch_rows<2, 1>(mK, mV, a, rows, tile, s)
-        : a.D <= 256 ? launch_rows<2, 2>(mK, mV, a, rows, tile, s)
-                     : launch_rows<2, 4>(mK, mV, a, rows, tile, s);
+    e = a.mask ? launch_rows<true>(mK, mV, a, rows, tile, s) : launch_rows<false>(mK, mV, a, rows, tile, s);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("pt_attn_decode: launch failed: %s", cudaGetErrorString(e));

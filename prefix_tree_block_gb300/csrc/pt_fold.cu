@@ -63,6 +63,8 @@ struct pt_foldplan {
   // contiguous copy), or one token of a shared node with all its copies
   int32_t n_tasks;
   int4* tasks;
+  int32_t n_follow;    // tokens that follow another
+  int2* follow;        // [n_nodes] {entries of the rows before the node's, entry of the node's first token}
 };
 
 namespace {
@@ -421,6 +423,21 @@ __global__ void k_fold_positions(const int32_t* __restrict__ tok_pos, int T, int
   for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < T; t += gridDim.x * blockDim.x) pos[t] = tok_pos[t];
 }
 
+// Which tokens follow which, as lists by the token before: a node's tokens
+// follow one another, its first one the last of the nearest node above it that
+// has any; behind all lists, the tokens that follow none.
+__global__ void k_fold_successors(const int4* __restrict__ node, const int2* __restrict__ follow,
+                                  const int32_t* __restrict__ tok_node, int T, int n_follow,
+                                  int32_t* __restrict__ succ_ptr, int32_t* __restrict__ succ) {
+  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < T; t += gridDim.x * blockDim.x) {
+    const int i = tok_node[t], k = t - node[i].x;
+    const int2 f = follow[i];
+    succ_ptr[t] = f.x + k;
+    succ[k > 0 ? f.x + k - 1 : f.y] = t;
+    if (t == 0) succ_ptr[T] = n_follow;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host helpers
 
@@ -619,6 +636,28 @@ extern "C" pt_status pt_fold_plan(const int32_t* node_lengths, int32_t n_nodes, 
       copiesM += (long long)node_lengths[i] * n_through[i];
     }
   }
+  // lists of following tokens: the nearest node above with tokens, its children with tokens
+  std::vector<int2> follow(std::max(N, 1));
+  std::vector<int> above(N, -1), below(N, 0);
+  int n_follow = 0;
+  for (int i = 0; i < N; ++i) {
+    const int p = parent[i];
+    if (p >= 0) above[i] = node_lengths[p] > 0 ? p : above[p];
+    if (node_lengths[i] > 0 && above[i] >= 0) ++below[above[i]];
+  }
+  for (int i = 0; i < N; ++i) {
+    follow[i] = make_int2(n_follow, 0);
+    if (node_lengths[i] > 0) n_follow += node_lengths[i] - 1 + below[i];
+  }
+  {
+    std::vector<int> used(N, 0);
+    int none = n_follow;
+    for (int i = 0; i < N; ++i)
+      if (node_lengths[i] > 0) {
+        const int p = above[i];
+        follow[i].y = p >= 0 ? follow[p].x + node_lengths[p] - 1 + used[p]++ : none++;
+      }
+  }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     set_error("%s: no CUDA device", who);
@@ -630,8 +669,8 @@ extern "C" pt_status pt_fold_plan(const int32_t* node_lengths, int32_t n_nodes, 
                b_roll = pad(4 * std::max((size_t)S * L, (size_t)1));
   const size_t b_c1 = pad(sizeof(int2) * std::max<size_t>(cls1.size(), 1)),
                b_cM = pad(sizeof(int2) * std::max<size_t>(clsM.size(), 1)),
-               b_tk = pad(sizeof(int4) * std::max<size_t>(tasks.size(), 1));
-  const size_t tables = b_node + b_sp + b_samp + b_pp + b_pn + b_c1 + b_cM + b_tk;
+               b_tk = pad(sizeof(int4) * std::max<size_t>(tasks.size(), 1)), b_fo = pad(sizeof(int2) * follow.size());
+  const size_t tables = b_node + b_sp + b_samp + b_pp + b_pn + b_c1 + b_cM + b_tk + b_fo;
   const size_t total = tables + 3 * b_tok + b_roll;
   pt_foldplan* p = new pt_foldplan();
   p->device = dev;
@@ -646,6 +685,7 @@ extern "C" pt_status pt_fold_plan(const int32_t* node_lengths, int32_t n_nodes, 
   p->TM = TM;
   p->copiesM = copiesM;
   p->n_tasks = (int32_t)tasks.size();
+  p->n_follow = n_follow;
   int rc = pt::pool_alloc(&p->mem, total, dev, stream);
   if (rc) {
     delete p;
@@ -661,6 +701,7 @@ extern "C" pt_status pt_fold_plan(const int32_t* node_lengths, int32_t n_nodes, 
   p->cls1 = reinterpret_cast<int2*>(base + o), o += b_c1;
   p->clsM = reinterpret_cast<int2*>(base + o), o += b_cM;
   p->tasks = reinterpret_cast<int4*>(base + o), o += b_tk;
+  p->follow = reinterpret_cast<int2*>(base + o), o += b_fo;
   p->tok_node = reinterpret_cast<int32_t*>(base + o), o += b_tok;
   p->tok_src = reinterpret_cast<int32_t*>(base + o), o += b_tok;
   p->tok_pos = reinterpret_cast<int32_t*>(base + o), o += b_tok;
@@ -679,6 +720,8 @@ extern "C" pt_status pt_fold_plan(const int32_t* node_lengths, int32_t n_nodes, 
   if (!clsM.empty()) std::memcpy(host.data() + h, clsM.data(), sizeof(int2) * clsM.size());
   h += b_cM;
   if (!tasks.empty()) std::memcpy(host.data() + h, tasks.data(), sizeof(int4) * tasks.size());
+  h += b_tk;
+  std::memcpy(host.data() + h, follow.data(), sizeof(int2) * follow.size());
   rc = pt::upload(p->mem, host.data(), tables, dev, stream);
   if (rc) {
     set_error("%s: upload of the plan tables failed", who);
@@ -873,6 +916,31 @@ extern "C" pt_status pt_fold_positions(const pt_foldplan* p, int64_t* pos, cudaS
     pt::ProfScope ps(stream, "fold_positions");
     const int cap = pt::num_sms(p->device) * 8;
     k_fold_positions<<<std::max(1, std::min((p->T + 255) / 256, cap)), 256, 0, stream>>>(p->tok_pos, p->T, pos);
+    pt::count_launch();
+  }
+  return (pt_status)launch_status(who);
+}
+
+extern "C" pt_status pt_fold_successors(const pt_foldplan* p, int32_t* succ_ptr, int32_t* succ, cudaStream_t stream) {
+  static const char* who = "pt_fold_successors";
+  int rc = check_plan(p, who);
+  if (rc) return (pt_status)rc;
+  if (!succ_ptr || (p->T > 0 && !succ)) {
+    set_error("%s: null buffer", who);
+    return PT_ERR_INVALID_ARG;
+  }
+  if (p->T == 0) {
+    if (cudaMemsetAsync(succ_ptr, 0, sizeof(int32_t), stream) != cudaSuccess) {
+      set_error("%s: clearing succ_ptr failed", who);
+      return PT_ERR_CUDA;
+    }
+    return PT_OK;
+  }
+  {
+    pt::ProfScope ps(stream, "fold_successors");
+    const int cap = pt::num_sms(p->device) * 8;
+    k_fold_successors<<<std::max(1, std::min((p->T + 255) / 256, cap)), 256, 0, stream>>>(p->node, p->follow, p->tok_node, p->T,
+                                                                                         p->n_follow, succ_ptr, succ);
     pt::count_launch();
   }
   return (pt_status)launch_status(who);
