@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
     float q[R][DL], acc[R][DL];
     int lim_max = 0, lim_min = INT_MAX, my_lim = 0;  // (the least of the rows there are)
     int lim[R];
-    int my_lo = 0, my_mask = -1;  // TREE: what the row sees in any case, and its mask's row
+    int my_lo = 0, my_mask = -1, my_self = 0;  // TREE: what the row sees in any case, its mask's row, its own draft
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = p.rt * R + r;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
           const DecTreeRow tr = dec_tree_row(a, p.member0, p.hk, row, p.len);
           d = tr.d;
           lim_min = min(lim_min, tr.lo);
-          if (r == my_r) my_lo = tr.lo, my_mask = tr.mask_row;
+          if (r == my_r) my_lo = tr.lo, my_mask = tr.mask_row, my_self = tr.mask_row % a.q_len;
         } else {
           d = dec_row(a, p.member0, p.hk, row, p.len);
           lim_min = min(lim_min, d.lim);
@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
     for (int kv0 = b + p.t0 * kSimtBT; kv0 < end; kv0 += STEP) {
       // this step's values are loaded with its keys, and the next step's pages are looked up now
       const long long off = next;
+      unsigned sees = 0xffffu;  // TREE: the step's tokens that row my_r sees
+      if (TREE && kv0 + STEP > lim_min) sees = dec_sees16(a, my_lo, my_lim, my_mask, my_self, kv0);
       V kk[STEP][NV], vv[EARLY ? STEP : 1][NV];
 #pragma unroll
       for (int u = 0; u < STEP; ++u) {
@@ -166,10 +168,9 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
         }
         d[0] += __shfl_xor_sync(0xffffffffu, d[0], 1);
         const int kv = kv0 + gq * 4 + ((lane >> 1) & 3);
-        bool sees = kv < end && kv < my_lim;
-        if (TREE && sees && kv >= my_lo) sees = dec_sees16(a, my_lo, my_lim, my_mask, kv) & 1u;
-        s[gq] = sees ? d[0] : -INFINITY;
-        if (TREE && !sees) hidden |= 1 << gq;
+        const bool in = kv < end && (TREE ? sees >> (kv - kv0) & 1u : kv < my_lim);
+        s[gq] = in ? d[0] : -INFINITY;
+        if (TREE && !in) hidden |= 1 << gq;
       }
       float mt = fmaxf(s[0], s[1]);
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
@@ -210,8 +211,8 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
 #pragma unroll
               for (int r = 0; r < R; ++r) {  // a value that the row must not see does not reach it, whatever it is
                 const float y = fmaf(pr[r], to_f(w.e[x]), acc[r][v * VEC + x]);
-                const bool sees = !masked || (TREE ? !(pr[r] < 0.f) : kv0 + i < lim[r]);
-                acc[r][v * VEC + x] = sees ? y : acc[r][v * VEC + x];
+                const bool in = !masked || (TREE ? !(pr[r] < 0.f) : kv0 + i < lim[r]);
+                acc[r][v * VEC + x] = in ? y : acc[r][v * VEC + x];
               }
           }
         }

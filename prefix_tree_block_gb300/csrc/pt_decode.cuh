@@ -177,8 +177,9 @@ __device__ __forceinline__ DecTreeRow dec_tree_row(const DecArgs& a, int member0
   return t;
 }
 
-// Which of 16 tokens from kv0 a row sees (bit i: token kv0 + i).
-__device__ __forceinline__ unsigned dec_sees16(const DecArgs& a, int lo, int lim, int mask_row, int kv0) {
+// Which of 16 tokens from kv0 a row sees (bit i: token kv0 + i); self: its own
+// draft's number.
+__device__ __forceinline__ unsigned dec_sees16(const DecArgs& a, int lo, int lim, int mask_row, int self, int kv0) {
   const auto below = [&](int x) { return x >= 16 ? 0xffffu : x <= 0 ? 0u : (1u << x) - 1u; };
   unsigned b = below(lo - kv0);
   const int t = kv0 - lo;  // the first of them is draft t
@@ -187,8 +188,7 @@ __device__ __forceinline__ unsigned dec_sees16(const DecArgs& a, int lo, int lim
     const int w = max(t, 0) >> 5;
     const unsigned m0 = w < a.mask_w ? m[w] : 0u, m1 = w + 1 < a.mask_w ? m[w + 1] : 0u;
     b |= t >= 0 ? __funnelshift_r(m0, m1, t & 31) : m0 << -t;
-    const int self = mask_row % a.q_len - t;
-    if (self >= 0 && self < 16) b |= 1u << self;
+    if ((unsigned)(self - t) < 16u) b |= 1u << (self - t);
   }
   return b & below(lim - kv0);
 }

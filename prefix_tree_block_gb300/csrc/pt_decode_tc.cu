@@ -117,7 +117,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
   // the current piece
   int t = 0, t1 = 0, kv_base = 0, rows_left = 0, lim_min = 0, lim_max = 0;
   int lim[2] = {0, 0};
-  int lo[2] = {0, 0}, mask_row[2] = {-1, -1};  // TREE
+  int lo[2] = {0, 0}, mask_row[2] = {-1, -1}, self[2] = {0, 0};  // TREE
   int slot = 0;
   uint8_t* qbuf = ring + C::STAGES * C::STAGE;
   float o[NP * 8][4], m[2], l[2];
@@ -230,6 +230,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
         if constexpr (TREE) {
           lo[i] = row ? lims[(2 + (at & 1)) * kRowsR + r_lo + i * 8] : 0;
           mask_row[i] = row ? lims[(4 + (at & 1)) * kRowsR + r_lo + i * 8] : -1;
+          self[i] = mask_row[i] % a.q_len;
         }
         if (row) own_lo = min(own_lo, TREE ? lo[i] : lim[i]);
         m[i] = -INFINITY, l[i] = 0.f;
@@ -243,12 +244,17 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     }
     // --- a tile of 16 tokens
     const uint32_t s = used % C::STAGES;
+    const int kv0 = kv_base + t * kRowsBT;
+    unsigned sees[2] = {0, 0};  // TREE: the tile's tokens that this lane's rows keep, looked up while the tile is on its way
+    if (TREE && kv0 + kRowsBT > lim_min) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sees[i] = dec_sees16(a, lo[i], lim[i], mask_row[i], self[i], kv0);
+    }
     ok = mbar_wait(full + s, (used / C::STAGES) & 1, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     const uint32_t kb = ring_u + s * C::STAGE, vb = kb + NP * C::PANEL;
     const uint32_t qa = ring_u + C::STAGES * C::STAGE + ((at - 1) & 1) * C::QBUF;
-    const int kv0 = kv_base + t * kRowsBT;
     // S, in two chains of accumulation a column tile
     float sc[2][2][4];
 #pragma unroll
@@ -288,12 +294,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       }
     }
     int n_mul = kRowsBT, n_any = kRowsBT;  // tokens whose values the product takes; tokens that any row keeps
-    unsigned sees[2] = {0, 0};             // TREE: the tile's tokens that this lane's rows keep
     if (kv0 + kRowsBT > lim_min) {
-      if constexpr (TREE) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sees[i] = dec_sees16(a, lo[i], lim[i], mask_row[i], kv0);
-      }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -310,8 +311,21 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       uint8_t* vs = ring + s * C::STAGE + NP * C::PANEL;
       if (n_all < n_any) {
         bool odd = false;
+        if constexpr (TREE) {  // (all drafts are in question here: 0 times each value, several loads at a time; not 0: not finite)
+          const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
+          __nv_bfloat162 sum[2] = {none, none};
+#pragma unroll 4
+          for (int i = n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vs + ((i % (NP * 8)) >> 3) * C::PANEL + (i / (NP * 8)) * 128 + (i & 7) * 16);
+            const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v);
+            sum[0] = __hfma2(w[0], none, sum[0]), sum[1] = __hfma2(w[1], none, sum[1]);
+            sum[0] = __hfma2(w[2], none, sum[0]), sum[1] = __hfma2(w[3], none, sum[1]);
+          }
+          const float2 f = __bfloat1622float2(__hadd2(sum[0], sum[1]));
+          odd = !(f.x == 0.f && f.y == 0.f);
+        }
 #pragma unroll 1
-        for (int i = n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
+        for (int i = TREE ? INT_MAX : n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
           const uint4 v = *reinterpret_cast<const uint4*>(vs + ((i % (NP * 8)) >> 3) * C::PANEL + (i / (NP * 8)) * 128 +
                                                           (i & 7) * 16);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -452,7 +466,8 @@ __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& 
   s.n_tile = units_t > 0 ? sms : 0;
   if (units_t > 0 && units_r > 0) {
     // (a tile unit of 128 rows costs an SM about as much as 10 units of 16 rows and tokens, 14 at head_dim 64)
-    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f);
+    // (with masks a row tile's tokens are masked ones in all of a tail, and cost about twice that)
+    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f) * (a.mask ? 0.5f : 1.f);
     s.n_tile = min(max((int)(sms * (x / (x + (float)cost[1]))), 1), sms - 1);
   }
   s.per_t = dec_share(units_t, max(s.n_tile, 1), kTileMinUnits);

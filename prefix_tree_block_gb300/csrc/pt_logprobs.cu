@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "pt.h"
 #include "pt_device.cuh"
@@ -109,16 +110,25 @@ struct Row {
   __device__ __forceinline__ uint4 load(int s) const {  // of a whole slot
     return __ldg(reinterpret_cast<const uint4*>(x + ((long long)s * V - lead)));
   }
-  __device__ __forceinline__ void get(int s, float (&f)[V]) const {  // -inf where there is no element
-    if (whole(s)) {
-      unpack(load(s), f);
-    } else {
+  __device__ __forceinline__ uint4 pack(int s) const {  // any slot; -inf where there is no element
+    if (whole(s)) return load(s);
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(E) == 4) {
         const int v = s * V - lead + i;
-        f[i] = v >= 0 && v < n ? Type<E>::f(x[v]) : -INFINITY;
+        w[i] = v >= 0 && v < n ? __float_as_uint(x[v]) : 0xff800000u;
+      } else {
+        const int v = s * V - lead + 2 * i;
+        const uint32_t lo = v >= 0 && v < n ? __bfloat16_as_ushort(x[v]) : 0xff80u;
+        const uint32_t hi = v + 1 >= 0 && v + 1 < n ? __bfloat16_as_ushort(x[v + 1]) : 0xff80u;
+        w[i] = lo | hi << 16;
       }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void get(int s, float (&f)[V]) const {
+    unpack(pack(s), f);
   }
 };
 
@@ -137,22 +147,57 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
 }
 __device__ __forceinline__ int index_of(unsigned long long key) { return (int)(0xffffffffu - (unsigned)key); }
 
-// Running statistics of a softmax: the maximum, the sum of exp(z - m), and the
-// sum of (x - m) exp(z - m).
+// Statistics of a softmax in base 2, c1 = scale log2(e): a logit m near the
+// largest, and the sums of 2^((x - m) c1) and of (x - m) c1 2^((x - m) c1).
 struct Stat {
   float m, s, t;
 };
-// Both on the larger maximum.  c1 = scale * log2(e).
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c1) {
-  Stat r;
-  r.m = fmaxf(a.m, b.m);
-  const float ref = r.m == -INFINITY ? 0.f : r.m;
-  const float da = a.m - ref, db = b.m - ref;
-  const float fa = ex2(da * c1), fb = ex2(db * c1);
-  r.s = a.s * fa + b.s * fb;
-  // (a part without a weight has no share, however far below its maximum is)
-  r.t = (fa > 0.f ? fa * fmaf(da, a.s, a.t) : a.t != a.t ? a.t : 0.f) + (fb > 0.f ? fb * fmaf(db, b.s, b.t) : b.t != b.t ? b.t : 0.f);
+// The sums when every exponent grows by d.  (A sum without weight has no share,
+// however far below it was.)
+__device__ __forceinline__ void rebase(float& s, float& t, float d) {
+  const float f = ex2(d);
+  t = f > 0.f ? f * fmaf(d, s, t) : t != t ? t : 0.f;
+  s *= f;
+}
+// Of the warp's lanes below 2 * HALF, in all of them: on the largest m, then summed.
+template <int HALF>
+__device__ __forceinline__ Stat join_lanes(Stat a, float c1) {
+  float m = a.m;
+#pragma unroll
+  for (int o = HALF; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  rebase(a.s, a.t, (a.m - (m == -INFINITY ? 0.f : m)) * c1);
+#pragma unroll
+  for (int o = HALF; o; o >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
+  }
+  return Stat{m, a.s, a.t};
+}
+
+// Largest of packed pairs of bf16 (NaN gives way), and the same with NaN kept.
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The sums of one slot's terms, by differences from m.
+template <class E>
+__device__ __noinline__ float2 far_terms(uint4 v, float m, float c1) {
+  float x[Type<E>::V], s = 0.f, t = 0.f;
+  unpack(v, x);
+#pragma unroll
+  for (int k = 0; k < Type<E>::V; ++k) {
+    const float d = (x[k] - m) * c1, e = ex2(d);
+    s += e;
+    t = fmaf(fmaxf(d, -3.402823466e38f), e, t);
+  }
+  return make_float2(s, t);
 }
 
 struct ScoreArgs {
@@ -188,10 +233,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
   constexpr int V = Type<E>::V, U = 4;
   __shared__ Stat sm_stat[NT / 32];
   __shared__ Stat sm_part;
+  __shared__ unsigned sm_most[NT / 32];
   __shared__ unsigned long long sm_key[TOP ? NT : 1], sm_cand[TOP ? kCandidates : 1], sm_best[TOP ? kMaxTop : 1];
   __shared__ int sm_who[TOP ? NT : 1];
   __shared__ int sm_n, sm_w;
-  __shared__ unsigned long long sm_bound;
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int part = blockIdx.x % a.parts, r = blockIdx.x / a.parts;
@@ -209,29 +254,87 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
       if (my_target >= 0) my_x = Type<E>::f(row.x[my_target]);
     }
   }
+  // A term's exponent is one fused product and difference, x c1 - ref with ref the
+  // rounded m c1; what the rounding took is made up for at the end.
+  // ref follows the largest logit in steps of 2^8 of the terms' size.
   Stat st = {-INFINITY, 0.f, 0.f};
-  int first = -1;  // TOP: the slots (from this one on, U of them) that the maximum was first seen in
-  auto take = [&](const float* x, int n, int at) {  // n values of slots from `at` on
-    float bm = x[0];
+  float ref = 0.f, next = -INFINITY, own_max = -INFINITY;
+  bool plain = true;  // (ref is small enough for that (what it lost is below 1 / 16); else the sums are m's own)
+  int first = -1;     // TOP: the slots (from this one on, U of them) that the largest was first seen in
+  // Terms that are 0 in any case are raised to `low`, where their exponent is
+  // finite: 0 times it stays 0.  It lies so far below m, by 2^13 in the exponent
+  // and by several steps of bf16, that no term with a weight is touched.
+  float low = -1e4f / a.c1;
+  uint32_t low2 = pack_bf16(low, low);
+  auto take = [&](const uint4* v, auto count, int at) {  // so many slots from `at` on
+    constexpr int n = decltype(count)::value;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+    float bm;
+    if constexpr (sizeof(E) == 2) {
+      uint32_t b[4] = {w[0], w[1], w[2], w[3]};
 #pragma unroll
-    for (int i = 1; i < n; ++i) bm = fmaxf(bm, x[i]);
-    if (first < 0) first = at;
-    if (bm > st.m) {
-      const float f = ex2((st.m - bm) * a.c1);
-      st.t = f > 0.f ? f * fmaf(st.m - bm, st.s, st.t) : st.t != st.t ? st.t : 0.f;
-      st.s *= f;
-      st.m = bm;
-      first = at;
+      for (int i = 4; i < 4 * n; ++i) b[i & 3] = max_bf2(b[i & 3], w[i]);
+      const uint32_t c = max_bf2(max_bf2(b[0], b[1]), max_bf2(b[2], b[3]));
+      bm = fmaxf(__uint_as_float(c << 16), __uint_as_float(c & 0xffff0000u));
+    } else {
+      bm = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+#pragma unroll
+      for (int i = 4; i < 4 * n; i += 2) bm = fmax3(bm, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
     }
-    const float ref = st.m == -INFINITY ? 0.f : st.m;
+    if constexpr (TOP) {
+      if (first < 0 || bm > own_max) first = at;
+      own_max = fmaxf(own_max, bm);
+    }
+    if (bm > next) {
+      const float old = st.m, old_ref = ref;
+      const bool was = plain;
+      st.m = bm;
+      next = bm + 8.f / a.c1;
+      const float base = st.m == -INFINITY ? 0.f : st.m;
+      ref = base * a.c1;
+      plain = fabsf(ref) < 1048576.f && fabsf(base) < 1e37f;
+      if (old != -INFINITY)
+        rebase(st.s, st.t, was && plain ? old_ref - ref
+                                        : (old - base) * a.c1 - (was ? fmaf(old, a.c1, -old_ref) : 0.f) + (plain ? fmaf(base, a.c1, -ref) : 0.f));
+      low = base - fmaxf(1e4f / a.c1, fabsf(base) * 0.03125f);
+      low2 = pack_bf16(low, low);
+    }
+    if (plain) {
+      const unsigned long long c2 = f2_splat(a.c1), r2 = f2_splat(-ref);
+      unsigned long long s2[2] = {0ull, 0ull}, t2[2] = {0ull, 0ull};
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float d = x[i] - ref;
-      const float e = ex2(d * a.c1);
-      st.s += e;
-      st.t = fmaf(fmaxf(d, -3.402823466e38f), e, st.t);
+      for (int i = 0; i < 4 * n; ++i) {
+        unsigned long long x2;
+        if constexpr (sizeof(E) == 2) {
+          const uint32_t y = max_nan_bf2(w[i], low2);
+          x2 = f2_pack(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+        } else {
+          if (i & 1) continue;
+          const float x = __uint_as_float(w[i]), y = __uint_as_float(w[i + 1]);
+          x2 = f2_pack(x < low ? low : x, y < low ? low : y);
+        }
+        const unsigned long long d2 = f2_fma(x2, c2, r2);
+        float d0, d1;
+        f2_unpack(d2, d0, d1);
+        const unsigned long long e2 = f2_pack(ex2(d0), ex2(d1));
+        s2[(i >> 1) & 1] = f2_add(s2[(i >> 1) & 1], e2);
+        t2[(i >> 1) & 1] = f2_fma(d2, e2, t2[(i >> 1) & 1]);
+      }
+      float x0, x1, y0, y1;
+      f2_unpack(f2_add(s2[0], s2[1]), x0, x1);
+      f2_unpack(f2_add(t2[0], t2[1]), y0, y1);
+      st.s += x0 + x1;
+      st.t += y0 + y1;
+    } else {  // logits (times scale) of a million and more, infinities: differences first
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float2 d = far_terms<E>(v[i], st.m == -INFINITY ? 0.f : st.m, a.c1);
+        st.s += d.x, st.t += d.y;
+      }
     }
   };
+  using One = std::integral_constant<int, 1>;
+  using All = std::integral_constant<int, U>;
   // whole slots, then the ones at the row's ends
   const int w0 = max(s0, row.whole(0) ? 0 : 1), w1 = min(s1, row.whole(slots - 1) ? slots : slots - 1);
 #pragma unroll 1
@@ -241,79 +344,68 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
     for (int u = 0; u < U; ++u)
       if (s + u * NT < w1) v[u] = row.load(s + u * NT);
     if (s + (U - 1) * NT < w1) {
-      float x[U * V];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float y[V];
-        unpack(v[u], y);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[u * V + i] = y[i];
-      }
-      take(x, U * V, s);
+      take(v, All{}, s);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (s + u * NT < w1) {
-          float y[V];
-          unpack(v[u], y);
-          take(y, V, s + u * NT);
-        }
+        if (s + u * NT < w1) take(v + u, One{}, s + u * NT);
     }
   }
   int edge = -1;  // a slot at the row's end that is this thread's
   if (tid == 0 && s0 == 0 && s1 > 0 && !row.whole(0)) edge = 0;
   if (tid == NT - 1 && s1 == slots && s1 > s0 && slots > 1 && !row.whole(slots - 1)) edge = slots - 1;
   if (edge >= 0) {
-    float y[V];
-    row.get(edge, y);
-    take(y, V, edge);
+    const uint4 y = row.pack(edge);
+    take(&y, One{}, edge);
   }
-  const float own_max = st.m;
+  if (plain) rebase(st.s, st.t, -fmaf(st.m == -INFINITY ? 0.f : st.m, a.c1, -ref));
   // the CTA's statistics
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    b.t = __shfl_xor_sync(0xffffffffu, st.t, o);
-    st = join(st, b, a.c1);
-  }
+  st = join_lanes<16>(st, a.c1);
   if (lane == 0) sm_stat[warp] = st;
+  unsigned mine = 0;  // TOP: this thread's largest logit
   if constexpr (TOP) {
-    sm_key[tid] = first >= 0 ? (unsigned long long)ordered(own_max) << 32 : 0ull;
+    mine = first >= 0 ? ordered(own_max) : 0u;
+    const unsigned most = __reduce_max_sync(0xffffffffu, mine);
+    if (lane == 0) sm_most[warp] = most;
     if (tid == 0) sm_n = sm_w = 0;
   }
   __syncthreads();
-  st = sm_stat[0];
-#pragma unroll 1
-  for (int w = 1; w < NT / 32; ++w) st = join(st, sm_stat[w], a.c1);
+  if (warp == 0) {
+    st = join_lanes<NT / 64>(lane < NT / 32 ? sm_stat[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c1);
+    if (lane == 0) sm_part = st;
+  }
   if constexpr (TOP) {
-    // the bound: the k-th largest of the threads' maxima
+    // The bound: at least k threads' maxima reach it, by halving; not many more
+    // unless they are equal.
     const int k = a.k;
-    unsigned long long mine = sm_key[tid];
-    {
-      int above = 0, same = 0;
-#pragma unroll 4
-      for (int i = 0; i < NT; ++i) {
-        const unsigned long long o = sm_key[i];
-        above += o > mine, same += o == mine;
-      }
-      if (above < k && above + same >= k) sm_bound = mine;  // (all that hold it write the same; 0: fewer than k have any)
+    unsigned lo = 0, hi = 0;
+#pragma unroll 1
+    for (int w = 0; w < NT / 32; ++w) hi = max(hi, sm_most[w]);
+    ++hi;  // (a value's order is below 2^32 - 1)
+    int reach = NT;                           // threads that reach lo
+#pragma unroll 1
+    while (hi - lo > 1 && reach > k + 8) {
+      const unsigned mid = lo + ((hi - lo) >> 1);
+      const int n = __syncthreads_count(mine >= mid);
+      if (n >= k)
+        lo = mid, reach = n;
+      else
+        hi = mid;
     }
-    __syncthreads();
-    unsigned long long bound = sm_bound;
-    const bool may = mine != 0 && mine >= bound;
-    if (__syncthreads_count(may) > k) {
+    unsigned long long bound = (unsigned long long)lo << 32;
+    unsigned long long best_key = (unsigned long long)mine << 32 | 0xffffffffu;  // (no less than the thread's best)
+    if (hi - lo == 1 && lo && reach > k + 8) {
       // equal maxima: by the first index that holds it
-      if (may) {
+      unsigned inv = 0;  // ~index: larger for lower ones
+      if (mine == lo) {
         int at = INT_MAX;
-        if (first == edge && edge >= 0) {
+        if (first == edge) {
           float y[V];
           row.get(edge, y);
 #pragma unroll
           for (int i = V - 1; i >= 0; --i) {
             const int v = edge * V - row.lead + i;
-            if (v >= 0 && v < a.V && ordered(y[i]) == (unsigned)(mine >> 32)) at = v;
+            if (v >= 0 && v < a.V && ordered(y[i]) == mine) at = v;
           }
         } else {
 #pragma unroll 1
@@ -322,22 +414,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
             row.get(s, y);
 #pragma unroll
             for (int i = V - 1; i >= 0; --i)
-              if (ordered(y[i]) == (unsigned)(mine >> 32)) at = min(at, s * V - row.lead + i);
+              if (ordered(y[i]) == mine) at = min(at, s * V - row.lead + i);
           }
         }
-        mine |= 0xffffffffu - (unsigned)at;
+        inv = 0xffffffffu - (unsigned)at;
+        best_key = (unsigned long long)mine << 32 | inv;
       }
-      sm_key[tid] = mine;
-      __syncthreads();
-      int above = 0;
-#pragma unroll 4
-      for (int i = 0; i < NT; ++i) above += sm_key[i] > mine;
-      if (above == k - 1) sm_bound = mine;
-      __syncthreads();
-      bound = sm_bound;
+      const int above = __syncthreads_count(mine > lo);
+      unsigned l = 0, h = 0xffffffffu;
+#pragma unroll 1
+      while (h - l > 1) {
+        const unsigned mid = l + ((h - l) >> 1);
+        if (above + __syncthreads_count(mine == lo && inv >= mid) >= k)
+          l = mid;
+        else
+          h = mid;
+      }
+      bound |= l;
     }
     // the threads that hold candidates, and their elements
-    if (mine != 0 && mine >= bound) sm_who[atomicAdd(&sm_w, 1)] = tid;
+    if (mine && best_key >= bound) sm_who[atomicAdd(&sm_w, 1)] = tid;
     __syncthreads();
     auto put = [&](int s) {
       float y[V];
@@ -405,10 +501,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
   }
   if (a.parts > 1) {  // the cluster's
     cg::cluster_group cluster = cg::this_cluster();
-    if (tid == 0) sm_part = st;
     cluster.sync();
     if (part == 0) {
-      for (int p = 1; p < a.parts; ++p) st = join(st, *cluster.map_shared_rank(&sm_part, p), a.c1);
+      if (warp == 0) st = join_lanes<kMaxParts / 2>(lane < a.parts ? *cluster.map_shared_rank(&sm_part, lane) : Stat{-INFINITY, 0.f, 0.f}, a.c1);
       if constexpr (TOP) {
         const int n = a.parts * a.k;  // (at most kMaxParts * kMaxTop)
         for (int i = tid; i < n; i += NT) sm_cand[i] = cluster.map_shared_rank(&sm_best[0], i / a.k)[i % a.k];
@@ -424,16 +519,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
     }
     cluster.sync();  // (the others' shared memory has been read)
     if (part) return;
+    if (tid == 0) sm_part = st;
   }
+  __syncthreads();
+  st = sm_part;
   // the row's results
-  const float z = st.m * a.scale;  // (exp of the maximum is 1: S is at least that)
+  const float z = st.m * a.scale;  // (S is at least 1)
   const float ln_s = st.m == -INFINITY ? 0.f : logf(st.s);
   const float lse = st.s != st.s ? st.s : st.m == -INFINITY ? -INFINITY : z + ln_s;
   if (tid == 0) {
     a.lse[r] = lse;
-    if (a.H) a.H[r] = st.m == -INFINITY && st.s == st.s ? 0.f : ln_s - a.scale * st.t / st.s;
+    if (a.H) a.H[r] = st.m == -INFINITY && st.s == st.s ? 0.f : ln_s - 0.69314718055994531f * (st.t / st.s);
   }
-  // (from the maximum, not from LSE: large logits then lose nothing)
+  // (from m, not from LSE: large logits then lose nothing)
   auto log_p = [&](float x) { return lse == -INFINITY ? -INFINITY : (x - st.m) * a.scale - ln_s; };
   if constexpr (TOP) {
     const unsigned long long* best = a.parts > 1 ? sm_key : sm_best;
@@ -757,7 +855,7 @@ extern "C" pt_status pt_token_logprobs_bwd(const float* dlogp, const float* dent
   constexpr int NT = 256;
   // about two rounds of loads a CTA where rows are few
   int parts = 1;
-  while (parts < 64 && slots / (parts * 2) >= NT * 4 && (long long)R * parts < 8ll * num_sms(dev)) parts *= 2;
+  while (parts < 64 && slots / (parts * 2) >= NT * 4 && (long long)R * parts < 16ll * num_sms(dev)) parts *= 2;
   while (parts > 1 && (long long)R * parts > INT_MAX) parts /= 2;
   a.parts = parts;
   cudaError_t e;

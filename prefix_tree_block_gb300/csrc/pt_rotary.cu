@@ -26,7 +26,7 @@ struct RotArgs {
   const float* inv_freq;         // [half]
   int cut[3];                    // the first pairs of axes 1, 2 and 3
   int T, H, D, half;
-  int tokens;  // of a CTA
+  int tokens, lanes;  // tokens of a CTA; threads that share a token's heads
   int inverse, copy;  // negative angles; whether the columns behind the rotated ones have to be copied
 };
 
@@ -96,92 +96,83 @@ struct alignas(sizeof(E) * V) RotVec {
 // rounding.  A CTA takes some tokens, all their heads; its angles are computed
 // once, while its first vectors are on their way.  V elements a vector; NEAR:
 // pairs lie side by side (V of them in two vectors one after the other), else
-// half the rotated columns apart.  A thread holds what it loaded until it
-// stores, so Y may be X.
+// half the rotated columns apart.  A thread keeps V pairs' sines and cosines and
+// turns them in every `lanes`-th head of one token, U heads in flight.  It holds
+// what it loaded until it stores, so Y may be X.
 template <class E, int V, bool NEAR, int U>
-__global__ void __launch_bounds__(256) k_rotary(const RotArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 512 : 256, V == 1 ? 2 : 3) k_rotary(const RotArgs a) {
   using Vec = RotVec<E, V>;
   extern __shared__ float sm[];
   pdl_wait();
   const int t0 = blockIdx.x * a.tokens, n = min(a.tokens, a.T - t0);
   float *cs = sm, *sn = sm + a.tokens * a.half;
-  const int per = a.half / V;  // items of a head: two vectors each
-  const int items = n * a.H * per;
-  Vec p[U], q[U];
-  auto locate = [&](int x, int& t, int& i, long long& col) {
-    const int th = x / per;
-    i = (x - th * per) * V;  // the first pair
-    t = th / a.H;
-    col = (long long)(th - t * a.H) * a.D + (NEAR ? 2 * i : i);
-  };
+  const int per = a.half / V;  // groups of V pairs
+  const int x = threadIdx.x / per, i = (threadIdx.x - x * per) * V, t = x / a.lanes, h0 = x - t * a.lanes;
   const long long apart = NEAR ? V : a.half;
-  auto load = [&](int x0) {
+  const E* src = reinterpret_cast<const E*>(a.X + (t0 + t) * a.x_stride) + (NEAR ? 2 * i : i);
+  E* dst = reinterpret_cast<E*>(a.Y + (t0 + t) * a.y_stride) + (NEAR ? 2 * i : i);
+  const int H = t < n ? a.H : 0;  // (no heads for threads behind the last token)
+  Vec p[U], q[U];
+  auto load = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int x = x0 + u * 256;
-      if (x < items) {
-        int t, i;
-        long long col;
-        locate(x, t, i, col);
-        const E* src = reinterpret_cast<const E*>(a.X + (t0 + t) * a.x_stride) + col;
-        p[u] = *reinterpret_cast<const Vec*>(src);
-        q[u] = *reinterpret_cast<const Vec*>(src + apart);
+    for (int u = 0; u < U; ++u)
+      if (h + u * a.lanes < H) {
+        p[u] = *reinterpret_cast<const Vec*>(src + (h + u * a.lanes) * a.D);
+        q[u] = *reinterpret_cast<const Vec*>(src + (h + u * a.lanes) * a.D + apart);
       }
-    }
   };
-  load(threadIdx.x);
+  load(h0);
   angles(a, t0, n, cs, sn);
   __syncthreads();
+  if (t < n) {
+    float c[V], s[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) c[k] = cs[t * a.half + i + k], s[k] = sn[t * a.half + i + k];
 #pragma unroll 1
-  for (int x0 = threadIdx.x; x0 < items; x0 += 256 * U) {
-    if (x0 != (int)threadIdx.x) load(x0);
+    for (int h = h0; h < H; h += U * a.lanes) {
+      if (h != h0) load(h);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int x = x0 + u * 256;
-      if (x < items) {
-        int t, i;
-        long long col;
-        locate(x, t, i, col);
-        const float *c = cs + t * a.half + i, *s = sn + t * a.half + i;
-        Vec y, z;
+      for (int u = 0; u < U; ++u)
+        if (h + u * a.lanes < H) {
+          Vec y, z;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          if constexpr (NEAR && V > 1) {  // pair k: elements 2k and 2k + 1 of the two vectors
-            const Vec& w = 2 * k < V ? p[u] : q[u];
-            Vec& o = 2 * k < V ? y : z;
-            const float f = up(w.e[2 * k % V]), g = up(w.e[2 * k % V + 1]);
-            o.e[2 * k % V] = down<E>(f * c[k] - g * s[k]);
-            o.e[2 * k % V + 1] = down<E>(g * c[k] + f * s[k]);
-          } else {
-            const float f = up(p[u].e[k]), g = up(q[u].e[k]);
-            y.e[k] = down<E>(f * c[k] - g * s[k]);
-            z.e[k] = down<E>(g * c[k] + f * s[k]);
+          for (int k = 0; k < V; ++k) {
+            if constexpr (NEAR && V > 1) {  // pair k: elements 2k and 2k + 1 of the two vectors
+              const Vec& w = 2 * k < V ? p[u] : q[u];
+              Vec& o = 2 * k < V ? y : z;
+              const float f = up(w.e[2 * k % V]), g = up(w.e[2 * k % V + 1]);
+              o.e[2 * k % V] = down<E>(f * c[k] - g * s[k]);
+              o.e[2 * k % V + 1] = down<E>(g * c[k] + f * s[k]);
+            } else {
+              const float f = up(p[u].e[k]), g = up(q[u].e[k]);
+              y.e[k] = down<E>(f * c[k] - g * s[k]);
+              z.e[k] = down<E>(g * c[k] + f * s[k]);
+            }
           }
+          E* to = dst + (h + u * a.lanes) * a.D;
+          *reinterpret_cast<Vec*>(to) = y;
+          *reinterpret_cast<Vec*>(to + apart) = z;
         }
-        E* dst = reinterpret_cast<E*>(a.Y + (t0 + t) * a.y_stride) + col;
-        *reinterpret_cast<Vec*>(dst) = y;
-        *reinterpret_cast<Vec*>(dst + apart) = z;
-      }
     }
   }
   if (a.copy) {  // columns behind the rotated ones
     const int rest = a.D / V - 2 * per, all = n * a.H * rest;
 #pragma unroll 1
-    for (int x = threadIdx.x; x < all; x += 256) {
-      const int th = x / rest, t = th / a.H;
-      const long long col = (long long)(th - t * a.H) * a.D + 2 * a.half + (x - th * rest) * V;
-      *reinterpret_cast<Vec*>(reinterpret_cast<E*>(a.Y + (t0 + t) * a.y_stride) + col) =
-          *reinterpret_cast<const Vec*>(reinterpret_cast<const E*>(a.X + (t0 + t) * a.x_stride) + col);
+    for (int y = threadIdx.x; y < all; y += blockDim.x) {
+      const int th = y / rest, tt = th / a.H;
+      const long long col = (long long)(th - tt * a.H) * a.D + 2 * a.half + (y - th * rest) * V;
+      *reinterpret_cast<Vec*>(reinterpret_cast<E*>(a.Y + (t0 + tt) * a.y_stride) + col) =
+          *reinterpret_cast<const Vec*>(reinterpret_cast<const E*>(a.X + (t0 + tt) * a.x_stride) + col);
     }
   }
 }
 
 template <class E, bool NEAR>
-cudaError_t launch(const RotArgs& a, int unit, dim3 grid, size_t smem, cudaStream_t s) {
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), smem, s, a); };
-  if (unit == 16) return go(k_rotary<E, 16 / (int)sizeof(E), NEAR, 4>);
-  if (unit == 8) return go(k_rotary<E, 8 / (int)sizeof(E), NEAR, 4>);
-  return go(k_rotary<E, 1, NEAR, 4>);
+cudaError_t launch(const RotArgs& a, int unit, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads), smem, s, a); };
+  if (unit == 16) return go(k_rotary<E, 16 / (int)sizeof(E), NEAR, 2>);
+  if (unit == 8) return go(k_rotary<E, 8 / (int)sizeof(E), NEAR, 2>);
+  return go(k_rotary<E, 1, NEAR, 2>);
 }
 
 }  // namespace
@@ -275,22 +266,23 @@ extern "C" pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, 
   a.T = T, a.H = H, a.D = D, a.half = half;
   a.inverse = inverse != 0;
   a.copy = !same && rot_dim < D;
-  // Tokens of a CTA: a few rounds of loads, at most 16 KB of angles, and few tokens a CTA where there are few.
+  // Eight heads a thread and about 256 threads a CTA; fewer heads where that leaves SMs idle.
   const int per = half / (unit / es), sms = num_sms(dev);
-  long long tokens = std::max(1, 1024 / std::max(1, H * per));
-  tokens = std::min<long long>(tokens, std::max(1, 2048 / half));
-  tokens = std::min<long long>(tokens, std::max(1, T / (4 * sms)));
-  a.tokens = (int)tokens;
-  const dim3 grid((unsigned)((T + tokens - 1) / tokens));
-  const size_t smem = (size_t)tokens * half * 8;
+  int each = 8;
+  while (each > 1 && (long long)T * ((H + each - 1) / each) * per < 512ll * sms) each /= 2;
+  a.lanes = std::max(1, std::min((H + each - 1) / each, 256 / per));
+  a.tokens = std::max(1, 256 / (per * a.lanes));
+  const int threads = per * a.lanes * a.tokens;
+  const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
+  const size_t smem = (size_t)a.tokens * half * 8;
   cudaError_t e;
   {
     ProfScope ps(stream, "rotary");
     if (dtype == PT_BF16)
-      e = interleaved ? launch<__nv_bfloat16, true>(a, unit, grid, smem, stream)
-                      : launch<__nv_bfloat16, false>(a, unit, grid, smem, stream);
+      e = interleaved ? launch<__nv_bfloat16, true>(a, unit, grid, threads, smem, stream)
+                      : launch<__nv_bfloat16, false>(a, unit, grid, threads, smem, stream);
     else
-      e = interleaved ? launch<float, true>(a, unit, grid, smem, stream) : launch<float, false>(a, unit, grid, smem, stream);
+      e = interleaved ? launch<float, true>(a, unit, grid, threads, smem, stream) : launch<float, false>(a, unit, grid, threads, smem, stream);
     count_launch();
   }
   if (e == cudaSuccess) e = cudaGetLastError();
