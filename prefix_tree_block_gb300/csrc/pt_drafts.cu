@@ -46,6 +46,68 @@ struct TreeArgs {
   long long* positions;
 };
 
+// Up to 64 drafts: a warp per sample and a lane for two drafts, all in registers.
+__global__ void __launch_bounds__(128) k_draft_tree64(const TreeArgs a) {
+  pdl_wait();
+  const int s = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (s >= a.S) return;
+  int c = a.q_count ? a.q_count[s] : a.q;
+  const long long row0 = (long long)s * a.q;
+  int up[2];
+  unsigned m[2][2];  // [draft lane, draft lane + 32][word]
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    up[i] = j < a.q ? a.parents[row0 + j] : -1;
+  }
+  long long first = 0;
+  if (a.positions) {
+    const int leaf = leaf_of(a.path_ptr, a.path_ent, s);
+    first = (long long)a.lens[leaf] + (a.start ? a.start[leaf] : 0);
+  }
+  bool bad = c < 0 || c > a.q;
+  c = min(max(c, 0), a.q);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    bad |= j < c && (up[i] < -1 || up[i] >= j);
+    if (j >= c || up[i] < 0 || up[i] >= j) up[i] = -1;
+    m[i][0] = i == 0 ? 1u << lane : 0u;
+    m[i][1] = i == 1 ? 1u << lane : 0u;
+  }
+  if (bad) record_status(PT_STATUS_INVALID);
+#pragma unroll 1
+  for (int span = 1; span < a.q; span <<= 1) {
+    unsigned n[2][2];
+    int nu[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // (draft up[i] is lane up[i] & 31's, its first or second)
+      const int from = up[i] & 31;
+      const bool hi = up[i] >= 32;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const unsigned x = __shfl_sync(0xffffffffu, m[0][w], from), y = __shfl_sync(0xffffffffu, m[1][w], from);
+        n[i][w] = m[i][w] | (up[i] < 0 ? 0u : hi ? y : x);
+      }
+      const int x = __shfl_sync(0xffffffffu, up[0], from), y = __shfl_sync(0xffffffffu, up[1], from);
+      nu[i] = up[i] < 0 ? -1 : hi ? y : x;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i][0] = n[i][0], m[i][1] = n[i][1], up[i] = nu[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = lane + 32 * i;
+    if (j >= a.q) continue;
+    const bool real = j < c;
+    if (a.w == 1)
+      a.mask[row0 + j] = real ? (int)m[i][0] : 0;
+    else
+      reinterpret_cast<int2*>(a.mask)[row0 + j] = real ? make_int2((int)m[i][0], (int)m[i][1]) : make_int2(0, 0);
+    if (a.positions) a.positions[row0 + j] = real ? first - c + __popc(m[i][0]) + __popc(m[i][1]) - 1 : 0;
+  }
+}
+
 __global__ void __launch_bounds__(128) k_draft_tree(const TreeArgs a) {
   extern __shared__ int sm[];
   pdl_wait();
@@ -241,10 +303,12 @@ extern "C" pt_status pt_draft_tree(const int32_t* parents, const int32_t* lens, 
   a.mask = mask;
   a.positions = reinterpret_cast<long long*>(positions);
   const size_t smem = 4 * ((size_t)a.per * a.q * (2 + 2 * a.w) + a.per);
+  const bool warps = a.q <= 64 && (reinterpret_cast<uintptr_t>(mask) & 7) == 0;
   cudaError_t e;
   {
     ProfScope ps(stream, "draft_tree");
-    e = launch_pdl(k_draft_tree, dim3((unsigned)((a.S + a.per - 1) / a.per)), dim3(128), smem, stream, a);
+    e = warps ? launch_pdl(k_draft_tree64, dim3((unsigned)((a.S + 3) / 4)), dim3(128), 0, stream, a)
+              : launch_pdl(k_draft_tree, dim3((unsigned)((a.S + a.per - 1) / a.per)), dim3(128), smem, stream, a);
     count_launch();
   }
   return (pt_status)launch_status(who, e);

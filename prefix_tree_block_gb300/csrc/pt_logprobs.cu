@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -33,6 +34,7 @@ namespace {
 constexpr int kMaxTop = 64;
 constexpr int kMaxParts = 8;   // CTAs of a row: a cluster
 constexpr int kCandidates = 1024;
+constexpr int kGroups = 16;      // of a thread's slots
 
 // Entries of the rows: row r has entries [row_ptr[r], row_ptr[r + 1]), or entry
 // r; entry n is token index[n], or n.
@@ -203,7 +205,7 @@ __device__ __noinline__ float2 far_terms(uint4 v, float m, float c1) {
 struct ScoreArgs {
   const void* x;
   long long stride;  // elements between rows
-  int V, parts, k;
+  int V, lparts, k;  // 2^lparts CTAs a row
   float scale, c1;
   Entries e;
   float* logp;
@@ -217,42 +219,160 @@ struct ScoreArgs {
 // Scores: one pass over the logits.  A row is one CTA's, or a cluster's that
 // shares it where rows are few; a thread takes every NT-th 16 bytes, U of them
 // in flight, and keeps its own running maximum and sums, which are joined at
-// the end (through shared memory, then the cluster's).
+// the end (through shared memory, then the cluster's).  A CTA takes rows one
+// after the other, the next one's first loads issued before the joining.
+//   RING: long rows, and many of them.  One warp brings the rows by bulk copies
+//     into a ring of stages, running ahead across the rows' ends, so that no
+//     thread waits for memory and the joining costs no time in which nothing is
+//     loaded; one warp looks up the row's tokens (row_ptr, index, target, logit:
+//     a chain of latencies); eight compute.  Three such CTAs on an SM.
+//   CLERK alone: few long rows, shared by clusters; loads into registers.
+//   NT = 32, 128: short rows, whose latencies many rows at once hide.
 //
-// The alternatives take one more look at very little: the k-th largest of the
-// threads' maxima bounds the k-th largest element from below, so only the
-// threads whose maximum is at least that have candidates, k of them unless
-// values are equal; their elements are read again (from L2), those at or above
-// the bound listed, and the list ranked.  Equal maxima are told apart by their
-// first index before, so that a row of equal logits lists few of them.  A list
-// that overflows all the same (many large elements in few threads) is replaced
-// by k searches through the part.
+// The alternatives take one more look at very little.  If every warp has q threads
+// whose maxima reach a bound, and all warps together at least k, the bound is no
+// higher than the k-th largest element; so it is the least of the warps' q-th
+// largest maxima.  A thread also keeps the maxima of groups of U slots (16 bits of
+// their order, 16 groups): only the groups that reach the bound are read again
+// (from L2), their elements at or above it listed, and the list ranked.  Where
+// many more threads reach the bound it is raised by halving, and equal maxima are
+// told apart by their first index, so that a row of equal logits lists few of
+// them.  A list that overflows all the same (many large elements in few threads)
+// is replaced by k searches through the part.
 // ---------------------------------------------------------------------------
-template <class E, int NT, bool TOP>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
-  constexpr int V = Type<E>::V, U = 4;
+constexpr int kStages = 3;  // (four: the same; two: 2% more without alternatives)
+// Shared memory of the ring: stages of four slots a thread.
+constexpr int ring_bytes(int nt) { return kStages * nt * 4 * 16; }
+
+template <int N>
+__device__ __forceinline__ int bar_count(bool p) {  // how many of the N threads of barrier 1 say yes
+  int r;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, 1, %2, q;\n\t}"
+               : "=r"(r)
+               : "r"((unsigned)p), "n"(N)
+               : "memory");
+  return r;
+}
+
+template <class E, int NT, bool TOP, bool CLERK, bool RING>
+__global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (NT + 32 * CLERK)) k_score(const ScoreArgs a) {
+  constexpr int V = Type<E>::V, U = 4, ALL = NT + 32 * CLERK;  // ALL: without the warp that loads
   __shared__ Stat sm_stat[NT / 32];
   __shared__ Stat sm_part;
-  __shared__ unsigned sm_most[NT / 32];
-  __shared__ unsigned long long sm_key[TOP ? NT : 1], sm_cand[TOP ? kCandidates : 1], sm_best[TOP ? kMaxTop : 1];
-  __shared__ int sm_who[TOP ? NT : 1];
-  __shared__ int sm_n, sm_w;
-  pdl_wait();
+  __shared__ unsigned sm_most[NT / 32], sm_least[NT / 32];
+  __shared__ unsigned long long sm_key[TOP ? kMaxTop : 1], sm_cand[TOP ? kCandidates : 1], sm_best[TOP ? kMaxTop : 1];
+  __shared__ int sm_who[TOP ? kCandidates : 1];  // groups: thread, and 2^16 times the group
+  __shared__ unsigned short sm_group[TOP ? kGroups : 1][TOP ? NT : 1];
+  __shared__ int sm_n, sm_w, sm_e0, sm_e1;
+  __shared__ uint64_t sm_full[RING ? kStages : 1], sm_empty[RING ? kStages : 1];
+  __shared__ volatile int abort_flag;
+  extern __shared__ __align__(128) uint8_t sm_ring[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part = blockIdx.x % a.parts, r = blockIdx.x / a.parts;
-  const Row<E> row(static_cast<const E*>(a.x) + (long long)r * a.stride, a.V);
-  const int slots = row.slots();
-  const int s0 = (int)((long long)slots * part / a.parts), s1 = (int)((long long)slots * (part + 1) / a.parts);
+  const bool reads = tid < NT;
+  const auto sync = [&]() {
+    if constexpr (RING)
+      named_bar_sync(1, ALL);
+    else
+      __syncthreads();
+  };
+  const auto count = [&](bool p) {
+    if constexpr (RING)
+      return bar_count<ALL>(p);
+    else
+      return __syncthreads_count(p);
+  };
+  if constexpr (RING) {
+    if (tid == 0) {
+      for (int i = 0; i < kStages; ++i) mbar_init(sm_full + i, 1), mbar_init(sm_empty + i, NT / 32);
+      abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  pdl_wait();
+  const int part = blockIdx.x & ((1 << a.lparts) - 1), step = gridDim.x >> a.lparts;
+  // a row: its slots that are this part's, and of those the whole ones
+  struct Span {
+    int slots, s0, s1, w0, w1;
+  };
+  auto row_of = [&](int r) { return Row<E>(static_cast<const E*>(a.x) + (long long)r * a.stride, a.V); };
+  auto span_of = [&](const Row<E>& row) {
+    Span p;
+    p.slots = row.slots();
+    p.s0 = (int)((unsigned)p.slots * part >> a.lparts), p.s1 = (int)((unsigned)p.slots * (part + 1) >> a.lparts);  // (up to 2^28 slots)
+    p.w0 = max(p.s0, row.whole(0) ? 0 : 1), p.w1 = min(p.s1, row.whole(p.slots - 1) ? p.slots : p.slots - 1);
+    return p;
+  };
+  if constexpr (RING) {
+    if (warp == ALL / 32) {
+      if (lane == 0) {
+        uint32_t n = 0;  // stages filled
+        bool ok = true;
+#pragma unroll 1
+        for (int r = blockIdx.x; ok && r < a.e.R; r += step) {
+          const Row<E> row = row_of(r);
+          const Span p = span_of(row);
+#pragma unroll 1
+          for (int s = p.w0; s < p.w1; s += NT * U, ++n) {
+            const uint32_t st = n % kStages;
+            if (n >= kStages) ok = mbar_wait(sm_empty + st, (n / kStages - 1) & 1, &abort_flag);
+            if (!ok) break;
+            const uint32_t bytes = min(p.w1 - s, NT * U) * 16;
+            mbar_expect_tx(sm_full + st, bytes);
+            bulk_load(sm_ring + st * (NT * U * 16), row.x + ((long long)s * V - row.lead), bytes, sm_full + st);
+          }
+        }
+        if (!ok)  // a wait ran out: let the copies in flight land
+          for (uint32_t i = 0; i < kStages && i < n; ++i)
+            mbar_wait_drain(sm_full + (n - 1 - i) % kStages, ((n - 1 - i) / kStages) & 1, 20000000);
+      }
+      return;
+    }
+  }
+  uint32_t used = 0;  // RING: stages read
+  uint4 v[U];
+  auto fetch = [&](const Row<E>& row, int s, int w1) {
+    if constexpr (RING) {
+      // (a wait that runs out is recorded; the barriers are kept, so that the CTA ends)
+      const uint32_t st = used % kStages;
+      mbar_wait(sm_full + st, (used / kStages) & 1, &abort_flag);
+      const uint4* from = reinterpret_cast<const uint4*>(sm_ring + st * (NT * U * 16)) + tid;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s + u * NT < w1) v[u] = from[u * NT];
+      ++used;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm_empty + st);
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (reads && s + u * NT < w1) v[u] = row.load(s + u * NT);
+  };
+  int r = blockIdx.x >> a.lparts;
+  if constexpr (!RING) {
+    const Row<E> row = row_of(r);
+    const Span p = span_of(row);
+    fetch(row, p.w0 + tid, p.w1);
+  }
+#pragma unroll 1
+  for (; r < a.e.R; r += step) {
+  const Row<E> row = row_of(r);
+  const Span span = span_of(row);
+  const int slots = span.slots, s0 = span.s0, s1 = span.s1, w0 = span.w0, w1 = span.w1;
   // the first entries' logits, while the row is read
-  int e0 = 0, e1 = 0, my_tok = -1, my_target = -1;
+  int my_tok = -1, my_target = -1;
   float my_x = 0.f;
-  if (part == 0) {
+  const int me = CLERK ? tid - NT : tid;  // the entry (of the first 32, or as many as threads) that is this thread's
+  if (part == 0 && (!CLERK || me >= 0)) {
+    int e0, e1;
     a.e.range(r, e0, e1);
-    if (tid < e1 - e0) {
-      my_tok = a.e.token(e0 + tid);
+    if (me < e1 - e0) {
+      my_tok = a.e.token(e0 + me);
       my_target = a.e.target(my_tok, a.V);
       if (my_target >= 0) my_x = Type<E>::f(row.x[my_target]);
     }
+    if (me == 0) sm_e0 = e0, sm_e1 = e1;
   }
   // A term's exponent is one fused product and difference, x c1 - ref with ref the
   // rounded m c1; what the rounding took is made up for at the end.
@@ -266,7 +386,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
   // and by several steps of bf16, that no term with a weight is touched.
   float low = -1e4f / a.c1;
   uint32_t low2 = pack_bf16(low, low);
-  auto take = [&](const uint4* v, auto count, int at) {  // so many slots from `at` on
+  auto take = [&](const uint4* v, auto count, int at) {  // so many slots from `at` on; their largest
     constexpr int n = decltype(count)::value;
     const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
     float bm;
@@ -332,23 +452,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
         st.s += d.x, st.t += d.y;
       }
     }
+    return bm;
   };
   using One = std::integral_constant<int, 1>;
   using All = std::integral_constant<int, U>;
   // whole slots, then the ones at the row's ends
-  const int w0 = max(s0, row.whole(0) ? 0 : 1), w1 = min(s1, row.whole(slots - 1) ? slots : slots - 1);
+  int chunks = 0;  // rounds of U slots
 #pragma unroll 1
-  for (int s = w0 + tid; s < w1; s += NT * U) {
-    uint4 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u * NT < w1) v[u] = row.load(s + u * NT);
+  for (int s = w0 + tid; reads && (RING ? s - tid : s) < w1; s += NT * U, ++chunks) {  // (RING: whole warps, for the stages)
+    if (RING || s != w0 + tid) fetch(row, s, w1);
+    float largest = -INFINITY;
     if (s + (U - 1) * NT < w1) {
-      take(v, All{}, s);
+      largest = take(v, All{}, s);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (s + u * NT < w1) take(v + u, One{}, s + u * NT);
+        if (s + u * NT < w1) largest = fmaxf(largest, take(v + u, One{}, s + u * NT));
+    }
+    if constexpr (TOP) {
+      const unsigned short o = (unsigned short)(ordered(largest) >> 16);
+      unsigned short& g = sm_group[chunks & (kGroups - 1)][tid];
+      g = chunks < kGroups ? o : max(g, o);
     }
   }
   int edge = -1;  // a slot at the row's end that is this thread's
@@ -358,35 +482,48 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
     const uint4 y = row.pack(edge);
     take(&y, One{}, edge);
   }
+  if (!RING && r + step < a.e.R) {
+    const Row<E> next_row = row_of(r + step);
+    const Span p = span_of(next_row);
+    fetch(next_row, p.w0 + tid, p.w1);
+  }
   if (plain) rebase(st.s, st.t, -fmaf(st.m == -INFINITY ? 0.f : st.m, a.c1, -ref));
   // the CTA's statistics
   st = join_lanes<16>(st, a.c1);
-  if (lane == 0) sm_stat[warp] = st;
+  if (lane == 0 && reads) sm_stat[warp] = st;
   unsigned mine = 0;  // TOP: this thread's largest logit
   if constexpr (TOP) {
     mine = first >= 0 ? ordered(own_max) : 0u;
-    const unsigned most = __reduce_max_sync(0xffffffffu, mine);
-    if (lane == 0) sm_most[warp] = most;
+    // the warp's largest maximum and its q-th largest
+    unsigned rest = mine, most = 0, least = 0;
+    const int q = (a.k + NT / 32 - 1) / (NT / 32);
+#pragma unroll 1
+    for (int i = 0; i < q; ++i) {
+      least = __reduce_max_sync(0xffffffffu, rest);
+      if (i == 0) most = least;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, rest == least)) - 1) rest = 0;
+    }
+    if (lane == 0 && reads) sm_most[warp] = most, sm_least[warp] = least;
     if (tid == 0) sm_n = sm_w = 0;
+    for (int i = tid; i < a.k; i += ALL) sm_best[i] = 0;
   }
-  __syncthreads();
+  sync();
   if (warp == 0) {
-    st = join_lanes<NT / 64>(lane < NT / 32 ? sm_stat[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c1);
+    if constexpr (NT > 32) st = join_lanes<NT <= 128 ? 2 : 8>(lane < NT / 32 ? sm_stat[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c1);
     if (lane == 0) sm_part = st;
   }
   if constexpr (TOP) {
-    // The bound: at least k threads' maxima reach it, by halving; not many more
-    // unless they are equal.
     const int k = a.k;
-    unsigned lo = 0, hi = 0;
-#pragma unroll 1
-    for (int w = 0; w < NT / 32; ++w) hi = max(hi, sm_most[w]);
+    unsigned lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) lo = min(lo, sm_least[w]), hi = max(hi, sm_most[w]);
     ++hi;  // (a value's order is below 2^32 - 1)
-    int reach = NT;                           // threads that reach lo
+    int reach = count(mine >= lo);  // threads that reach lo: k at least (with lo = 0 all)
+    const bool far = reach > 2 * k + 32 || lo == 0;  // (0: a warp without q threads that hold any)
 #pragma unroll 1
-    while (hi - lo > 1 && reach > k + 8) {
+    while (far && hi - lo > 1 && reach > k + 8) {
       const unsigned mid = lo + ((hi - lo) >> 1);
-      const int n = __syncthreads_count(mine >= mid);
+      const int n = count(mine >= mid);
       if (n >= k)
         lo = mid, reach = n;
       else
@@ -394,7 +531,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
     }
     unsigned long long bound = (unsigned long long)lo << 32;
     unsigned long long best_key = (unsigned long long)mine << 32 | 0xffffffffu;  // (no less than the thread's best)
-    if (hi - lo == 1 && lo && reach > k + 8) {
+    if (far && hi - lo == 1 && lo && reach > k + 8) {
       // equal maxima: by the first index that holds it
       unsigned inv = 0;  // ~index: larger for lower ones
       if (mine == lo) {
@@ -420,26 +557,40 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
         inv = 0xffffffffu - (unsigned)at;
         best_key = (unsigned long long)mine << 32 | inv;
       }
-      const int above = __syncthreads_count(mine > lo);
+      const int above = count(mine > lo);
       unsigned l = 0, h = 0xffffffffu;
 #pragma unroll 1
       while (h - l > 1) {
         const unsigned mid = l + ((h - l) >> 1);
-        if (above + __syncthreads_count(mine == lo && inv >= mid) >= k)
+        if (above + count(mine == lo && inv >= mid) >= k)
           l = mid;
         else
           h = mid;
       }
       bound |= l;
     }
-    // the threads that hold candidates, and their elements
-    if (mine && best_key >= bound) sm_who[atomicAdd(&sm_w, 1)] = tid;
-    __syncthreads();
-    auto put = [&](int s) {
+    // the groups that hold candidates, and their elements
+    if (reads && mine && best_key >= bound) {
+      const unsigned reach16 = (unsigned)(bound >> 48);
+#pragma unroll 1
+      for (int c = 0; c < min(chunks, kGroups); ++c)
+        if (sm_group[c][tid] >= reach16) {
+          const int at = atomicAdd(&sm_w, 1);
+          if (at < kCandidates) sm_who[at] = tid | c << 16;
+        }
+    }
+    sync();
+    const float least = value_of(bound);
+    auto put = [&](int s, const uint4& w) {
       float y[V];
-      row.get(s, y);
+      unpack(w, y);
+      float top = y[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = fmaxf(top, y[i]);
+      if (top < least) return;  // most slots (a NaN passes on)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        if (y[i] < least) continue;
         const int v = s * V - row.lead + i;
         const unsigned long long key = key_of(y[i], v);
         if (key >= bound && v >= 0 && v < a.V) {
@@ -448,20 +599,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
         }
       }
     };
-    const int each = w1 > w0 ? (w1 - w0 + NT - 1) / NT : 0, who = sm_w;
+    // (a group: U slots of every kGroups-th round)
+    const int rounds = (w1 - w0 + NT * U - 1) / (NT * U), reps = (rounds + kGroups - 1) / kGroups, listed = sm_w;
+    const int all = min(listed, kCandidates) * U * reps;
 #pragma unroll 1
-    for (int x = tid; x < who * each; x += NT) {
-      const int s = w0 + sm_who[x / each] + (x % each) * NT;
-      if (s < w1) put(s);
+    for (int x = tid; x < all; x += ALL) {
+      const int y = x / U, i = reps == 1 ? y : y / reps, g = sm_who[i];
+      const int s = w0 + (g & 0xffff) + ((g >> 16) + (y - i * reps) * kGroups) * (NT * U) + (x % U) * NT;
+      if (s < w1) put(s, row.load(s));
     }
-    if (edge >= 0) put(edge);
-    __syncthreads();
+    if (edge >= 0) put(edge, row.pack(edge));
+    sync();
     const int n = sm_n;
-    if (n <= kCandidates) {
-      for (int i = tid; i < k; i += NT) sm_best[i] = 0;
-      __syncthreads();
+    if (n <= kCandidates && listed <= kCandidates) {
 #pragma unroll 1
-      for (int i = tid; i < n; i += NT) {
+      for (int i = tid; i < n; i += ALL) {
         const unsigned long long key = sm_cand[i];
         int above = 0;
 #pragma unroll 4
@@ -474,7 +626,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
       for (int i = 0; i < k; ++i) {
         unsigned long long best = 0;
 #pragma unroll 1
-        for (int s = s0 + tid; s < s1; s += NT) {
+        for (int s = s0 + tid; s < s1; s += ALL) {
           float y[V];
           row.get(s, y);
 #pragma unroll
@@ -484,31 +636,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
             if (v >= 0 && v < a.V && key < below && key > best) best = key;
           }
         }
-        __syncthreads();
-        sm_key[tid] = best;
-        __syncthreads();
-        for (int o = NT / 2; o; o >>= 1) {
-          if (tid < o) sm_key[tid] = max(sm_key[tid], sm_key[tid + o]);
-          __syncthreads();
-        }
-        below = sm_key[0];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        sync();
+        if (lane == 0) sm_cand[warp] = best;
+        sync();
+        below = 0;
+        for (int w = 0; w < ALL / 32; ++w) below = max(below, sm_cand[w]);
         if (tid == 0) sm_best[i] = below;
-        __syncthreads();
         if (below == 0) below = 1;  // (no more of them)
       }
     }
-    __syncthreads();
+    sync();
   }
-  if (a.parts > 1) {  // the cluster's
+  if (a.lparts > 0) {  // the cluster's
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     if (part == 0) {
-      if (warp == 0) st = join_lanes<kMaxParts / 2>(lane < a.parts ? *cluster.map_shared_rank(&sm_part, lane) : Stat{-INFINITY, 0.f, 0.f}, a.c1);
+      if (warp == 0) st = join_lanes<kMaxParts / 2>(lane < 1 << a.lparts ? *cluster.map_shared_rank(&sm_part, lane) : Stat{-INFINITY, 0.f, 0.f}, a.c1);
       if constexpr (TOP) {
-        const int n = a.parts * a.k;  // (at most kMaxParts * kMaxTop)
-        for (int i = tid; i < n; i += NT) sm_cand[i] = cluster.map_shared_rank(&sm_best[0], i / a.k)[i % a.k];
-        __syncthreads();
-        for (int i = tid; i < n; i += NT) {
+        const int n = a.k << a.lparts;  // (at most kMaxParts * kMaxTop)
+        for (int i = tid; i < n; i += ALL) sm_cand[i] = cluster.map_shared_rank(&sm_best[0], i / a.k)[i % a.k];
+        sync();
+        for (int i = tid; i < n; i += ALL) {
           const unsigned long long key = sm_cand[i];
           int above = 0;
 #pragma unroll 4
@@ -521,7 +671,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
     if (part) return;
     if (tid == 0) sm_part = st;
   }
-  __syncthreads();
+  const int e0 = sm_e0, e1 = sm_e1;  // (before the barrier: behind it the next row's may come)
+  sync();
   st = sm_part;
   // the row's results
   const float z = st.m * a.scale;  // (S is at least 1)
@@ -534,8 +685,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
   // (from m, not from LSE: large logits then lose nothing)
   auto log_p = [&](float x) { return lse == -INFINITY ? -INFINITY : (x - st.m) * a.scale - ln_s; };
   if constexpr (TOP) {
-    const unsigned long long* best = a.parts > 1 ? sm_key : sm_best;
-    for (int i = tid; i < a.k; i += NT) {
+    const unsigned long long* best = a.lparts > 0 ? sm_key : sm_best;
+    for (int i = tid; i < a.k; i += ALL) {
       const unsigned long long key = best[i];
       a.top[(long long)r * a.k + i] = log_p(value_of(key));
       a.ids[(long long)r * a.k + i] = index_of(key);
@@ -544,18 +695,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score(const ScoreArgs a) {
   auto put_logp = [&](int tok, int target, float x) {
     if (tok >= 0) a.logp[tok] = target < 0 ? 0.f : log_p(x);
   };
-  if (tid < e1 - e0) put_logp(my_tok, my_target, my_x);
+  if (me >= 0) put_logp(my_tok, my_target, my_x);
 #pragma unroll 1
-  for (int n = e0 + NT + tid; n < e1; n += NT) {
+  for (int n = e0 + (CLERK ? 32 : NT) + tid; n < e1; n += ALL) {
     const int tok = a.e.token(n), target = a.e.target(tok, a.V);
     put_logp(tok, target, target >= 0 ? Type<E>::f(row.x[target]) : 0.f);
   }
   if (r == a.e.R - 1 && a.e.row_ptr) {  // entries of no row
     const int end = min(max(a.e.row_ptr[a.e.R], 0), a.e.N);
-    for (int n = end + tid; n < a.e.N; n += NT) {
+    for (int n = end + tid; n < a.e.N; n += ALL) {
       const int tok = a.e.token(n);
       if (tok >= 0) a.logp[tok] = 0.f;
     }
+  }
   }
 }
 
@@ -563,7 +715,7 @@ struct GradArgs {
   const void* x;
   void* d;
   long long stride, d_stride;
-  int V, parts;
+  int V, lparts;
   float scale;
   Entries e;
   const float* g;
@@ -590,11 +742,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const GradArgs a) {
   __shared__ float sm_g[NT / 32];
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part = blockIdx.x % a.parts, r = blockIdx.x / a.parts;
+  const int part = blockIdx.x & ((1 << a.lparts) - 1), r = blockIdx.x >> a.lparts;
   const Row<E> row(static_cast<const E*>(a.x) + (long long)r * a.stride, a.V);
   E* out = static_cast<E*>(a.d) + (long long)r * a.d_stride;
   const int slots = row.slots();
-  const int s0 = (int)((long long)slots * part / a.parts), s1 = (int)((long long)slots * (part + 1) / a.parts);
+  const int s0 = (int)((long long)slots * part >> a.lparts), s1 = (int)((long long)slots * (part + 1) >> a.lparts);
+  uint4 v[U];
+  auto fetch = [&](int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u * NT < s1 && row.whole(s + u * NT)) v[u] = *reinterpret_cast<const uint4*>(row.x + ((long long)(s + u * NT) * V - row.lead));
+  };
+  fetch(s0 + tid);
   int e0, e1;
   a.e.range(r, e0, e1);
   float lse = a.lse[r];
@@ -653,10 +812,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const GradArgs a) {
   };
 #pragma unroll 1
   for (int s = s0 + tid; s < s1; s += NT * U) {
-    uint4 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u * NT < s1 && row.whole(s + u * NT)) v[u] = *reinterpret_cast<const uint4*>(row.x + ((long long)(s + u * NT) * V - row.lead));
+    if (s != s0 + tid) fetch(s);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = s + u * NT;
@@ -698,12 +854,22 @@ int launch_status(const char* who, cudaError_t e) {
   return PT_OK;
 }
 
+// Lets a kernel use `bytes` of shared memory, once per device (a bit each).
+template <class K>
+cudaError_t opt_in_smem(K kernel, size_t bytes, int dev, std::atomic<uint64_t>& opted) {
+  if (dev < 64 && (opted.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) opted.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
 // As launch_pdl, with `parts` CTAs a cluster.
 template <class K, class A>
-cudaError_t launch_cluster(K kernel, unsigned grid, int threads, int parts, cudaStream_t s, const A& a) {
+cudaError_t launch_cluster(K kernel, unsigned grid, int threads, size_t smem, int parts, cudaStream_t s, const A& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -787,26 +953,45 @@ extern "C" pt_status pt_token_logprobs(const void* logits, int64_t row_stride, p
   a.e = Entries{reinterpret_cast<const long long*>(targets), row_ptr, index, R, N};
   a.logp = logp, a.lse = LSE, a.H = entropy, a.top = top_logp;
   a.ids = reinterpret_cast<long long*>(top_ids);
-  const int slots = (V + 16 / es - 1) / (16 / es), nt = slots >= 1024 ? 512 : 128;
-  // Few rows: a cluster each, until the SMs have three CTAs or a thread less than four loads.
+  // Rows of up to 8 KB: a warp each, or a CTA of four where the alternatives
+  // need maxima of more threads.  Longer ones: a CTA each with its ring, three on
+  // an SM, or where rows are few a cluster (two CTAs on an SM): the slots that the
+  // busiest SM reads, and about 5000 more for the latencies of each round.
+  const int slots = (V + 16 / es - 1) / (16 / es), sms = num_sms(dev);
+  const bool small = slots <= 512;
   int parts = 1;
-  while (parts < kMaxParts && (long long)R * parts * 2 <= 3ll * num_sms(dev) && slots / (parts * 2) >= nt * 4) parts *= 2;
-  a.parts = parts;
+  if (!small) {
+    long long least = LLONG_MAX;
+    for (int p = 1; p <= kMaxParts && slots / p >= 480; p *= 2) {
+      const long long all = (long long)R * p, at_once = sms * (p == 1 ? 3 : 2);
+      const long long cost = (all + sms - 1) / sms * (slots / p) + (all + at_once - 1) / at_once * 5000;
+      if (cost < least) least = cost, parts = p;
+    }
+  }
+  a.lparts = __builtin_ctz((unsigned)parts);
   cudaError_t e;
   {
     ProfScope ps(stream, "token_logprobs");
-    auto go = [&](auto kernel) { return launch_cluster(kernel, (unsigned)R * (unsigned)parts, nt, parts, stream, a); };
-    if (dtype == PT_BF16) {
-      if (top_k)
-        e = nt == 512 ? go(k_score<__nv_bfloat16, 512, true>) : go(k_score<__nv_bfloat16, 128, true>);
-      else
-        e = nt == 512 ? go(k_score<__nv_bfloat16, 512, false>) : go(k_score<__nv_bfloat16, 128, false>);
-    } else {
-      if (top_k)
-        e = nt == 512 ? go(k_score<float, 512, true>) : go(k_score<float, 128, true>);
-      else
-        e = nt == 512 ? go(k_score<float, 512, false>) : go(k_score<float, 128, false>);
-    }
+    // CTAs take rows in turn (a cluster one row)
+    auto go = [&](auto kernel, int threads, int per_sm) {
+      const long long grid = parts > 1 ? (long long)R * parts : std::min<long long>(R, (long long)sms * per_sm);
+      const size_t smem = threads == 320 ? ring_bytes(256) : 0;
+      if (smem) {
+        static std::atomic<uint64_t> opted[4];
+        const int which = (dtype == PT_BF16 ? 0 : 1) + (top_k ? 2 : 0);
+        if (cudaError_t o = opt_in_smem(kernel, smem, dev, opted[which])) return o;
+      }
+      return launch_cluster(kernel, (unsigned)grid, threads, smem, parts, stream, a);
+    };
+    auto pick = [&](auto type) {
+      using E = decltype(type);
+      if (!small && parts == 1)
+        return top_k ? go(k_score<E, 256, true, true, true>, 320, 3) : go(k_score<E, 256, false, true, true>, 320, 3);
+      if (!small)
+        return top_k ? go(k_score<E, 480, true, true, false>, 512, 2) : go(k_score<E, 480, false, true, false>, 512, 2);
+      return top_k ? go(k_score<E, 128, true, false, false>, 128, 8) : go(k_score<E, 32, false, false, false>, 32, 32);
+    };
+    e = dtype == PT_BF16 ? pick(__nv_bfloat16()) : pick(float());
     count_launch();
   }
   return (pt_status)launch_status(who, e);
@@ -851,28 +1036,27 @@ extern "C" pt_status pt_token_logprobs_bwd(const float* dlogp, const float* dent
   a.g = dlogp, a.lse = LSE, a.H = entropy, a.dH = dentropy;
   // 16-byte stores where every row of the gradient starts as its logits do
   const bool whole = ((x ^ y) & 15u) == 0 && (row_stride - d_stride) % vec == 0;
-  const int slots = (V + vec - 1) / vec;
-  constexpr int NT = 256;
-  // about two rounds of loads a CTA where rows are few
+  const int slots = (V + vec - 1) / vec, nt = slots <= 256 ? 32 : slots <= 1024 ? 128 : 256;
+  // a thread keeps at least one round of loads
   int parts = 1;
-  while (parts < 64 && slots / (parts * 2) >= NT * 4 && (long long)R * parts < 16ll * num_sms(dev)) parts *= 2;
+  while (parts < 64 && slots / (parts * 2) >= nt * 4 && (long long)R * parts < 16ll * num_sms(dev)) parts *= 2;
   while (parts > 1 && (long long)R * parts > INT_MAX) parts /= 2;
-  a.parts = parts;
+  a.lparts = __builtin_ctz((unsigned)parts);
   cudaError_t e;
   {
     ProfScope ps(stream, "token_logprobs_bwd");
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)R * (unsigned)parts), dim3(NT), 0, stream, a); };
-    if (dtype == PT_BF16) {
-      if (dentropy)
-        e = whole ? go(k_grad<__nv_bfloat16, NT, true, true>) : go(k_grad<__nv_bfloat16, NT, true, false>);
-      else
-        e = whole ? go(k_grad<__nv_bfloat16, NT, false, true>) : go(k_grad<__nv_bfloat16, NT, false, false>);
-    } else {
-      if (dentropy)
-        e = whole ? go(k_grad<float, NT, true, true>) : go(k_grad<float, NT, true, false>);
-      else
-        e = whole ? go(k_grad<float, NT, false, true>) : go(k_grad<float, NT, false, false>);
-    }
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)R * (unsigned)parts), dim3(nt), 0, stream, a); };
+    auto pick = [&](auto type, auto threads) {
+      using E = decltype(type);
+      constexpr int NT = decltype(threads)::value;
+      if (dentropy) return whole ? go(k_grad<E, NT, true, true>) : go(k_grad<E, NT, true, false>);
+      return whole ? go(k_grad<E, NT, false, true>) : go(k_grad<E, NT, false, false>);
+    };
+    auto by_threads = [&](auto type) {
+      if (nt == 32) return pick(type, std::integral_constant<int, 32>{});
+      return nt == 128 ? pick(type, std::integral_constant<int, 128>{}) : pick(type, std::integral_constant<int, 256>{});
+    };
+    e = dtype == PT_BF16 ? by_threads(__nv_bfloat16()) : by_threads(float());
     count_launch();
   }
   return (pt_status)launch_status(who, e);
