@@ -226,8 +226,8 @@ struct ScoreArgs {
 //     thread waits for memory and the joining costs no time in which nothing is
 //     loaded; one warp looks up the row's tokens (row_ptr, index, target, logit:
 //     a chain of latencies); eight compute.  Three such CTAs on an SM.
-//   CLERK alone: few long rows, shared by clusters; loads into registers.
-//   NT = 32, 128: short rows, whose latencies many rows at once hide.
+//   CLERK alone: few rows, shared by clusters; loads into registers.
+//   NT = 32, 128: many rows, or short ones; those at once hide their latencies.
 //
 // The alternatives take one more look at very little.  If every warp has q threads
 // whose maxima reach a bound, and all warps together at least k, the bound is no
@@ -953,17 +953,22 @@ extern "C" pt_status pt_token_logprobs(const void* logits, int64_t row_stride, p
   a.e = Entries{reinterpret_cast<const long long*>(targets), row_ptr, index, R, N};
   a.logp = logp, a.lse = LSE, a.H = entropy, a.top = top_logp;
   a.ids = reinterpret_cast<long long*>(top_ids);
-  // Rows of up to 8 KB: a warp each, or a CTA of four where the alternatives
-  // need maxima of more threads.  Longer ones: a CTA each with its ring, three on
-  // an SM, or where rows are few a cluster (two CTAs on an SM): the slots that the
-  // busiest SM reads, and about 5000 more for the latencies of each round.
+  // Which kernel (slots: 16 bytes of a row; us, bf16).
+  // Without alternatives: a warp a row where rows are short, or many and not long
+  // (30000 x 2048 30 and with rings 140, 15000 x 16384 87 and 113, 4864 x 32768 54
+  // and 60; but 1500 x 50001 48 and 31, 4864 x 65536 99 and 100); else a ring, or a
+  // cluster a row where rows are few.  With them: CTAs of four warps from four rows
+  // an SM on (4864 x 65536 137, with rings 167, 1000 x 16384 15 and 24), else again
+  // clusters.  A cluster's CTAs: the least of the slots that the busiest SM reads
+  // and about 5000 more for the latencies of each round of CTAs.
   const int slots = (V + 16 / es - 1) / (16 / es), sms = num_sms(dev);
-  const bool small = slots <= 512;
+  const bool rows = slots <= 512 || (top_k ? R >= 4 * sms : slots <= 4096 && R >= 20 * sms);
+  const int per_sm = top_k ? 2 : 3;  // of the undivided rows' CTAs
   int parts = 1;
-  if (!small) {
+  if (!rows) {
     long long least = LLONG_MAX;
     for (int p = 1; p <= kMaxParts && slots / p >= 480; p *= 2) {
-      const long long all = (long long)R * p, at_once = sms * (p == 1 ? 3 : 2);
+      const long long all = (long long)R * p, at_once = sms * (p == 1 ? per_sm : 2);
       const long long cost = (all + sms - 1) / sms * (slots / p) + (all + at_once - 1) / at_once * 5000;
       if (cost < least) least = cost, parts = p;
     }
@@ -977,19 +982,16 @@ extern "C" pt_status pt_token_logprobs(const void* logits, int64_t row_stride, p
       const long long grid = parts > 1 ? (long long)R * parts : std::min<long long>(R, (long long)sms * per_sm);
       const size_t smem = threads == 320 ? ring_bytes(256) : 0;
       if (smem) {
-        static std::atomic<uint64_t> opted[4];
-        const int which = (dtype == PT_BF16 ? 0 : 1) + (top_k ? 2 : 0);
-        if (cudaError_t o = opt_in_smem(kernel, smem, dev, opted[which])) return o;
+        static std::atomic<uint64_t> opted[2];
+        if (cudaError_t o = opt_in_smem(kernel, smem, dev, opted[dtype == PT_BF16 ? 0 : 1])) return o;
       }
       return launch_cluster(kernel, (unsigned)grid, threads, smem, parts, stream, a);
     };
     auto pick = [&](auto type) {
       using E = decltype(type);
-      if (!small && parts == 1)
-        return top_k ? go(k_score<E, 256, true, true, true>, 320, 3) : go(k_score<E, 256, false, true, true>, 320, 3);
-      if (!small)
-        return top_k ? go(k_score<E, 480, true, true, false>, 512, 2) : go(k_score<E, 480, false, true, false>, 512, 2);
-      return top_k ? go(k_score<E, 128, true, false, false>, 128, 8) : go(k_score<E, 32, false, false, false>, 32, 32);
+      if (top_k) return rows ? go(k_score<E, 128, true, false, false>, 128, 8) : go(k_score<E, 480, true, true, false>, 512, 2);
+      if (rows) return go(k_score<E, 32, false, false, false>, 32, 32);
+      return parts == 1 ? go(k_score<E, 256, false, true, true>, 320, 3) : go(k_score<E, 480, false, true, false>, 512, 2);
     };
     e = dtype == PT_BF16 ? pick(__nv_bfloat16()) : pick(float());
     count_launch();
@@ -1036,8 +1038,12 @@ extern "C" pt_status pt_token_logprobs_bwd(const float* dlogp, const float* dent
   a.g = dlogp, a.lse = LSE, a.H = entropy, a.dH = dentropy;
   // 16-byte stores where every row of the gradient starts as its logits do
   const bool whole = ((x ^ y) & 15u) == 0 && (row_stride - d_stride) % vec == 0;
-  const int slots = (V + vec - 1) / vec, nt = slots <= 256 ? 32 : slots <= 1024 ? 128 : 256;
-  // a thread keeps at least one round of loads
+  // Threads of a CTA: a warp for short rows (30000 x 4096 77 us, four warps 97, eight
+  // 149), eight for many long ones (3000 x 50001 97, four 102), else four (15000 x
+  // 16384 147, eight 161, one 160; 256 x 131072 24 and 27).
+  const int slots = (V + vec - 1) / vec;
+  const int nt = slots <= 768 ? 32 : slots <= 4096 || R < 16 * num_sms(dev) ? 128 : 256;
+  // CTAs of a row: each thread keeps at least one round of loads
   int parts = 1;
   while (parts < 64 && slots / (parts * 2) >= nt * 4 && (long long)R * parts < 16ll * num_sms(dev)) parts *= 2;
   while (parts > 1 && (long long)R * parts > INT_MAX) parts /= 2;

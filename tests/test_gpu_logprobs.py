@@ -97,10 +97,12 @@ def check(x, targets, row_ptr=None, index=None, k=0, scale=1.0, seed=0, grad=Tru
     wp, wl, wh = OT.logprobs(xs, targets, rows, scale)
     b = Bounds(xs, scale)
     close(lse, wl, b.tl)
+    close(bare[1], wl, b.tl)  # (with alternatives another kernel than without)
     close(H, wh, b.th)
     z = np.array([abs(xs[r, v]) * scale if r >= 0 and v >= 0 and np.isfinite(xs[r, v]) else 0.0 for v, r in zip(targets, rows)])
     at = np.maximum(rows, 0)
     close(logp, wp, b.tl[at] + 2 * U * (z + b.alse[at]) if N else 0.0)
+    close(bare[0], wp, b.tl[at] + 2 * U * (z + b.alse[at]) if N else 0.0)
     if k:
         wi = OT.top(xs, k)
         assert ids.cpu().numpy().tolist() == wi.tolist()
@@ -150,9 +152,10 @@ def test_sizes(dtype, V, R):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("R,V", [(1, 131072), (3, 200003), (40, 70001), (300, 9000), (700, 300), (1, 1048577)])
+@pytest.mark.parametrize("R,V", [(1, 131072), (3, 200003), (40, 70001), (300, 9000), (700, 300), (700, 9001), (600, 17000), (3100, 4507), (1, 1048577)])
 def test_parts(dtype, R, V):
-    """A cluster of one, two, four or eight CTAs a row; one CTA."""
+    """A cluster of two, four or eight CTAs a row; a CTA a row, with a ring or
+    without, several rows one after the other; a warp a row."""
     check(logits(R, V, dtype, R), targets_of(R, V, 2), k=7)
 
 
