@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const Dec
       // this step's values are loaded with its keys, and the next step's pages are looked up now
       const long long off = next;
       unsigned sees = 0xffffu;  // TREE: the step's tokens that row my_r sees
-      if (TREE && kv0 + STEP > lim_min) sees = dec_sees16(a, my_lo, my_lim, my_mask, my_self, kv0);
+      if (TREE && kv0 + STEP > lim_min) sees = dec_sees(a, my_lo, my_lim, my_mask, my_self, kv0);
       V kk[STEP][NV], vv[EARLY ? STEP : 1][NV];
 #pragma unroll
       for (int u = 0; u < STEP; ++u) {
@@ -665,6 +665,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
   std::vector<DecSeg> seg[kDecClasses];
   long long items[kDecClasses] = {0, 0, 0, 0};
   double tile_gain = 0.0;
+  bool few = false;
   for (int i = 0; i < N; ++i) {
     const int n = np[i + 1] - np[i];
     const long long rows = (long long)n * q_len * g;
@@ -679,6 +680,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
       const int rk = n && kind[c] >= 0 ? (int)rows | kind[c] << 29 : 0;
       seg[c].push_back(DecSeg{rk, (int)std::min<long long>(items[c], INT_MAX), np[i], n == 1 ? samp[np[i]] & INT_MAX : -1});
       if (rk) items[c] += (rows + dec_r(c) - 1) / dec_r(c) * Hkv;
+      if (rk && c == kDecRowsFew && kind[c] != kSegTail) few = true;
     }
   }
   for (int c = 0; c < kDecClasses; ++c)
@@ -709,7 +711,7 @@ extern "C" pt_status pt_decode_plan(int32_t n_nodes, const int32_t* path_ptr, co
   p->device = dev;
   p->sms = num_sms(dev);
   p->stream = stream;
-  p->N = N, p->S = S, p->Hq = Hq, p->Hkv = Hkv, p->q_len = q_len, p->own_leaves = own_leaves, p->tile_gain = (float)tile_gain;
+  p->N = N, p->S = S, p->Hq = Hq, p->Hkv = Hkv, p->q_len = q_len, p->own_leaves = own_leaves, p->few = few, p->tile_gain = (float)tile_gain;
   int rc = pool_alloc(&p->mem, host.size(), dev, stream);
   if (rc) {
     delete p;
@@ -806,7 +808,6 @@ pt_status attn_decode(const char* who, const void* Q, int64_t q_stride, const vo
   a.scale_log2 = scale * 1.4426950408889634f;
   a.mask = plan->q_len > 1 ? reinterpret_cast<const unsigned*>(mask) : nullptr;  // (one query sees itself in any case)
   a.mask_w = (plan->q_len + 31) / 32;
-  a.first_seen = a.mask ? 0 : 1;
   const bool tc = dtype == PT_BF16 && decode_tc_supported(D, page_size);
   const bool tiles = tc && use_tiles(plan, D, max_pages * page_size);
   for (int c = 0; c < kDecClasses; ++c) {
@@ -827,6 +828,7 @@ pt_status attn_decode(const char* who, const void* Q, int64_t q_stride, const vo
   if (tc) {
     m.c0 = class_args(plan, tiles ? kDecRowsFew : kDecRows, D, ws);
     if (tiles) m.c1 = class_args(plan, kDecTile, D, ws);
+    if (tiles && a.mask && !plan->few) m.c0.nitems = 0;  // (masks leave no tails)
     m.g0 = kRows;
     a.q_vec = (reinterpret_cast<uintptr_t>(Q) & 15u) == 0 && q_stride % 8 == 0;
     const int rc = decode_tc(plan, a, m.c0, m.c1, stream);

@@ -115,7 +115,6 @@ struct DecArgs {
   int q_vec;           // Q's rows start on 16-byte boundaries
   const unsigned* mask;  // [n_samples * q_len][mask_w] which drafts a query sees, or NULL: those up to itself
   int mask_w;
-  int first_seen;        // queries of a sample that all of them see: 1, or 0 with masks
   float scale_log2;
 };
 
@@ -127,9 +126,15 @@ __device__ __forceinline__ DecSeg load_seg(const DecSeg* p) {
 // A node's length, or the nearest that its table can hold.
 __device__ __forceinline__ int dec_clamp(const DecArgs& a, int len) { return min(max(len, 0), a.cap); }
 
-// Tokens [b, e) of a node of len tokens.
+// Tokens [b, e) of a node of len tokens.  With masks the tile kernel takes a
+// sample's own continuation whole (it masks by rows), and no tail is left.
 __device__ __forceinline__ void dec_range(const DecArgs& a, int kind, int len, int& b, int& e) {
-  const int body = max(len - a.q_len + a.first_seen, 0) & ~15;
+  if (a.mask) {
+    b = kind == kSegTail ? len : 0;
+    e = len;
+    return;
+  }
+  const int body = max(len - a.q_len + 1, 0) & ~15;
   b = kind == kSegTail ? body : 0;
   e = kind == kSegBody ? body : len;
 }
@@ -177,18 +182,18 @@ __device__ __forceinline__ DecTreeRow dec_tree_row(const DecArgs& a, int member0
   return t;
 }
 
-// Which of 16 tokens from kv0 a row sees (bit i: token kv0 + i); self: its own
+// Which of 32 tokens from kv0 a row sees (bit i: token kv0 + i); self: its own
 // draft's number.
-__device__ __forceinline__ unsigned dec_sees16(const DecArgs& a, int lo, int lim, int mask_row, int self, int kv0) {
-  const auto below = [&](int x) { return x >= 16 ? 0xffffu : x <= 0 ? 0u : (1u << x) - 1u; };
+__device__ __forceinline__ unsigned dec_sees(const DecArgs& a, int lo, int lim, int mask_row, int self, int kv0) {
+  const auto below = [&](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
   unsigned b = below(lo - kv0);
   const int t = kv0 - lo;  // the first of them is draft t
-  if (mask_row >= 0 && t > -16) {
+  if (mask_row >= 0 && t > -32) {
     const unsigned* m = a.mask + (long long)mask_row * a.mask_w;
     const int w = max(t, 0) >> 5;
     const unsigned m0 = w < a.mask_w ? m[w] : 0u, m1 = w + 1 < a.mask_w ? m[w + 1] : 0u;
     b |= t >= 0 ? __funnelshift_r(m0, m1, t & 31) : m0 << -t;
-    if ((unsigned)(self - t) < 16u) b |= 1u << (self - t);
+    if ((unsigned)(self - t) < 32u) b |= 1u << (self - t);
   }
   return b & below(lim - kv0);
 }
@@ -383,6 +388,7 @@ struct pt_decodeplan {
   void* mem;            // one pool allocation for every array below
   int32_t N, S, Hq, Hkv, q_len;
   bool own_leaves;      // no two samples end at one node
+  bool few;             // the class kDecRowsFew has more than tails
   float tile_gain;      // what the tile kernel saves per 128 tokens of every node that it takes
   int32_t* member;
   struct Class {

@@ -248,7 +248,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
     unsigned sees[2] = {0, 0};  // TREE: the tile's tokens that this lane's rows keep, looked up while the tile is on its way
     if (TREE && kv0 + kRowsBT > lim_min) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) sees[i] = dec_sees16(a, lo[i], lim[i], mask_row[i], self[i], kv0);
+      for (int i = 0; i < 2; ++i) sees[i] = dec_sees(a, lo[i], lim[i], mask_row[i], self[i], kv0);
     }
     ok = mbar_wait(full + s, (used / C::STAGES) & 1, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
@@ -466,8 +466,7 @@ __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& 
   s.n_tile = units_t > 0 ? sms : 0;
   if (units_t > 0 && units_r > 0) {
     // (a tile unit of 128 rows costs an SM about as much as 10 units of 16 rows and tokens, 14 at head_dim 64)
-    // (with masks a row tile's tokens are masked ones in all of a tail, and cost about twice that)
-    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f) * (a.mask ? 0.5f : 1.f);
+    const float x = (float)cost[0] * (NP == 1 ? 14.f : 10.f);
     s.n_tile = min(max((int)(sms * (x / (x + (float)cost[1]))), 1), sms - 1);
   }
   s.per_t = dec_share(units_t, max(s.n_tile, 1), kTileMinUnits);
@@ -573,7 +572,59 @@ struct TileCfg {
   static_assert(TM_O + 2 * D <= 512, "TMEM budget");
 };
 
-template <int NP>
+// Whether a token's values (D of them, D a multiple of 8) are not all finite.
+__device__ __forceinline__ bool odd_values(const uint4* v, int n) {
+  const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
+  __nv_bfloat162 sum = none;  // 0 times each
+  for (int i = 0; i < n; ++i) {
+    const uint4 x = v[i];
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum = __hfma2(w[k], none, sum);
+  }
+  const float2 f = __bfloat1622float2(sum);
+  return !(f.x == 0.f && f.y == 0.f);
+}
+
+// Trees of drafts, tile kernel: a draft's values that are not finite were kept out
+// of the products, which would have carried them (0 times them) into every row.
+// They are added here to the rows that see the draft, O in TMEM (columns from ob
+// on), once a piece's products are done.  Tokens [t, end) in question; a whole
+// warp, a row per lane (row < 0: none).  m: the reference of the row's weights.
+__device__ __noinline__ void add_odd_values(const DecArgs& a, int node, int hk, int member0, int len, int row, int t,
+                                            int end, int skip, float m, uint32_t ob) {
+  DecTreeRow d = {};
+  d.mask_row = -1;
+  if (row >= 0) d = dec_tree_row(a, member0, hk, row, len);
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.Q) + (long long)d.d.tok * a.q_stride + (long long)d.d.head * a.D;
+#pragma unroll 1
+  for (; t < end; ++t) {
+    if (skip >= 0 && ((t >> kTile.t) & 1) == skip) continue;  // (the other warpgroup's tile)
+    const int pi = t / a.ps;
+    const long long at = (((long long)dec_page(a, node, pi) * a.Hkv + hk) * a.ps + (t - pi * a.ps)) * a.D;
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.Kc) + at;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.Vc) + at;
+    if (!odd_values(reinterpret_cast<const uint4*>(v), a.D / 8)) continue;
+    const bool sees = row >= 0 && (dec_sees(a, d.lo, d.d.lim, d.mask_row, d.mask_row >= 0 ? d.mask_row % a.q_len : 0, t) & 1u);
+    float s = 0.f;
+    if (sees)
+      for (int i = 0; i < a.D; ++i) s = fmaf(__bfloat162float(q[i]), __bfloat162float(k[i]), s);
+    const float w = ex2(fmaf(s, a.scale_log2, m == -INFINITY ? 0.f : -m));
+#pragma unroll 1
+    for (int c = 0; c < a.D; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(ob + c, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (sees && c + i < a.D) o[i] = __float_as_uint(fmaf(w, __bfloat162float(v[c + i]), __uint_as_float(o[i])));
+      tmem_st32(ob + c, o);
+      tmem_st_wait();
+    }
+  }
+}
+
+template <int NP, bool TREE>
 __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     k_decode_tile(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const DecArgs a,
                   const DecClass c, const DecClass cr, const int rows_per_sm, const int box_rows, const int oob_head) {
@@ -602,6 +653,8 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   int* chunk = reinterpret_cast<int*>(smem + C::OFF_CHUNK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ unsigned long long cost[2];
+  __shared__ volatile int odd_piece[8];  // TREE: the piece (by its number modulo 8) in which a value was not finite
+  if (TREE && threadIdx.x < 8) odd_piece[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 8);
     mbar_init(q_empty, 1);
@@ -851,6 +904,9 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     while (ok) {
       // of the piece: row tiles in it, its steps, this warpgroup's rows, tokens from its first tile on, partial result
       int pair, steps, n_rows, tok, slot;
+      // TREE: the piece; its first token that a row may not see, from its first tile on; what this thread's row sees
+      DecPiece tp;
+      int mixed = INT_MAX, lo = 0, lim = 0, mask_row = -1, self = 0;
       {
         DecPiece p;
         if (!get_piece(p, it)) break;
@@ -863,6 +919,17 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         steps = (p.t1 - p.t0) << pair;
         n_rows = min(pair ? left - h * 128 : left, 128);
         slot = p.slot;
+        if constexpr (TREE) {
+          tp = p;
+          if (p.kind == kSegBody && p.t1 * kTileBT > p.len - a.q_len) {
+            mixed = max(p.len - a.q_len, 0) - p.t0 * kTileBT;
+            if (r < n_rows) {
+              const DecTreeRow d = dec_tree_row(a, p.member0, p.hk, p.rt * kTileR + (pair ? h * 128 : 0) + r, p.len);
+              lo = d.lo, lim = d.d.lim, mask_row = d.mask_row;
+              self = mask_row >= 0 ? mask_row % a.q_len : 0;
+            }
+          }
+        }
       }
       const bool live = (warp & 3) * 32 < n_rows;  // this warp has some
       float m_use = -INFINITY, l = 0.f;
@@ -872,6 +939,31 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         ok = mbar_wait(s_full + h, sc & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
+        const int from = (u >> pair) * kTileBT;  // the tile's first token, from the piece's first tile on
+        const bool masked = TREE && from + kTileBT > mixed;
+        if (masked) {
+          // Values that are not finite, of tokens that some rows do not see, are cleared (see add_odd_values; first it
+          // is said that there are some: the other warpgroup of a pair may find them cleared).
+          const uint32_t x = n + (u >> pair), vs = x % C::VS;
+          ok = mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (from + r >= mixed && r < n_tok) {
+            bool odd = false;
+#pragma unroll
+            for (int pn = 0; pn < NP; ++pn)
+              odd |= odd_values(reinterpret_cast<const uint4*>(smem + C::OFF_V + vs * C::TILE + pn * C::PANEL + r * 128), 8);
+            if (odd) {
+              odd_piece[it & 7] = (int)it;
+              __threadfence_block();
+#pragma unroll
+              for (int k = 0; k < NP * 8; ++k)
+                *reinterpret_cast<uint4*>(smem + C::OFF_V + vs * C::TILE + (k >> 3) * C::PANEL + r * 128 + (k & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          }
+          __threadfence_block();
+          fence_proxy_async_smem();
+        }
         if (n_tok < kTileBT) {
           // Clear V's rows behind the last token (both warpgroups of a pair: the same zeros).  Only now: S of this
           // step being done, the product with the tile that was in this stage before is done too, so the parity
@@ -894,7 +986,15 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
           tmem_ld32(sb + 64, sr + 64);
           tmem_ld32(sb + 96, sr + 96);
           tmem_ld_wait();
-          if (n_tok < kTileBT) {
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 128; k += 32) {
+              const unsigned sees = dec_sees(a, lo, lim, mask_row, self, tp.t0 * kTileBT + from + k);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(sees >> i & 1u)) sr[k + i] = 0xff800000u;  // -inf
+            }
+          } else if (n_tok < kTileBT) {
 #pragma unroll
             for (int k = 0; k < 128; ++k)
               if (k >= n_tok) sr[k] = 0xff800000u;  // -inf
@@ -955,6 +1055,10 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         ++oc;
         tc_fence_after();
+        if (TREE && live && odd_piece[it & 7] == (int)it)
+          add_odd_values(a, tp.node, tp.hk, tp.member0, tp.len,
+                         r < n_rows ? tp.rt * kTileR + (pair ? h * 128 : 0) + r : -1, max(mixed, 0) + tp.t0 * kTileBT,
+                         min(tp.t1 * kTileBT, tp.len), pair ? -1 : (tp.t0 + h + 1) & 1, m_use, ob);
         if (live) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           if (r < n_rows) c.lse[at] = l == 0.f ? -INFINITY : m_use + log2f(l);
@@ -1058,15 +1162,15 @@ cudaError_t launch_rows(const CUtensorMap& mK, const CUtensorMap& mV, const DecA
   return a.D <= 256 ? launch_rows<2, 2, TREE>(mK, mV, a, c, ct, s) : launch_rows<2, 4, TREE>(mK, mV, a, c, ct, s);
 }
 
-template <int NP>
+template <int NP, bool TREE>
 cudaError_t launch_tile(const CUtensorMap& mK, const CUtensorMap& mV, const DecArgs& a, const DecClass& c,
                         const DecClass& cr, int box_rows, int heads, cudaStream_t s) {
   using C = TileCfg<NP>;
   const size_t smem = C::smem(c.nseg);
   static std::atomic<uint64_t> opted{0};
-  if (cudaError_t e = opt_in_smem(k_decode_tile<NP>, C::smem(kDecMaxNodes), opted)) return e;
+  if (cudaError_t e = opt_in_smem(k_decode_tile<NP, TREE>, C::smem(kDecMaxNodes), opted)) return e;
   count_launch();
-  return launch_pdl(k_decode_tile<NP>, dim3(a.sms), dim3(C::THREADS), smem, s, mK, mV, a, c, cr,
+  return launch_pdl(k_decode_tile<NP, TREE>, dim3(a.sms), dim3(C::THREADS), smem, s, mK, mV, a, c, cr,
                     RowsCfg<NP, 1>::CTAS * RowsCfg<NP, 1>::GROUPS, box_rows, heads);
 }
 
@@ -1091,8 +1195,11 @@ int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const Dec
     const int box = std::min(a.ps & -a.ps, kTileBT);  // the largest power of two that divides a page
     if (!make_tmap_pages(&mKt, a.Kc, a.D, a.ps, heads, box, false) || !make_tmap_pages(&mVt, a.Vc, a.D, a.ps, heads, box, false))
       return PT_ERR_CUDA;
-    e = np == 1 ? launch_tile<1>(mKt, mVt, a, tile, rows, box, (int)heads, s)
-                : launch_tile<2>(mKt, mVt, a, tile, rows, box, (int)heads, s);
+    auto go = [&](auto launch) { return launch(mKt, mVt, a, tile, rows, box, (int)heads, s); };
+    if (a.mask)
+      e = np == 1 ? go(launch_tile<1, true>) : go(launch_tile<2, true>);
+    else
+      e = np == 1 ? go(launch_tile<1, false>) : go(launch_tile<2, false>);
   }
   if (e == cudaSuccess && rows.nitems)
     e = a.mask ? launch_rows<true>(mK, mV, a, rows, tile, s) : launch_rows<false>(mK, mV, a, rows, tile, s);
