@@ -289,7 +289,7 @@ __device__ __forceinline__ void merge_pieces(const MergeArgs& m, int node, const
     if (tiles > 0) {
       const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
       two = mine && sg.rows() - (rt << rl) <= kTileR / 2;
-      const int nu = dec_line(DecTiling{rl, bl, mine ? kTile.k : m.g0.k}, sg.rows(), tiles);
+      const int nu = dec_line(DecTiling{rl, bl, mine ? dec_tile(a).k : m.g0.k}, sg.rows(), tiles);
       const unsigned u0 = before + it * nu, w0 = u0 / (unsigned)per, w1 = (u0 + nu - 1) / (unsigned)per;
       row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
       count = (int)(w1 - w0 + 1) << two;
@@ -813,7 +813,7 @@ pt_status attn_decode(const char* who, const void* Q, int64_t q_stride, const vo
   for (int c = 0; c < kDecClasses; ++c) {
     const bool used = c == kDecSimt ? !tc : c == kDecRows ? tc && !tiles : tiles;
     const int bt = c == kDecSimt ? kSimtBT : c == kDecTile ? kTileBT : kRowsBT;
-    const long long line = 2ll * ((a.cap + bt - 1) / bt) + 8;  // more than an item's units
+    const long long line = 2ll * ((a.cap + bt - 1) / bt) + (a.mask ? 16 : 8);  // more than an item's units
     if (used && plan->cls[c].nitems * line > INT_MAX) {
       set_error("%s: %d work items over tables of %d tokens are out of range", who, plan->cls[c].nitems, a.cap);
       return PT_ERR_UNSUPPORTED;

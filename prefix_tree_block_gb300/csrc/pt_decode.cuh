@@ -45,6 +45,7 @@ enum : int {
 constexpr DecTiling kSimt = {2, 4, 1};  // a warp per worker
 constexpr DecTiling kRows = {4, 4, 2};  // a warp per worker
 constexpr DecTiling kTile = {8, 7, 4};  // a CTA per worker; an item of up to 128 rows has two partial results
+constexpr int kTileMaskedK = 10;        // its units beside the tiles' in calls with masks
 constexpr int kSimtR = 1 << kSimt.r, kSimtBT = 1 << kSimt.t;
 constexpr int kRowsR = 1 << kRows.r, kRowsBT = 1 << kRows.t;
 constexpr int kTileR = 1 << kTile.r, kTileBT = 1 << kTile.t;
@@ -227,6 +228,11 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
 // A tile of an item counts 2^wide units: in the tile class twice when the
 // segment has more than half a row tile, which costs twice the time.
 __device__ __forceinline__ int dec_wide(DecTiling g, int rows) { return g.r == kTile.r && rows > kTileR / 2; }
+
+// The tile class's tiling.  With masks small items are many (a sample's whole
+// continuation each) and cost more beside their tiles: the rows' limits, the masks
+// and the values' check are chains of latencies.
+__device__ __forceinline__ DecTiling dec_tile(const DecArgs& a) { return DecTiling{kTile.r, kTile.t, a.mask ? kTileMaskedK : kTile.k}; }
 
 // Units of an item of so many tiles.
 __device__ __forceinline__ int dec_line(DecTiling g, int rows, int tiles) {

@@ -456,9 +456,9 @@ __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& 
                                               int* chunk_r, unsigned long long* cost, int sms, int rows_per_sm) {
   const bool both = ct.nitems && cr.nitems;
   if (both)
-    dec_scan(a, ct, cr, kTile, kRows, chunk_t, chunk_r, cost);
+    dec_scan(a, ct, cr, dec_tile(a), kRows, chunk_t, chunk_r, cost);
   else
-    dec_scan(a, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t, ct.nitems ? kTile.k : kRows.k}, kRows,
+    dec_scan(a, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t, ct.nitems ? dec_tile(a).k : kRows.k}, kRows,
              ct.nitems ? chunk_t : chunk_r, chunk_r, nullptr);
   const int nc = (max(ct.nseg, cr.nseg) + 31) >> 5;
   const int units_t = ct.nitems ? chunk_t[nc] : 0, units_r = cr.nitems ? chunk_r[nc] : 0;
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   }
   __syncthreads();
   const DecSplit sp = dec_split<NP>(a, c, cr, chunk, chunk + ((c.nseg + 31) >> 5) + 1, cost, gridDim.x, rows_per_sm);
-  if (blockIdx.x == 0) dec_publish(a, c, kTile, chunk, sp.per_t);
+  if (blockIdx.x == 0) dec_publish(a, c, dec_tile(a), chunk, sp.per_t);
   if ((int)blockIdx.x >= sp.n_tile) return;
   const int worker = blockIdx.x, per = sp.per_t;
   if (warp == 9) {
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   };
 
   const auto producer_role = [&]() {
-    DecWalk walk(a, c, kTile, chunk, worker, per);
+    DecWalk walk(a, c, dec_tile(a), chunk, worker, per);
     DecPiece p;
     uint32_t n = 0, np = 0;  // tiles issued; pieces
     bool ok = true;
