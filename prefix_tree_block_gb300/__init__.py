@@ -851,7 +851,7 @@ def draft_tree(parents, lens, plan: DecodePlan, q_count=None, start=None, stream
     rc = load_library().pt_draft_tree(
         parents.data_ptr(), lens.data_ptr(), None if q_count is None else q_count.data_ptr(),
         None if start is None else start.data_ptr(), plan.handle, mask.data_ptr(), positions.data_ptr(),
-        _launch_stream(stream, dev, mask, positions))
+        _T[5](dev) if stream is None else _launch_stream(stream, dev, mask, positions))
     if rc:
         _check(rc)
     return mask, positions
@@ -894,27 +894,29 @@ def rotary(X, positions, inv_freq, sections=None, interleaved: bool = False, inv
     gradient.  X and out may be slices of a fused projection; out may be X."""
     _, _, i64, f32, _, _, device = _torch()
     dev = device() if X.is_cuda else -1
-    if X.dim() != 3:
+    shape = X.shape
+    if len(shape) != 3:
         raise ValueError("X is [T, H, head_dim]")
-    T, H, D = X.shape
-    code = _code(X.dtype)
-    xs = _token_rows(X, "X", X.dtype, T, H, D, dev)
+    T, H, D = shape
+    dtype = X.dtype
+    code = _code(dtype)
+    xs = _token_rows(X, "X", dtype, T, H, D, dev)
     axes = 1 if sections is None else len(sections)
-    _need(positions, "positions", i64, (T,) if positions.dim() == 1 and axes == 1 else (axes, T), dev)
+    _need(positions, "positions", i64, (T,) if axes == 1 and positions.dim() == 1 else (axes, T), dev)
     half = inv_freq.numel()
     _need(inv_freq, "inv_freq", f32, (half,), dev)
-    held = ()
-    if out is None:
-        out = _out((T, H, D), X.dtype, X)
-        held, ys = (out,), H * D
+    given = out is not None
+    if given:
+        ys = _token_rows(out, "out", dtype, T, H, D, dev)
     else:
-        ys = _token_rows(out, "out", X.dtype, T, H, D, dev)
+        out, ys = _out(shape, dtype, X), H * D
     if T == 1:  # (a token has no neighbour: one stride for both, whatever the slices')
         xs = ys = H * D
     pairs = None if sections is None else (ctypes.c_int32 * max(axes, 1))(*sections)
-    rc = load_library().pt_rotary(X.data_ptr(), xs, code, T, H, D, positions.data_ptr(), inv_freq.data_ptr(), 2 * half,
-                                  pairs, axes, interleaved, inverse, out.data_ptr(), ys,
-                                  _launch_stream(stream, dev, *held))
+    rc = load_library().pt_rotary(
+        X.data_ptr(), xs, code, T, H, D, positions.data_ptr(), inv_freq.data_ptr(), 2 * half, pairs, axes, interleaved,
+        inverse, out.data_ptr(), ys,
+        _T[5](dev) if stream is None else _launch_stream(stream, dev, *(() if given else (out,))))
     if rc:
         _check(rc)
     return out
@@ -956,21 +958,27 @@ def token_logprobs(logits, targets, row_ptr=None, index=None, top_k: int = 0, en
     likely tokens' log probabilities and ids [R, top_k] or None."""
     _, _, i64, f32, _, _, device = _torch()
     dev = device() if logits.is_cuda else -1
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits is [rows, vocabulary]")
-    R, V = logits.shape
-    code = _code(logits.dtype)
-    rs = _logit_rows(logits, "logits", logits.dtype, (R, V), dev)
-    N, *entries = _entries(targets, row_ptr, index, R, dev)
+    R, V = shape
+    dtype = logits.dtype
+    code = _code(dtype)
+    rs = _logit_rows(logits, "logits", dtype, shape, dev)
+    N, targets_p, ptr_p, index_p = _entries(targets, row_ptr, index, R, dev)
     logp, lse = _out((N,), f32, logits), _out((R,), f32, logits)
-    H = _out((R,), f32, logits) if entropy else None
-    top = _out((R, top_k), f32, logits) if top_k > 0 else None
-    ids = _out((R, top_k), i64, logits) if top_k > 0 else None
-    held = [t for t in (logp, lse, H, top, ids) if t is not None]
+    H = top = ids = None
+    H_p = top_p = ids_p = None
+    if entropy:
+        H = _out((R,), f32, logits)
+        H_p = H.data_ptr()
+    if top_k > 0:
+        top, ids = _out((R, top_k), f32, logits), _out((R, top_k), i64, logits)
+        top_p, ids_p = top.data_ptr(), ids.data_ptr()
     rc = load_library().pt_token_logprobs(
-        logits.data_ptr(), rs, code, R, V, *entries, N, scale, top_k, logp.data_ptr(), lse.data_ptr(),
-        H.data_ptr() if entropy else None, top.data_ptr() if top_k > 0 else None, ids.data_ptr() if top_k > 0 else None,
-        _launch_stream(stream, dev, *held))
+        logits.data_ptr(), rs, code, R, V, targets_p, ptr_p, index_p, N, scale, top_k, logp.data_ptr(), lse.data_ptr(),
+        H_p, top_p, ids_p, _T[5](dev) if stream is None else
+        _launch_stream(stream, dev, *[t for t in (logp, lse, H, top, ids) if t is not None]))
     if rc:
         _check(rc)
     return logp, lse, H, top, ids
