@@ -77,6 +77,7 @@ enum : int {
   kSegFull = 0,  // all of them
   kSegBody = 1,  // a sample's own continuation up to its first query token, in whole groups of 16
   kSegTail = 2,  // the rest of it: the tokens that some of the queries must not see
+  // (with masks a body is all of them, a tail none: see dec_range)
 };
 
 // One node of a class.

@@ -239,6 +239,13 @@ struct ScoreArgs {
 // told apart by their first index, so that a row of equal logits lists few of
 // them.  A list that overflows all the same (many large elements in few threads)
 // is replaced by k searches through the part.
+//
+// Bound by memory and, in bf16, nearly by issue: per element half an instruction
+// each for the maximum, the clamp, the exponent and the two sums, one each to
+// unpack and for ex2.  14k x 65536 in bf16 (1.83 GB) 272 us, the copy's rate; with
+// loads into registers instead of rings 357, with separate differences, one join of
+// all warps' statistics in each of them and no packed arithmetic 474.  One row of
+// 131072 5.3 us, 64 rows 7.7, 12 with 20 alternatives.
 // ---------------------------------------------------------------------------
 constexpr int kStages = 3;  // (four: the same; two: 2% more without alternatives)
 // Shared memory of the ring: stages of four slots a thread.
@@ -357,357 +364,357 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
   }
 #pragma unroll 1
   for (; r < a.e.R; r += step) {
-  const Row<E> row = row_of(r);
-  const Span span = span_of(row);
-  const int slots = span.slots, s0 = span.s0, s1 = span.s1, w0 = span.w0, w1 = span.w1;
-  // the first entries' logits, while the row is read
-  int my_tok = -1, my_target = -1;
-  float my_x = 0.f;
-  const int me = CLERK ? tid - NT : tid;  // the entry (of the first 32, or as many as threads) that is this thread's
-  if (part == 0 && (!CLERK || me >= 0)) {
-    int e0, e1;
-    a.e.range(r, e0, e1);
-    if (me < e1 - e0) {
-      my_tok = a.e.token(e0 + me);
-      my_target = a.e.target(my_tok, a.V);
-      if (my_target >= 0) my_x = Type<E>::f(row.x[my_target]);
-    }
-    if (me == 0) sm_e0 = e0, sm_e1 = e1;
-  }
-  // A term's exponent is one fused product and difference, x c1 - ref with ref the
-  // rounded m c1; what the rounding took is made up for at the end.
-  // ref follows the largest logit in steps of 2^8 of the terms' size.
-  Stat st = {-INFINITY, 0.f, 0.f};
-  float ref = 0.f, next = -INFINITY, own_max = -INFINITY;
-  bool plain = true;  // (ref is small enough for that (what it lost is below 1 / 16); else the sums are m's own)
-  int first = -1;     // TOP: the slots (from this one on, U of them) that the largest was first seen in
-  // Terms that are 0 in any case are raised to `low`, where their exponent is
-  // finite: 0 times it stays 0.  It lies so far below m, by 2^13 in the exponent
-  // and by several steps of bf16, that no term with a weight is touched.
-  float low = -1e4f / a.c1;
-  uint32_t low2 = pack_bf16(low, low);
-  auto take = [&](const uint4* v, auto count, int at) {  // so many slots from `at` on; their largest
-    constexpr int n = decltype(count)::value;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-    float bm;
-    if constexpr (sizeof(E) == 2) {
-      uint32_t b[4] = {w[0], w[1], w[2], w[3]};
-#pragma unroll
-      for (int i = 4; i < 4 * n; ++i) b[i & 3] = max_bf2(b[i & 3], w[i]);
-      const uint32_t c = max_bf2(max_bf2(b[0], b[1]), max_bf2(b[2], b[3]));
-      bm = fmaxf(__uint_as_float(c << 16), __uint_as_float(c & 0xffff0000u));
-    } else {
-      bm = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
-#pragma unroll
-      for (int i = 4; i < 4 * n; i += 2) bm = fmax3(bm, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-    }
-    if constexpr (TOP) {
-      if (first < 0 || bm > own_max) first = at;
-      own_max = fmaxf(own_max, bm);
-    }
-    if (bm > next) {
-      const float old = st.m, old_ref = ref;
-      const bool was = plain;
-      st.m = bm;
-      next = bm + 8.f / a.c1;
-      const float base = st.m == -INFINITY ? 0.f : st.m;
-      ref = base * a.c1;
-      plain = fabsf(ref) < 1048576.f && fabsf(base) < 1e37f;
-      if (old != -INFINITY)
-        rebase(st.s, st.t, was && plain ? old_ref - ref
-                                        : (old - base) * a.c1 - (was ? fmaf(old, a.c1, -old_ref) : 0.f) + (plain ? fmaf(base, a.c1, -ref) : 0.f));
-      low = base - fmaxf(1e4f / a.c1, fabsf(base) * 0.03125f);
-      low2 = pack_bf16(low, low);
-    }
-    if (plain) {
-      const unsigned long long c2 = f2_splat(a.c1), r2 = f2_splat(-ref);
-      unsigned long long s2[2] = {0ull, 0ull}, t2[2] = {0ull, 0ull};
-#pragma unroll
-      for (int i = 0; i < 4 * n; ++i) {
-        unsigned long long x2;
-        if constexpr (sizeof(E) == 2) {
-          const uint32_t y = max_nan_bf2(w[i], low2);
-          x2 = f2_pack(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
-        } else {
-          if (i & 1) continue;
-          const float x = __uint_as_float(w[i]), y = __uint_as_float(w[i + 1]);
-          x2 = f2_pack(x < low ? low : x, y < low ? low : y);
-        }
-        const unsigned long long d2 = f2_fma(x2, c2, r2);
-        float d0, d1;
-        f2_unpack(d2, d0, d1);
-        const unsigned long long e2 = f2_pack(ex2(d0), ex2(d1));
-        s2[(i >> 1) & 1] = f2_add(s2[(i >> 1) & 1], e2);
-        t2[(i >> 1) & 1] = f2_fma(d2, e2, t2[(i >> 1) & 1]);
+    const Row<E> row = row_of(r);
+    const Span span = span_of(row);
+    const int slots = span.slots, s0 = span.s0, s1 = span.s1, w0 = span.w0, w1 = span.w1;
+    // the first entries' logits, while the row is read
+    int my_tok = -1, my_target = -1;
+    float my_x = 0.f;
+    const int me = CLERK ? tid - NT : tid;  // the entry (of the first 32, or as many as threads) that is this thread's
+    if (part == 0 && (!CLERK || me >= 0)) {
+      int e0, e1;
+      a.e.range(r, e0, e1);
+      if (me < e1 - e0) {
+        my_tok = a.e.token(e0 + me);
+        my_target = a.e.target(my_tok, a.V);
+        if (my_target >= 0) my_x = Type<E>::f(row.x[my_target]);
       }
-      float x0, x1, y0, y1;
-      f2_unpack(f2_add(s2[0], s2[1]), x0, x1);
-      f2_unpack(f2_add(t2[0], t2[1]), y0, y1);
-      st.s += x0 + x1;
-      st.t += y0 + y1;
-    } else {  // logits (times scale) of a million and more, infinities: differences first
+      if (me == 0) sm_e0 = e0, sm_e1 = e1;
+    }
+    // A term's exponent is one fused product and difference, x c1 - ref with ref the
+    // rounded m c1; what the rounding took is made up for at the end.
+    // ref follows the largest logit in steps of 2^8 of the terms' size.
+    Stat st = {-INFINITY, 0.f, 0.f};
+    float ref = 0.f, next = -INFINITY, own_max = -INFINITY;
+    bool plain = true;  // (ref is small enough for that (what it lost is below 1 / 16); else the sums are m's own)
+    int first = -1;     // TOP: the slots (from this one on, U of them) that the largest was first seen in
+    // Terms that are 0 in any case are raised to `low`, where their exponent is
+    // finite: 0 times it stays 0.  It lies so far below m, by 2^13 in the exponent
+    // and by several steps of bf16, that no term with a weight is touched.
+    float low = -1e4f / a.c1;
+    uint32_t low2 = pack_bf16(low, low);
+    auto take = [&](const uint4* v, auto count, int at) {  // so many slots from `at` on; their largest
+      constexpr int n = decltype(count)::value;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+      float bm;
+      if constexpr (sizeof(E) == 2) {
+        uint32_t b[4] = {w[0], w[1], w[2], w[3]};
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float2 d = far_terms<E>(v[i], st.m == -INFINITY ? 0.f : st.m, a.c1);
-        st.s += d.x, st.t += d.y;
+        for (int i = 4; i < 4 * n; ++i) b[i & 3] = max_bf2(b[i & 3], w[i]);
+        const uint32_t c = max_bf2(max_bf2(b[0], b[1]), max_bf2(b[2], b[3]));
+        bm = fmaxf(__uint_as_float(c << 16), __uint_as_float(c & 0xffff0000u));
+      } else {
+        bm = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+#pragma unroll
+        for (int i = 4; i < 4 * n; i += 2) bm = fmax3(bm, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
       }
-    }
-    return bm;
-  };
-  using One = std::integral_constant<int, 1>;
-  using All = std::integral_constant<int, U>;
-  // whole slots, then the ones at the row's ends
-  int chunks = 0;  // rounds of U slots
-#pragma unroll 1
-  for (int s = w0 + tid; reads && (RING ? s - tid : s) < w1; s += NT * U, ++chunks) {  // (RING: whole warps, for the stages)
-    if (RING || s != w0 + tid) fetch(row, s, w1);
-    float largest = -INFINITY;
-    if (s + (U - 1) * NT < w1) {
-      largest = take(v, All{}, s);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u * NT < w1) largest = fmaxf(largest, take(v + u, One{}, s + u * NT));
-    }
-    if constexpr (TOP) {
-      const unsigned short o = (unsigned short)(ordered(largest) >> 16);
-      unsigned short& g = sm_group[chunks & (kGroups - 1)][tid];
-      g = chunks < kGroups ? o : max(g, o);
-    }
-  }
-  int edge = -1;  // a slot at the row's end that is this thread's
-  if (tid == 0 && s0 == 0 && s1 > 0 && !row.whole(0)) edge = 0;
-  if (tid == NT - 1 && s1 == slots && s1 > s0 && slots > 1 && !row.whole(slots - 1)) edge = slots - 1;
-  if (edge >= 0) {
-    const uint4 y = row.pack(edge);
-    take(&y, One{}, edge);
-  }
-  if (!RING && r + step < a.e.R) {
-    const Row<E> next_row = row_of(r + step);
-    const Span p = span_of(next_row);
-    fetch(next_row, p.w0 + tid, p.w1);
-  }
-  if (plain) rebase(st.s, st.t, -fmaf(st.m == -INFINITY ? 0.f : st.m, a.c1, -ref));
-  // the CTA's statistics
-  st = join_lanes<16>(st, a.c1);
-  if (lane == 0 && reads) sm_stat[warp] = st;
-  unsigned mine = 0;  // TOP: this thread's largest logit
-  if constexpr (TOP) {
-    mine = first >= 0 ? ordered(own_max) : 0u;
-    // the warp's largest maximum and its q-th largest
-    unsigned rest = mine, most = 0, least = 0;
-    const int q = (a.k + NT / 32 - 1) / (NT / 32);
-#pragma unroll 1
-    for (int i = 0; i < q; ++i) {
-      least = __reduce_max_sync(0xffffffffu, rest);
-      if (i == 0) most = least;
-      if (lane == __ffs(__ballot_sync(0xffffffffu, rest == least)) - 1) rest = 0;
-    }
-    if (lane == 0 && reads) sm_most[warp] = most, sm_least[warp] = least;
-    if (tid == 0) sm_n = sm_w = 0;
-    for (int i = tid; i < a.k; i += ALL) sm_best[i] = 0;
-  }
-  sync();
-  if (warp == 0) {
-    if constexpr (NT > 32) st = join_lanes<NT <= 128 ? 2 : 8>(lane < NT / 32 ? sm_stat[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c1);
-    if (lane == 0) sm_part = st;
-  }
-  if constexpr (TOP) {
-    const int k = a.k;
-    unsigned lo = 0xffffffffu, hi = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) lo = min(lo, sm_least[w]), hi = max(hi, sm_most[w]);
-    ++hi;  // (a value's order is below 2^32 - 1)
-    int reach = count(mine >= lo);  // threads that reach lo: k at least (with lo = 0 all)
-    const bool far = reach > 2 * k + 32 || lo == 0;  // (0: a warp without q threads that hold any)
-#pragma unroll 1
-    while (far && hi - lo > 1 && reach > k + 8) {
-      const unsigned mid = lo + ((hi - lo) >> 1);
-      const int n = count(mine >= mid);
-      if (n >= k)
-        lo = mid, reach = n;
-      else
-        hi = mid;
-    }
-    unsigned long long bound = (unsigned long long)lo << 32;
-    unsigned long long best_key = (unsigned long long)mine << 32 | 0xffffffffu;  // (no less than the thread's best)
-    if (far && hi - lo == 1 && lo && reach > k + 8) {
-      // equal maxima: by the first index that holds it
-      unsigned inv = 0;  // ~index: larger for lower ones
-      if (mine == lo) {
-        int at = INT_MAX;
-        if (first == edge) {
-          float y[V];
-          row.get(edge, y);
-#pragma unroll
-          for (int i = V - 1; i >= 0; --i) {
-            const int v = edge * V - row.lead + i;
-            if (v >= 0 && v < a.V && ordered(y[i]) == mine) at = v;
-          }
-        } else {
-#pragma unroll 1
-          for (int s = first; s < w1 && s < first + NT * U; s += NT) {
-            float y[V];
-            row.get(s, y);
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-              if (ordered(y[i]) == mine) at = min(at, s * V - row.lead + i);
-          }
-        }
-        inv = 0xffffffffu - (unsigned)at;
-        best_key = (unsigned long long)mine << 32 | inv;
-      }
-      const int above = count(mine > lo);
-      unsigned l = 0, h = 0xffffffffu;
-#pragma unroll 1
-      while (h - l > 1) {
-        const unsigned mid = l + ((h - l) >> 1);
-        if (above + count(mine == lo && inv >= mid) >= k)
-          l = mid;
-        else
-          h = mid;
-      }
-      bound |= l;
-    }
-    // the groups that hold candidates, and their elements
-    if (reads && mine && best_key >= bound) {
-      const unsigned reach16 = (unsigned)(bound >> 48);
-#pragma unroll 1
-      for (int c = 0; c < min(chunks, kGroups); ++c)
-        if (sm_group[c][tid] >= reach16) {
-          const int at = atomicAdd(&sm_w, 1);
-          if (at < kCandidates) sm_who[at] = tid | c << 16;
-        }
-    }
-    sync();
-    const float least = value_of(bound);
-    auto put = [&](int s, const uint4& w) {
-      float y[V];
-      unpack(w, y);
-      float top = y[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) top = fmaxf(top, y[i]);
-      if (top < least) return;  // most slots (a NaN passes on)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (y[i] < least) continue;
-        const int v = s * V - row.lead + i;
-        const unsigned long long key = key_of(y[i], v);
-        if (key >= bound && v >= 0 && v < a.V) {
-          const int at = atomicAdd(&sm_n, 1);
-          if (at < kCandidates) sm_cand[at] = key;
-        }
-      }
-    };
-    // (a group: U slots of every kGroups-th round)
-    const int rounds = (w1 - w0 + NT * U - 1) / (NT * U), reps = (rounds + kGroups - 1) / kGroups, listed = sm_w;
-    const int all = min(listed, kCandidates) * U * reps;
-#pragma unroll 1
-    for (int x = tid; x < all; x += ALL) {
-      const int y = x / U, i = reps == 1 ? y : y / reps, g = sm_who[i];
-      const int s = w0 + (g & 0xffff) + ((g >> 16) + (y - i * reps) * kGroups) * (NT * U) + (x % U) * NT;
-      if (s < w1) put(s, row.load(s));
-    }
-    if (edge >= 0) put(edge, row.pack(edge));
-    sync();
-    const int n = sm_n;
-    if (n <= kCandidates && listed <= kCandidates) {
-#pragma unroll 1
-      for (int i = tid; i < n; i += ALL) {
-        const unsigned long long key = sm_cand[i];
-        int above = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) above += sm_cand[j] > key;
-        if (above < k) sm_best[above] = key;
-      }
-    } else {  // k searches
-      unsigned long long below = ~0ull;
-#pragma unroll 1
-      for (int i = 0; i < k; ++i) {
-        unsigned long long best = 0;
-#pragma unroll 1
-        for (int s = s0 + tid; s < s1; s += ALL) {
-          float y[V];
-          row.get(s, y);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int v = s * V - row.lead + j;
-            const unsigned long long key = key_of(y[j], v);
-            if (v >= 0 && v < a.V && key < below && key > best) best = key;
-          }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        sync();
-        if (lane == 0) sm_cand[warp] = best;
-        sync();
-        below = 0;
-        for (int w = 0; w < ALL / 32; ++w) below = max(below, sm_cand[w]);
-        if (tid == 0) sm_best[i] = below;
-        if (below == 0) below = 1;  // (no more of them)
-      }
-    }
-    sync();
-  }
-  if (a.lparts > 0) {  // the cluster's
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    if (part == 0) {
-      if (warp == 0) st = join_lanes<kMaxParts / 2>(lane < 1 << a.lparts ? *cluster.map_shared_rank(&sm_part, lane) : Stat{-INFINITY, 0.f, 0.f}, a.c1);
       if constexpr (TOP) {
-        const int n = a.k << a.lparts;  // (at most kMaxParts * kMaxTop)
-        for (int i = tid; i < n; i += ALL) sm_cand[i] = cluster.map_shared_rank(&sm_best[0], i / a.k)[i % a.k];
-        sync();
+        if (first < 0 || bm > own_max) first = at;
+        own_max = fmaxf(own_max, bm);
+      }
+      if (bm > next) {
+        const float old = st.m, old_ref = ref;
+        const bool was = plain;
+        st.m = bm;
+        next = bm + 8.f / a.c1;
+        const float base = st.m == -INFINITY ? 0.f : st.m;
+        ref = base * a.c1;
+        plain = fabsf(ref) < 1048576.f && fabsf(base) < 1e37f;
+        if (old != -INFINITY)
+          rebase(st.s, st.t, was && plain ? old_ref - ref
+                                          : (old - base) * a.c1 - (was ? fmaf(old, a.c1, -old_ref) : 0.f) + (plain ? fmaf(base, a.c1, -ref) : 0.f));
+        low = base - fmaxf(1e4f / a.c1, fabsf(base) * 0.03125f);
+        low2 = pack_bf16(low, low);
+      }
+      if (plain) {
+        const unsigned long long c2 = f2_splat(a.c1), r2 = f2_splat(-ref);
+        unsigned long long s2[2] = {0ull, 0ull}, t2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int i = 0; i < 4 * n; ++i) {
+          unsigned long long x2;
+          if constexpr (sizeof(E) == 2) {
+            const uint32_t y = max_nan_bf2(w[i], low2);
+            x2 = f2_pack(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+          } else {
+            if (i & 1) continue;
+            const float x = __uint_as_float(w[i]), y = __uint_as_float(w[i + 1]);
+            x2 = f2_pack(x < low ? low : x, y < low ? low : y);
+          }
+          const unsigned long long d2 = f2_fma(x2, c2, r2);
+          float d0, d1;
+          f2_unpack(d2, d0, d1);
+          const unsigned long long e2 = f2_pack(ex2(d0), ex2(d1));
+          s2[(i >> 1) & 1] = f2_add(s2[(i >> 1) & 1], e2);
+          t2[(i >> 1) & 1] = f2_fma(d2, e2, t2[(i >> 1) & 1]);
+        }
+        float x0, x1, y0, y1;
+        f2_unpack(f2_add(s2[0], s2[1]), x0, x1);
+        f2_unpack(f2_add(t2[0], t2[1]), y0, y1);
+        st.s += x0 + x1;
+        st.t += y0 + y1;
+      } else {  // logits (times scale) of a million and more, infinities: differences first
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float2 d = far_terms<E>(v[i], st.m == -INFINITY ? 0.f : st.m, a.c1);
+          st.s += d.x, st.t += d.y;
+        }
+      }
+      return bm;
+    };
+    using One = std::integral_constant<int, 1>;
+    using All = std::integral_constant<int, U>;
+    // whole slots, then the ones at the row's ends
+    int chunks = 0;  // rounds of U slots
+#pragma unroll 1
+    for (int s = w0 + tid; reads && (RING ? s - tid : s) < w1; s += NT * U, ++chunks) {  // (RING: whole warps, for the stages)
+      if (RING || s != w0 + tid) fetch(row, s, w1);
+      float largest = -INFINITY;
+      if (s + (U - 1) * NT < w1) {
+        largest = take(v, All{}, s);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (s + u * NT < w1) largest = fmaxf(largest, take(v + u, One{}, s + u * NT));
+      }
+      if constexpr (TOP) {
+        const unsigned short o = (unsigned short)(ordered(largest) >> 16);
+        unsigned short& g = sm_group[chunks & (kGroups - 1)][tid];
+        g = chunks < kGroups ? o : max(g, o);
+      }
+    }
+    int edge = -1;  // a slot at the row's end that is this thread's
+    if (tid == 0 && s0 == 0 && s1 > 0 && !row.whole(0)) edge = 0;
+    if (tid == NT - 1 && s1 == slots && s1 > s0 && slots > 1 && !row.whole(slots - 1)) edge = slots - 1;
+    if (edge >= 0) {
+      const uint4 y = row.pack(edge);
+      take(&y, One{}, edge);
+    }
+    if (!RING && r + step < a.e.R) {
+      const Row<E> next_row = row_of(r + step);
+      const Span p = span_of(next_row);
+      fetch(next_row, p.w0 + tid, p.w1);
+    }
+    if (plain) rebase(st.s, st.t, -fmaf(st.m == -INFINITY ? 0.f : st.m, a.c1, -ref));
+    // the CTA's statistics
+    st = join_lanes<16>(st, a.c1);
+    if (lane == 0 && reads) sm_stat[warp] = st;
+    unsigned mine = 0;  // TOP: this thread's largest logit
+    if constexpr (TOP) {
+      mine = first >= 0 ? ordered(own_max) : 0u;
+      // the warp's largest maximum and its q-th largest
+      unsigned rest = mine, most = 0, least = 0;
+      const int q = (a.k + NT / 32 - 1) / (NT / 32);
+#pragma unroll 1
+      for (int i = 0; i < q; ++i) {
+        least = __reduce_max_sync(0xffffffffu, rest);
+        if (i == 0) most = least;
+        if (lane == __ffs(__ballot_sync(0xffffffffu, rest == least)) - 1) rest = 0;
+      }
+      if (lane == 0 && reads) sm_most[warp] = most, sm_least[warp] = least;
+      if (tid == 0) sm_n = sm_w = 0;
+      for (int i = tid; i < a.k; i += ALL) sm_best[i] = 0;
+    }
+    sync();
+    if (warp == 0) {
+      if constexpr (NT > 32) st = join_lanes<NT <= 128 ? 2 : 8>(lane < NT / 32 ? sm_stat[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c1);
+      if (lane == 0) sm_part = st;
+    }
+    if constexpr (TOP) {
+      const int k = a.k;
+      unsigned lo = 0xffffffffu, hi = 0;
+#pragma unroll
+      for (int w = 0; w < NT / 32; ++w) lo = min(lo, sm_least[w]), hi = max(hi, sm_most[w]);
+      ++hi;  // (a value's order is below 2^32 - 1)
+      int reach = count(mine >= lo);  // threads that reach lo: k at least (with lo = 0 all)
+      const bool far = reach > 2 * k + 32 || lo == 0;  // (0: a warp without q threads that hold any)
+#pragma unroll 1
+      while (far && hi - lo > 1 && reach > k + 8) {
+        const unsigned mid = lo + ((hi - lo) >> 1);
+        const int n = count(mine >= mid);
+        if (n >= k)
+          lo = mid, reach = n;
+        else
+          hi = mid;
+      }
+      unsigned long long bound = (unsigned long long)lo << 32;
+      unsigned long long best_key = (unsigned long long)mine << 32 | 0xffffffffu;  // (no less than the thread's best)
+      if (far && hi - lo == 1 && lo && reach > k + 8) {
+        // equal maxima: by the first index that holds it
+        unsigned inv = 0;  // ~index: larger for lower ones
+        if (mine == lo) {
+          int at = INT_MAX;
+          if (first == edge) {
+            float y[V];
+            row.get(edge, y);
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i) {
+              const int v = edge * V - row.lead + i;
+              if (v >= 0 && v < a.V && ordered(y[i]) == mine) at = v;
+            }
+          } else {
+#pragma unroll 1
+            for (int s = first; s < w1 && s < first + NT * U; s += NT) {
+              float y[V];
+              row.get(s, y);
+#pragma unroll
+              for (int i = V - 1; i >= 0; --i)
+                if (ordered(y[i]) == mine) at = min(at, s * V - row.lead + i);
+            }
+          }
+          inv = 0xffffffffu - (unsigned)at;
+          best_key = (unsigned long long)mine << 32 | inv;
+        }
+        const int above = count(mine > lo);
+        unsigned l = 0, h = 0xffffffffu;
+#pragma unroll 1
+        while (h - l > 1) {
+          const unsigned mid = l + ((h - l) >> 1);
+          if (above + count(mine == lo && inv >= mid) >= k)
+            l = mid;
+          else
+            h = mid;
+        }
+        bound |= l;
+      }
+      // the groups that hold candidates, and their elements
+      if (reads && mine && best_key >= bound) {
+        const unsigned reach16 = (unsigned)(bound >> 48);
+#pragma unroll 1
+        for (int c = 0; c < min(chunks, kGroups); ++c)
+          if (sm_group[c][tid] >= reach16) {
+            const int at = atomicAdd(&sm_w, 1);
+            if (at < kCandidates) sm_who[at] = tid | c << 16;
+          }
+      }
+      sync();
+      const float least = value_of(bound);
+      auto put = [&](int s, const uint4& w) {
+        float y[V];
+        unpack(w, y);
+        float top = y[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, y[i]);
+        if (top < least) return;  // most slots (a NaN passes on)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (y[i] < least) continue;
+          const int v = s * V - row.lead + i;
+          const unsigned long long key = key_of(y[i], v);
+          if (key >= bound && v >= 0 && v < a.V) {
+            const int at = atomicAdd(&sm_n, 1);
+            if (at < kCandidates) sm_cand[at] = key;
+          }
+        }
+      };
+      // (a group: U slots of every kGroups-th round)
+      const int rounds = (w1 - w0 + NT * U - 1) / (NT * U), reps = (rounds + kGroups - 1) / kGroups, listed = sm_w;
+      const int all = min(listed, kCandidates) * U * reps;
+#pragma unroll 1
+      for (int x = tid; x < all; x += ALL) {
+        const int y = x / U, i = reps == 1 ? y : y / reps, g = sm_who[i];
+        const int s = w0 + (g & 0xffff) + ((g >> 16) + (y - i * reps) * kGroups) * (NT * U) + (x % U) * NT;
+        if (s < w1) put(s, row.load(s));
+      }
+      if (edge >= 0) put(edge, row.pack(edge));
+      sync();
+      const int n = sm_n;
+      if (n <= kCandidates && listed <= kCandidates) {
+#pragma unroll 1
         for (int i = tid; i < n; i += ALL) {
           const unsigned long long key = sm_cand[i];
           int above = 0;
 #pragma unroll 4
           for (int j = 0; j < n; ++j) above += sm_cand[j] > key;
-          if (above < a.k && key) sm_key[above] = key;
+          if (above < k) sm_best[above] = key;
+        }
+      } else {  // k searches
+        unsigned long long below = ~0ull;
+#pragma unroll 1
+        for (int i = 0; i < k; ++i) {
+          unsigned long long best = 0;
+#pragma unroll 1
+          for (int s = s0 + tid; s < s1; s += ALL) {
+            float y[V];
+            row.get(s, y);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const int v = s * V - row.lead + j;
+              const unsigned long long key = key_of(y[j], v);
+              if (v >= 0 && v < a.V && key < below && key > best) best = key;
+            }
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+          sync();
+          if (lane == 0) sm_cand[warp] = best;
+          sync();
+          below = 0;
+          for (int w = 0; w < ALL / 32; ++w) below = max(below, sm_cand[w]);
+          if (tid == 0) sm_best[i] = below;
+          if (below == 0) below = 1;  // (no more of them)
         }
       }
+      sync();
     }
-    cluster.sync();  // (the others' shared memory has been read)
-    if (part) return;
-    if (tid == 0) sm_part = st;
-  }
-  const int e0 = sm_e0, e1 = sm_e1;  // (before the barrier: behind it the next row's may come)
-  sync();
-  st = sm_part;
-  // the row's results
-  const float z = st.m * a.scale;  // (S is at least 1)
-  const float ln_s = st.m == -INFINITY ? 0.f : logf(st.s);
-  const float lse = st.s != st.s ? st.s : st.m == -INFINITY ? -INFINITY : z + ln_s;
-  if (tid == 0) {
-    a.lse[r] = lse;
-    if (a.H) a.H[r] = st.m == -INFINITY && st.s == st.s ? 0.f : ln_s - 0.69314718055994531f * (st.t / st.s);
-  }
-  // (from m, not from LSE: large logits then lose nothing)
-  auto log_p = [&](float x) { return lse == -INFINITY ? -INFINITY : (x - st.m) * a.scale - ln_s; };
-  if constexpr (TOP) {
-    const unsigned long long* best = a.lparts > 0 ? sm_key : sm_best;
-    for (int i = tid; i < a.k; i += ALL) {
-      const unsigned long long key = best[i];
-      a.top[(long long)r * a.k + i] = log_p(value_of(key));
-      a.ids[(long long)r * a.k + i] = index_of(key);
+    if (a.lparts > 0) {  // the cluster's
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      if (part == 0) {
+        if (warp == 0) st = join_lanes<kMaxParts / 2>(lane < 1 << a.lparts ? *cluster.map_shared_rank(&sm_part, lane) : Stat{-INFINITY, 0.f, 0.f}, a.c1);
+        if constexpr (TOP) {
+          const int n = a.k << a.lparts;  // (at most kMaxParts * kMaxTop)
+          for (int i = tid; i < n; i += ALL) sm_cand[i] = cluster.map_shared_rank(&sm_best[0], i / a.k)[i % a.k];
+          sync();
+          for (int i = tid; i < n; i += ALL) {
+            const unsigned long long key = sm_cand[i];
+            int above = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) above += sm_cand[j] > key;
+            if (above < a.k && key) sm_key[above] = key;
+          }
+        }
+      }
+      cluster.sync();  // (the others' shared memory has been read)
+      if (part) return;
+      if (tid == 0) sm_part = st;
     }
-  }
-  auto put_logp = [&](int tok, int target, float x) {
-    if (tok >= 0) a.logp[tok] = target < 0 ? 0.f : log_p(x);
-  };
-  if (me >= 0) put_logp(my_tok, my_target, my_x);
+    const int e0 = sm_e0, e1 = sm_e1;  // (before the barrier: behind it the next row's may come)
+    sync();
+    st = sm_part;
+    // the row's results
+    const float z = st.m * a.scale;  // (S is at least 1)
+    const float ln_s = st.m == -INFINITY ? 0.f : logf(st.s);
+    const float lse = st.s != st.s ? st.s : st.m == -INFINITY ? -INFINITY : z + ln_s;
+    if (tid == 0) {
+      a.lse[r] = lse;
+      if (a.H) a.H[r] = st.m == -INFINITY && st.s == st.s ? 0.f : ln_s - 0.69314718055994531f * (st.t / st.s);
+    }
+    // (from m, not from LSE: large logits then lose nothing)
+    auto log_p = [&](float x) { return lse == -INFINITY ? -INFINITY : (x - st.m) * a.scale - ln_s; };
+    if constexpr (TOP) {
+      const unsigned long long* best = a.lparts > 0 ? sm_key : sm_best;
+      for (int i = tid; i < a.k; i += ALL) {
+        const unsigned long long key = best[i];
+        a.top[(long long)r * a.k + i] = log_p(value_of(key));
+        a.ids[(long long)r * a.k + i] = index_of(key);
+      }
+    }
+    auto put_logp = [&](int tok, int target, float x) {
+      if (tok >= 0) a.logp[tok] = target < 0 ? 0.f : log_p(x);
+    };
+    if (me >= 0) put_logp(my_tok, my_target, my_x);
 #pragma unroll 1
-  for (int n = e0 + (CLERK ? 32 : NT) + tid; n < e1; n += ALL) {
-    const int tok = a.e.token(n), target = a.e.target(tok, a.V);
-    put_logp(tok, target, target >= 0 ? Type<E>::f(row.x[target]) : 0.f);
-  }
-  if (r == a.e.R - 1 && a.e.row_ptr) {  // entries of no row
-    const int end = min(max(a.e.row_ptr[a.e.R], 0), a.e.N);
-    for (int n = end + tid; n < a.e.N; n += ALL) {
-      const int tok = a.e.token(n);
-      if (tok >= 0) a.logp[tok] = 0.f;
+    for (int n = e0 + (CLERK ? 32 : NT) + tid; n < e1; n += ALL) {
+      const int tok = a.e.token(n), target = a.e.target(tok, a.V);
+      put_logp(tok, target, target >= 0 ? Type<E>::f(row.x[target]) : 0.f);
     }
-  }
+    if (r == a.e.R - 1 && a.e.row_ptr) {  // entries of no row
+      const int end = min(max(a.e.row_ptr[a.e.R], 0), a.e.N);
+      for (int n = end + tid; n < a.e.N; n += ALL) {
+        const int tok = a.e.token(n);
+        if (tok >= 0) a.logp[tok] = 0.f;
+      }
+    }
   }
 }
 
@@ -731,7 +738,9 @@ struct GradArgs {
 // whether it holds one, and a slot that does adds the entries' gradients in
 // their order before it rounds, so equal targets and any order of the calls
 // give the same bits.  A thread holds what it read until it writes, so the
-// gradient may take the logits' place.
+// gradient may take the logits' place.  Its first loads are issued before the
+// tokens are looked up.  Bound by memory: 14k x 65536 in bf16 with the entropy's
+// part (3.7 GB) 549 us, the copy's rate; 1000 x 50001 in fp32 64 us, 92%.
 // ---------------------------------------------------------------------------
 constexpr int kSlotBits = 4096;
 
@@ -1023,8 +1032,12 @@ extern "C" pt_status pt_token_logprobs_bwd(const float* dlogp, const float* dent
   }
   const uintptr_t nx = ((uintptr_t)(R - 1) * row_stride + V) * es, ny = ((uintptr_t)(R - 1) * d_stride + V) * es;
   if (!(x == y && row_stride == d_stride) && x < y + ny && y < x + nx) {
-    set_error("%s: the gradient overlaps the logits without taking their place", who);
-    return PT_ERR_INVALID_ARG;
+    // (columns of one buffer that do not meet: equal strides, the rows side by side)
+    const uintptr_t gap = (x > y ? x - y : y - x) % ((uintptr_t)row_stride * es), row = (uintptr_t)V * es;
+    if (row_stride != d_stride || gap < row || (uintptr_t)row_stride * es - gap < row) {
+      set_error("%s: the gradient overlaps the logits without taking their place", who);
+      return PT_ERR_INVALID_ARG;
+    }
   }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {

@@ -190,6 +190,16 @@ def test_lengths_of_drafts(q, dtype):
         compare(*got, lens, paths, q, sees_of(up, q), None, 0.3)
 
 
+@pytest.mark.parametrize("D,dtype", [(1, F32), (33, F32), (66, F32), (128, F32), (130, F32), (256, F32), (257, F32), (512, F32),
+                                     (8, BF), (72, BF), (104, BF), (128, BF), (200, BF), (264, BF), (512, BF)])
+def test_head_dims(D, dtype):
+    lens, paths = NODES["deep"]
+    up = parents_of(len(paths), 7, "any", D)
+    for width in (None, 4096) if dtype == BF and D <= 128 else (None,):
+        got = attend(lens, paths, 24, 2, D, dtype, 16, 7, up, None, seed=D, width=width)
+        compare(*got, lens, paths, 7, sees_of(up, 7), None)
+
+
 def test_more_drafts_than_trees_have():
     """Masks of the caller's own, of more drafts than pt_draft_tree takes."""
     q, paths, lens = 300, [[0, 1]], [20, 340]
@@ -198,8 +208,8 @@ def test_more_drafts_than_trees_have():
     words = np.zeros((q, 320), np.uint64)
     words[:, :q] = sees
     words = (words.reshape(q, 10, 32) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32).view(np.int32)
-    for dtype in (BF, F32):
-        got = attend(lens, paths, 2, 1, 64, dtype, 16, q, None, None, mask=torch.from_numpy(words).cuda())
+    for dtype, width in ((BF, None), (BF, 65536), (F32, None)):  # (wide: the kernel for many rows)
+        got = attend(lens, paths, 2, 1, 64, dtype, 16, q, None, None, mask=torch.from_numpy(words).cuda(), width=width)
         compare(*got, lens, paths, q, [[sorted(set(np.flatnonzero(sees[j])) | {j}) for j in range(q)]], None)
 
 
@@ -270,6 +280,61 @@ def test_a_hidden_drafts_values_stay_hidden(dtype, D, value, what, width):
     O2[hit] = torch.from_numpy(wo).to(dtype)[hit]
     L2[:, hit] = torch.from_numpy(wl).float()[:, hit]
     compare(O2, L2, Q, clean[0], clean[1], tables, lens, paths, q, sees, None)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(16, 1), (40, 1), (60, 2)])
+@pytest.mark.parametrize("own", [6, 21, 130, 259, 300])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_with_many_rows(D, Hq, Hkv, own, value):
+    """In the kernel for nodes that many rows read: one column of some drafts'
+    values is not finite.  Only that column, and only of the drafts that see one
+    of them, is touched; the rest of those drafts' values counts as it is."""
+    lens, paths, q = [150, own, 40], [[0, 1], [0, 2]], 6
+    up = np.array([[-1, -1, 0, 1, 2, 3], [-1, 0, 1, 2, 3, 4]])
+    sees = sees_of(up, q)
+    odd = [2, 5]  # drafts of sample 0
+
+    def slots(tables):
+        return OD.slots_of(tables[1], own, 16)[own - 6 + np.array(odd)]
+
+    def edit(Kc, Vc, tables):
+        for s in slots(tables):
+            Vc[s // 16, :, s % 16, 3] = value
+
+    O, L, Q, Kc, Vc, tables = attend(lens, paths, Hq, Hkv, D, BF, 16, q, up, None, width=4096, edit=edit)
+    clean = Vc.clone()
+    for s in slots(tables):
+        clean[s // 16, :, s % 16, 3] = 0.0
+    hit = torch.tensor([any(j in sees[s][i] for j in odd) and s == 0 for s in range(2) for i in range(q)])
+    assert not O[hit][:, :, 3].isfinite().any()
+    O2 = O.clone()
+    wo, _ = OT.attention(Q.float().numpy(), Kc.float().numpy(), clean.float().numpy(), tables, lens, paths, sees, q, [q, q])
+    O2[hit, :, 3] = torch.from_numpy(wo).to(BF)[hit, :, 3]
+    compare(O2, L, Q, Kc, clean, tables, lens, paths, q, sees, None)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq", [16, 40])
+def test_hidden_keys_with_many_rows(D, Hq):
+    """A key that is NaN makes the drafts that see it NaN, and no others."""
+    lens, paths, q = [150, 130, 40], [[0, 1], [0, 2]], 6
+    up = np.array([[-1, -1, 0, 1, 2, 3], [-1, 0, 1, 2, 3, 4]])
+    sees = sees_of(up, q)
+
+    def edit(Kc, Vc, tables):
+        s = OD.slots_of(tables[1], 130, 16)[126]
+        Kc[s // 16, :, s % 16] = float("nan")
+
+    O, L, Q, Kc, Vc, tables = attend(lens, paths, Hq, 1, D, BF, 16, q, up, None, width=4096, edit=edit)
+    hit = torch.tensor([s == 0 and 2 in sees[0][i] for s in range(2) for i in range(q)])
+    assert O[hit].isnan().all() and L[:, hit].isnan().all()
+    s = OD.slots_of(tables[1], 130, 16)[126]
+    clean = Kc.clone()
+    clean[s // 16, :, s % 16] = 0.0
+    wo, wl = OT.attention(Q.float().numpy(), clean.float().numpy(), Vc.float().numpy(), tables, lens, paths, sees, q, [q, q])
+    O[hit], L[:, hit] = torch.from_numpy(wo).to(BF)[hit], torch.from_numpy(wl).float()[:, hit]
+    compare(O, L, Q, clean, Vc, tables, lens, paths, q, sees, None)
 
 
 def test_attention_refuses_bad_masks():

@@ -248,6 +248,17 @@ def test_strides_and_alignment(dtype, pad, shift):
     assert wide.isnan().all()
 
 
+def test_gradient_beside_the_logits():
+    """Columns of one buffer: the logits, then their gradient."""
+    both = torch.full((9, 2 * 501 + 3), 7.0, dtype=BF, device="cuda")
+    x, d = both[:, 1:502], both[:, 503:1004]
+    x.copy_(logits(9, 501, BF, 3))
+    check(x, targets_of(9, 501, 3), out=d)
+    assert (both[:, [0, 502, 1004]] == 7.0).all()
+    with pytest.raises(pt.PTError, match="overlaps"):
+        check(x, targets_of(9, 501, 3), out=both[:, 500:1001])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("V", [11, 2000, 33000])
 @pytest.mark.parametrize("mixed", [False, True])
