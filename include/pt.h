@@ -670,6 +670,8 @@ pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, 
  * -inf) get the tokens' own part only.  dlogits may be logits (same stride) or
  * not overlap it.  Sums are fp32 in a fixed order, rounded once to dtype, so
  * both calls repeat bit for bit.
+ * A row's tokens are looked through once for every 16 bytes of the row that hold
+ * one of their targets: meant for a prompt's completions, up to some thousands.
  *
  * Any V up to 2^30, stride and alignment to the element (rows whose gradient
  * does not start as their logits do modulo 16 bytes are stored by elements).
