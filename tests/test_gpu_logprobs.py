@@ -179,6 +179,17 @@ def test_equal_and_ordered_logits(V, R, what):
         check(x.repeat(R, 1).to(dtype).cuda(), targets_of(R, V, 4), k=64, grad=False)
 
 
+@pytest.mark.parametrize("threads,V,R", [(128, 4096, 2), (128, 9000, 610), (480, 40000, 230), (480, 131072, 3)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_large_logits_in_few_threads(threads, V, R, ties):
+    """More candidates than the list has room for: every large logit is among the
+    elements of 63 threads (of a CTA of 128, or of the 480 that read)."""
+    v = torch.arange(V)
+    for dtype, slot in ((BF, 8), (F32, 4)):
+        x = ((v // slot) % threads < 63) * 4.0 + (0.0 if ties else ((v * 7) % 11) / 16)
+        check(x.repeat(R, 1).to(dtype).cuda(), targets_of(R, V, 4), k=64, grad=False)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("V", [5, 300, 20001])
 def test_infinities(dtype, V):
