@@ -100,9 +100,9 @@ struct alignas(sizeof(E) * V) RotVec {
 // turns them in every `lanes`-th head of one token, U heads in flight.  It holds
 // what it loaded until it stores, so Y may be X.
 // Bound by memory: 27687 tokens of 40 heads of 128 out of 48 (bf16, three axes, 568
-// MB) 94 us, 89% of the copy's bandwidth; 2048 tokens 6.9 us.  One head a thread 137
+// MB) 89 us, 94% of the copy's bandwidth; 2048 tokens 6.9 us.  One head a thread 137
 // us, two 128, four 97 (its angles' share grows); four heads in flight instead of two
-// 114 (registers, then CTAs).
+// 114 (registers, then CTAs), four CTAs an SM 106 (spills).
 template <class E, int V, bool NEAR, int U>
 __global__ void __launch_bounds__(V == 1 ? 512 : 256, V == 1 ? 2 : 3) k_rotary(const RotArgs a) {
   using Vec = RotVec<E, V>;
@@ -270,12 +270,14 @@ extern "C" pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, 
   a.T = T, a.H = H, a.D = D, a.half = half;
   a.inverse = inverse != 0;
   a.copy = !same && rot_dim < D;
-  // Eight heads a thread and about 256 threads a CTA; fewer heads where that leaves SMs idle (40 heads: one token 2.1 us,
-  // 3.3 with eight; 64 tokens 2.2 and 4.3; 2048 tokens 6.9 with eight, 9.0 with one).
+  // Eight heads a thread or a few more and 256 threads a CTA; fewer heads where that leaves SMs idle (40 heads: one token
+  // 2.1 us, 3.3 with eight; 64 tokens 2.2 and 4.3; 2048 tokens 6.9 with eight, 9.0 with one).
   const int per = half / (unit / es), sms = num_sms(dev);
   int each = 8;
   while (each > 1 && (long long)T * ((H + each - 1) / each) * per < 512ll * sms) each /= 2;
-  a.lanes = std::max(1, std::min((H + each - 1) / each, 256 / per));
+  const int most = std::max(1, std::min((H + each - 1) / each, 256 / per));
+  a.lanes = 1;  // (a power of two, so that warps are full: 40 heads in four lanes 89 us, in five 93)
+  while (2 * a.lanes <= most) a.lanes *= 2;
   a.tokens = std::max(1, 256 / (per * a.lanes));
   const int threads = per * a.lanes * a.tokens;
   const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
