@@ -587,10 +587,11 @@ pt_status pt_attn_decode(const void* Q, int64_t q_stride, const void* Kc, const 
  *   row's end.  Kc and Vc (one layer's cache) change in place; lens still counts
  *   all drafts, and pt_cache_tables takes the others back (added = accepted -
  *   q_count).  The places behind the accepted ones keep what they had.  q_len
- *   up to 256.  Errors: PT_ERR_INVALID_ARG as pt_cache_write, and for a plan in
- *   which two samples end at one node.  On the device, PT_ERR_INVALID_ARG, and
- *   the sample's rows stay as they are: numbers out of order or out of range, a
- *   length below q_count or above the table's, a page id outside [0, n_pages).
+ *   up to 256.  Errors: PT_ERR_INVALID_ARG as pt_cache_write, for caches that
+ *   overlap, and for a plan in which two samples end at one node.  On the
+ *   device, PT_ERR_INVALID_ARG, and the sample's rows stay as they are: numbers
+ *   out of order or out of range, a length below q_count or above the table's, a
+ *   page id outside [0, n_pages).
  * ------------------------------------------------------------------------- */
 pt_status pt_draft_tree(const int32_t* parents, const int32_t* lens, const int32_t* q_count, const int32_t* start,
                         const pt_decodeplan* plan, int32_t* mask, int64_t* positions, cudaStream_t stream);

@@ -348,6 +348,12 @@ extern "C" pt_status pt_cache_keep(const int32_t* kept, const int32_t* q_count, 
     set_error("%s: a pointer is not aligned to its elements", who);
     return PT_ERR_INVALID_ARG;
   }
+  const uintptr_t kc = reinterpret_cast<uintptr_t>(Kc), vc = reinterpret_cast<uintptr_t>(Vc);
+  const uintptr_t bytes = (uintptr_t)n_pages * plan->Hkv * page_size * D * es;
+  if (kc < vc + bytes && vc < kc + bytes) {  // (each of the two would move the other's)
+    set_error("%s: Kc and Vc overlap", who);
+    return PT_ERR_INVALID_ARG;
+  }
   int unit = 16;
   while (unit > es && (all & (uintptr_t)(unit - 1))) unit >>= 1;
   KeepArgs a;

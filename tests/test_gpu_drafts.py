@@ -423,6 +423,16 @@ def test_keep_refuses_samples_that_share_a_leaf():
         pt.cache_keep(i32([[0, -1], [0, -1]]), c, c.clone(), i32([[0, 1], [2, 3]]), i32([5, 5]), plan)
 
 
+def test_keep_refuses_caches_that_overlap():
+    plan = pt.decode_plan(1, *csr([[0]]), 2, 2, 4)
+    c = torch.zeros(7, 2, 16, 8, device="cuda")
+    for k, v in ((c[:3], c[:3]), (c[:3], c[2:5]), (c[1:4], c[:3])):
+        with pytest.raises(pt.PTError, match="overlap"):
+            pt.cache_keep(i32([[0, -1, -1, -1]]), k, v, i32([[0, 1, 2]]), i32([40]), plan)
+    pt.cache_keep(i32([[1, -1, -1, -1]]), c[:3], c[3:6], i32([[0, 1, 2]]), i32([40]), plan)
+    pt.sync_status()
+
+
 def test_binding_refusals():
     plan = pt.decode_plan(1, *csr([[0]]), 2, 2, 4)
     c, t, n, k = torch.zeros(3, 2, 16, 8, device="cuda"), i32([[0, 1, 2]]), i32([40]), i32([[0, -1, -1, -1]])
