@@ -264,11 +264,12 @@ __device__ __forceinline__ int bar_count(bool p) {  // how many of the N threads
 template <class E, int NT, bool TOP, bool CLERK, bool RING>
 __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (NT + 32 * CLERK)) k_score(const ScoreArgs a) {
   constexpr int V = Type<E>::V, U = 4, ALL = NT + 32 * CLERK;  // ALL: without the warp that loads
+  constexpr int CAND = NT == 32 ? kCandidates / 2 : kCandidates;  // (a warp's: 24 alternatives at most, and more CTAs an SM)
   __shared__ Stat sm_stat[NT / 32];
   __shared__ Stat sm_part;
   __shared__ unsigned sm_most[NT / 32], sm_least[NT / 32];
-  __shared__ unsigned long long sm_key[TOP ? kMaxTop : 1], sm_cand[TOP ? kCandidates : 1], sm_best[TOP ? kMaxTop : 1];
-  __shared__ int sm_who[TOP ? kCandidates : 1];  // groups: thread, and 2^16 times the group
+  __shared__ unsigned long long sm_key[TOP ? kMaxTop : 1], sm_cand[TOP ? CAND : 1], sm_best[TOP ? kMaxTop : 1];
+  __shared__ int sm_who[TOP ? CAND : 1];  // groups: thread, and 2^16 times the group
   __shared__ unsigned short sm_group[TOP ? kGroups : 1][TOP ? NT : 1];
   __shared__ int sm_n, sm_w, sm_e0, sm_e1;
   __shared__ uint64_t sm_full[RING ? kStages : 1], sm_empty[RING ? kStages : 1];
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
         for (int c = 0; c < min(chunks, kGroups); ++c)
           if (sm_group[c][tid] >= reach16) {
             const int at = atomicAdd(&sm_w, 1);
-            if (at < kCandidates) sm_who[at] = tid | c << 16;
+            if (at < CAND) sm_who[at] = tid | c << 16;
           }
       }
       sync();
@@ -602,13 +603,13 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
           const unsigned long long key = key_of(y[i], v);
           if (key >= bound && v >= 0 && v < a.V) {
             const int at = atomicAdd(&sm_n, 1);
-            if (at < kCandidates) sm_cand[at] = key;
+            if (at < CAND) sm_cand[at] = key;
           }
         }
       };
       // (a group: U slots of every kGroups-th round)
       const int rounds = (w1 - w0 + NT * U - 1) / (NT * U), reps = (rounds + kGroups - 1) / kGroups, listed = sm_w;
-      const int all = min(listed, kCandidates) * U * reps;
+      const int all = min(listed, CAND) * U * reps;
 #pragma unroll 1
       for (int x = tid; x < all; x += ALL) {
         const int y = x / U, i = reps == 1 ? y : y / reps, g = sm_who[i];
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
       if (edge >= 0) put(edge, row.pack(edge));
       sync();
       const int n = sm_n;
-      if (n <= kCandidates && listed <= kCandidates) {
+      if (n <= CAND && listed <= CAND) {
 #pragma unroll 1
         for (int i = tid; i < n; i += ALL) {
           const unsigned long long key = sm_cand[i];
@@ -972,6 +973,10 @@ extern "C" pt_status pt_token_logprobs(const void* logits, int64_t row_stride, p
   // and about 5000 more for the latencies of each round of CTAs.
   const int slots = (V + 16 / es - 1) / (16 / es), sms = num_sms(dev);
   const bool rows = slots <= 512 || (top_k ? R >= 4 * sms : slots <= 4096 && R >= 20 * sms);
+  // Few alternatives of many short rows: a warp a row (1300 x 1000 with 5 7.5 us and with
+  // 20 12.3, four warps 11.4 and 14.1; 14000 x 1000 28 and 51, four warps 71 and 86; but
+  // 800 x 1000 with 20 11.3 and 8.9: eight CTAs of four warps stay on an SM).
+  const bool warps = rows && top_k <= 24 && slots <= 512 && R >= 8 * sms;
   const int per_sm = top_k ? 2 : 3;  // of the undivided rows' CTAs
   int parts = 1;
   if (!rows) {
@@ -998,6 +1003,7 @@ extern "C" pt_status pt_token_logprobs(const void* logits, int64_t row_stride, p
     };
     auto pick = [&](auto type) {
       using E = decltype(type);
+      if (top_k && warps) return go(k_score<E, 32, true, false, false>, 32, 24);
       if (top_k) return rows ? go(k_score<E, 128, true, false, false>, 128, 8) : go(k_score<E, 480, true, true, false>, 512, 2);
       if (rows) return go(k_score<E, 32, false, false, false>, 32, 32);
       return parts == 1 ? go(k_score<E, 256, false, true, true>, 320, 3) : go(k_score<E, 480, false, true, false>, 512, 2);

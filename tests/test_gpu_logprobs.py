@@ -179,6 +179,24 @@ def test_equal_and_ordered_logits(V, R, what):
         check(x.repeat(R, 1).to(dtype).cuda(), targets_of(R, V, 4), k=64, grad=False)
 
 
+@pytest.mark.parametrize("V", [2, 26, 103, 300, 1001, 4000])
+@pytest.mark.parametrize("k", [1, 5, 24])
+def test_alternatives_of_many_short_rows(V, k):
+    """A warp a row."""
+    for dtype in (BF, F32):
+        check(logits(1300, V, dtype, V), targets_of(1300, V, 3), k=min(k, V), grad=False)
+
+
+@pytest.mark.parametrize("V", [30, 999, 4096])
+@pytest.mark.parametrize("what", ["equal", "two values", "falling", "few threads", "nothing", "one", "lowest"])
+def test_equal_and_masked_logits_in_a_warp(V, what):
+    v = torch.arange(V)
+    for dtype, slot in ((BF, 8), (F32, 4)):
+        x = {"equal": torch.ones(V), "two values": (v % 3 == 1).float(), "falling": -v.float() / 256, "few threads": ((v // slot) % 32 < 20) * 4.0,
+             "nothing": torch.full((V,), -INF), "one": torch.where(v == V - 1, 1.0, -INF), "lowest": torch.full((V,), torch.finfo(dtype).min)}[what]
+        check(x.repeat(1300, 1).to(dtype).cuda(), targets_of(1300, V, 4), k=24, grad=False)
+
+
 @pytest.mark.parametrize("threads,V,R", [(128, 4096, 2), (128, 9000, 610), (480, 40000, 230), (480, 131072, 3)])
 @pytest.mark.parametrize("ties", [False, True])
 def test_large_logits_in_few_threads(threads, V, R, ties):
