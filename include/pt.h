@@ -651,9 +651,11 @@ pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, 
  * targets [N] (device int64): token ids; a negative one is not scored (logp 0,
  * no gradient).  Row r scores tokens index[row_ptr[r]] .. index[row_ptr[r + 1] -
  * 1] (device int32; index NULL: the entries' own numbers; row_ptr NULL: token r,
- * N = R).  The entries from row_ptr[R] on belong to no row: logp 0.  logp [N],
- * LSE [R], entropy [R] (or NULL): fp32.  An index that names a token twice gets
- * one of the two rows' logp.
+ * N = R).  The entries before row_ptr[0] and from row_ptr[R] on belong to no row:
+ * logp 0.  logp [N],
+ * LSE [R], entropy [R] (or NULL): fp32.  index names every token once: one that
+ * it names twice gets one of the two rows' logp (not always the same one's; the
+ * gradient has both), and one that it does not name keeps what logp held.
  * top_k > 0: top_ids [R, top_k] (int64) and top_logp [R, top_k] (fp32) are the
  * largest logits' tokens, descending, equal ones by the lower id.
  * Infinities: a logit of -inf is a token that cannot be chosen; a row of nothing
@@ -670,7 +672,7 @@ pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, 
  * be NULL without dentropy).  Every row is written; rows without weight (LSE =
  * -inf) get the tokens' own part only.  dlogits may be logits (same stride) or
  * not overlap it.  Sums are fp32 in a fixed order, rounded once to dtype, so
- * both calls repeat bit for bit.
+ * both calls repeat bit for bit (with an index that names every token once).
  * A row's tokens are looked through once for every 16 bytes of the row that hold
  * one of their targets: meant for a prompt's completions, up to some thousands.
  *
@@ -678,8 +680,8 @@ pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, 
  * does not start as their logits do modulo 16 bytes are stored by elements).
  * Errors: PT_ERR_INVALID_ARG for a bad dtype, sizes (V < 1, N != R without
  * row_ptr), strides, a scale outside [1e-30, 1e30], top_k outside [0, V],
- * overlap or NULL pointers; PT_ERR_UNSUPPORTED for top_k above 64, V above 2^30
- * or R above 2^28 - 1.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a
+ * overlap or NULL pointers; PT_ERR_UNSUPPORTED for top_k above 64, V or N above
+ * 2^30 or R above 2^28 - 1.  On the device (pt_sync_status), PT_ERR_INVALID_ARG: a
  * target of V or more (not scored), a row_ptr that decreases or passes N (the
  * row scores nothing), an index outside [0, N) (passed over).
  * ------------------------------------------------------------------------- */

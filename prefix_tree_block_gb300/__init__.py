@@ -953,8 +953,8 @@ def token_logprobs(logits, targets, row_ptr=None, index=None, top_k: int = 0, en
                    scale: float = 1.0, stream=None) -> Tuple:
     """Log probabilities of given tokens (pt_token_logprobs): logits [R, V],
     targets int64 [N] (negative: not scored).  Row r scores token r, or tokens
-    index[row_ptr[r]:row_ptr[r + 1]] (int32; FoldPlan.successors gives both for a
-    tree).  Returns logp [N], LSE [R], entropy [R] or None, and the top_k most
+    index[row_ptr[r]:row_ptr[r + 1]] (int32, every token once; FoldPlan.successors
+    gives both for a tree).  Returns logp [N], LSE [R], entropy [R] or None, and the top_k most
     likely tokens' log probabilities and ids [R, top_k] or None."""
     _, _, i64, f32, _, _, device = _torch()
     dev = device() if logits.is_cuda else -1

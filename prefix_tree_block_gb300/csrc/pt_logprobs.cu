@@ -710,8 +710,10 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
       put_logp(tok, target, target >= 0 ? Type<E>::f(row.x[target]) : 0.f);
     }
     if (r == a.e.R - 1 && a.e.row_ptr) {  // entries of no row
-      const int end = min(max(a.e.row_ptr[a.e.R], 0), a.e.N);
-      for (int n = end + tid; n < a.e.N; n += ALL) {
+      const int first_e = min(max(a.e.row_ptr[0], 0), a.e.N), end = min(max(a.e.row_ptr[a.e.R], first_e), a.e.N);
+      for (int n = tid; n < a.e.N; n += ALL) {
+        if (n >= first_e && n < end) n += (end - n + ALL - 1) / ALL * ALL;
+        if (n >= a.e.N) break;
         const int tok = a.e.token(n);
         if (tok >= 0) a.logp[tok] = 0.f;
       }
@@ -901,8 +903,8 @@ pt_status check(const char* who, pt_dtype dtype, int R, int V, int N, int64_t st
     set_error("%s: %d rows of %d logits or %d tokens out of range", who, R, V, N);
     return PT_ERR_INVALID_ARG;
   }
-  if (V > 1 << 30 || R > INT_MAX / kMaxParts) {
-    set_error("%s: %d rows of %d logits are out of range", who, R, V);
+  if (V > 1 << 30 || N > 1 << 30 || R > INT_MAX / kMaxParts) {
+    set_error("%s: %d rows of %d logits or %d tokens are more than supported", who, R, V, N);
     return PT_ERR_UNSUPPORTED;
   }
   if (stride < V) {

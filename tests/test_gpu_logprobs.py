@@ -305,6 +305,16 @@ def test_rows_with_any_number_of_tokens(dtype, V, mixed):
     check(logits(len(per), V, dtype, 8), t.tolist(), row_ptr=ptr.tolist(), index=None if index is None else index.tolist(), k=3)
 
 
+@pytest.mark.parametrize("V,R", [(50, 4), (50, 2000), (40000, 3)])
+@pytest.mark.parametrize("before,behind", [(1, 0), (700, 0), (45, 1300)])
+def test_entries_of_no_row(V, R, before, behind):
+    ptr = before + np.arange(R + 1)
+    N = int(ptr[-1]) + behind
+    x, t = logits(R, V, BF, 8), targets_of(N, V, 3)
+    check(x, t, row_ptr=ptr.tolist(), k=2)
+    check(x, t, row_ptr=ptr.tolist(), index=np.random.default_rng(1).permutation(N).tolist(), grad=False)
+
+
 def test_nothing():
     x = torch.zeros(0, 9, device="cuda")
     none = torch.zeros(0, dtype=torch.int64, device="cuda")

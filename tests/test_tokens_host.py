@@ -59,7 +59,7 @@ def _score(lib, **kw):
 BOTH = [(dict(x=None), INV), (dict(lse=None), INV), (dict(targets=None), INV), (dict(dt=7), INV), (dict(R=-1), INV),
         (dict(V=0), INV), (dict(N=-1), INV), (dict(N=2), INV), (dict(stride=99), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV),
         (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(scale=1e-31), INV), (dict(scale=1.1e30), INV),
-        (dict(V=(1 << 30) + 1, stride=1 << 31), UNS), (dict(R=1 << 28, N=1 << 28), UNS), (dict(x=P + 1), INV)]
+        (dict(V=(1 << 30) + 1, stride=1 << 31), UNS), (dict(R=1 << 28, N=1 << 28), UNS), (dict(N=(1 << 30) + 1, row_ptr=P), UNS), (dict(x=P + 1), INV)]
 
 
 @pytest.mark.parametrize("kw,want", BOTH + [
