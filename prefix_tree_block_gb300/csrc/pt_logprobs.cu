@@ -215,6 +215,39 @@ struct ScoreArgs {
   long long* ids;
 };
 
+// A warp takes from n listed keys those that reach no less than the k-th largest
+// value, by halving, to the list's front; returns their number.  (14000 x 150 with 20
+// 65 us, all of the row ranked 126.)
+__device__ __noinline__ int prune(unsigned long long* list, int n, int k, unsigned lo) {
+  const int lane = threadIdx.x & 31;
+  unsigned top = 0;
+  for (int i = lane; i < n; i += 32) top = max(top, (unsigned)(list[i] >> 32));
+  unsigned hi = __reduce_max_sync(0xffffffffu, top) + 1;
+  int c = n;
+#pragma unroll 1
+  while (hi - lo > 1 && c > k + 8) {
+    const unsigned mid = lo + ((hi - lo) >> 1);
+    int m = 0;
+    for (int i = lane; i < n; i += 32) m += (unsigned)(list[i] >> 32) >= mid;
+    m = __reduce_add_sync(0xffffffffu, m);
+    if (m >= k)
+      lo = mid, c = m;
+    else
+      hi = mid;
+  }
+  c = 0;
+#pragma unroll 1
+  for (int i = lane; i - lane < n; i += 32) {  // (in place: none moves up)
+    const unsigned long long key = i < n ? list[i] : 0ull;
+    const bool keep = i < n && (unsigned)(key >> 32) >= lo;
+    const unsigned kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) list[c + __popc(kept & ((1u << lane) - 1u))] = key;
+    c += __popc(kept);
+    __syncwarp();
+  }
+  return c;
+}
+
 // ---------------------------------------------------------------------------
 // Scores: one pass over the logits.  A row is one CTA's, or a cluster's that
 // shares it where rows are few; a thread takes every NT-th 16 bytes, U of them
@@ -262,9 +295,9 @@ __device__ __forceinline__ int bar_count(bool p) {  // how many of the N threads
 }
 
 template <class E, int NT, bool TOP, bool CLERK, bool RING>
-__global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (NT + 32 * CLERK)) k_score(const ScoreArgs a) {
+__global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 && TOP ? 24 : 1024 / (NT + 32 * CLERK)) k_score(const ScoreArgs a) {
   constexpr int V = Type<E>::V, U = 4, ALL = NT + 32 * CLERK;  // ALL: without the warp that loads
-  constexpr int CAND = NT == 32 ? kCandidates / 2 : kCandidates;  // (a warp's: 24 alternatives at most, and more CTAs an SM)
+  constexpr int CAND = NT == 32 ? kCandidates / 2 : kCandidates;  // (a warp's: more CTAs on an SM)
   __shared__ Stat sm_stat[NT / 32];
   __shared__ Stat sm_part;
   __shared__ unsigned sm_most[NT / 32], sm_least[NT / 32];
@@ -527,7 +560,8 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
       for (int w = 0; w < NT / 32; ++w) lo = min(lo, sm_least[w]), hi = max(hi, sm_most[w]);
       ++hi;  // (a value's order is below 2^32 - 1)
       int reach = count(mine >= lo);  // threads that reach lo: k at least (with lo = 0 all)
-      const bool far = reach > 2 * k + 32 || lo == 0;  // (0: a warp without q threads that hold any)
+      // (0: a warp without q threads that hold any; fewer than k in all: everything is listed)
+      const bool far = lo ? reach > 2 * k + 32 : count(mine > 0) >= k;
 #pragma unroll 1
       while (far && hi - lo > 1 && reach > k + 8) {
         const unsigned mid = lo + ((hi - lo) >> 1);
@@ -618,8 +652,10 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : 1024 / (N
       }
       if (edge >= 0) put(edge, row.pack(edge));
       sync();
-      const int n = sm_n;
+      int n = sm_n;
       if (n <= CAND && listed <= CAND) {
+        if constexpr (NT == 32)  // (a row of fewer slots than k, mostly: fewer of them, for the ranking's n^2)
+          if (n > 2 * k && n > 45) n = prune(sm_cand, n, k, (unsigned)(bound >> 32));
 #pragma unroll 1
         for (int i = tid; i < n; i += ALL) {
           const unsigned long long key = sm_cand[i];
@@ -975,10 +1011,12 @@ extern "C" pt_status pt_token_logprobs(const void* logits, int64_t row_stride, p
   // and about 5000 more for the latencies of each round of CTAs.
   const int slots = (V + 16 / es - 1) / (16 / es), sms = num_sms(dev);
   const bool rows = slots <= 512 || (top_k ? R >= 4 * sms : slots <= 4096 && R >= 20 * sms);
-  // Few alternatives of many short rows: a warp a row (1300 x 1000 with 5 7.5 us and with
-  // 20 12.3, four warps 11.4 and 14.1; 14000 x 1000 28 and 51, four warps 71 and 86; but
-  // 800 x 1000 with 20 11.3 and 8.9: eight CTAs of four warps stay on an SM).
-  const bool warps = rows && top_k <= 24 && slots <= 512 && R >= 8 * sms;
+  // Few alternatives of many short rows, or rows that a warp's list holds whole: a
+  // warp a row (1300 x 1000 with 5 7.5 us and with 20 12.3, four warps 11.4 and 14.1;
+  // 14000 x 1000 28 and 48, four warps 71 and 86; 14000 x 300 with 50 96 and 338; but
+  // 14000 x 4000 with 32 133 and 119, 800 x 1000 with 20 11.3 and 8.9: eight CTAs of
+  // four warps stay on an SM).
+  const bool warps = rows && (top_k <= 24 || V <= kCandidates / 2) && slots <= 512 && R >= 8 * sms;
   const int per_sm = top_k ? 2 : 3;  // of the undivided rows' CTAs
   int parts = 1;
   if (!rows) {

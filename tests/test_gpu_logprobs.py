@@ -187,6 +187,16 @@ def test_alternatives_of_many_short_rows(V, k):
         check(logits(1300, V, dtype, V), targets_of(1300, V, 3), k=min(k, V), grad=False)
 
 
+@pytest.mark.parametrize("V", [31, 150, 301, 512, 513])
+@pytest.mark.parametrize("k", [24, 33, 64])
+@pytest.mark.parametrize("values", [2, 40, 0])
+def test_short_rows_listed_whole(V, k, values):
+    """Fewer slots than alternatives: all are listed, and the list cut (few values: equal ones at the cut)."""
+    for dtype in (BF, F32):
+        x = logits(1300, V, dtype, V)
+        check((x * 7).round().remainder(values) if values else x, targets_of(1300, V, 3), k=min(k, V), grad=False)
+
+
 @pytest.mark.parametrize("V", [30, 999, 4096])
 @pytest.mark.parametrize("what", ["equal", "two values", "falling", "few threads", "nothing", "one", "lowest"])
 def test_equal_and_masked_logits_in_a_warp(V, what):
