@@ -661,9 +661,11 @@ pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, 
  * Infinities: a logit of -inf is a token that cannot be chosen; a row of nothing
  * else has LSE = -inf, entropy 0 and logp -inf.  A row with a NaN or +inf has
  * LSE, entropy and logp NaN (a NaN counts as -inf among the alternatives).
- * logp is taken from the row's maximum, so large logits cost it nothing; LSE
- * is one fp32 number, and what it was rounded by (2^-24 of it) is an error of
- * every ln p in the backward.
+ * logp and entropy are taken from the row's maximum, so large logits cost them
+ * nothing; LSE is one fp32 number.  The backward takes ln p from it while |LSE| is
+ * below 256, where its rounding costs ln p less than 2^-17; a row beyond that
+ * (masked with a large negative number, say) is looked through for its maximum
+ * and sum again, by one CTA, so that its gradient is that of logp and entropy too.
  *
  * pt_token_logprobs_bwd: dlogits [R, V] (dtype; rows d_stride elements apart) =
  * scale * (sum over the row's tokens of dlogp[t] (1[v = targets[t]] - p) -

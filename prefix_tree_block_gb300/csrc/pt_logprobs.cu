@@ -782,9 +782,117 @@ struct GradArgs {
 // part (3.7 GB) 549 us, the copy's rate; 1000 x 50001 in fp32 64 us, 92%.
 // ---------------------------------------------------------------------------
 constexpr int kSlotBits = 4096;
+// From this |LSE| on, z - LSE has lost too much to LSE's rounding (2^-17 of p there,
+// 2^-24 |LSE| in general; all of ln S in a row masked with -1e9), and the row's
+// maximum and sum are computed again.  Logits whose LSE is that large come from
+// masks and broken scales, so the second look costs ordinary rows nothing.
+constexpr float kFarLse = 256.f;
+
+// Adds a slot's scored tokens' gradients, in the entries' order.
+template <class E>
+__device__ __forceinline__ void add_entries(const GradArgs& a, const Row<E>& row, const unsigned* bits, int e0, int e1,
+                                            int s, float (&y)[Type<E>::V]) {
+  constexpr int V = Type<E>::V;
+  if (!(bits[(s & (kSlotBits - 1)) >> 5] >> (s & 31) & 1u)) return;
+#pragma unroll 1
+  for (int n = e0; n < e1; ++n) {
+    const int tok = a.e.token(n), target = a.e.target(tok, a.V);
+    if (target < 0) continue;
+    const int i = target + row.lead - s * V;
+    if (i < 0 || i >= V) continue;
+    const float g = a.g[tok] * a.scale;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (k == i) y[k] += g;
+  }
+}
+
+// Stores a slot of the gradient at out, the row's start: whole where its 16 bytes are
+// the row's own and aligned, else by elements.
+template <class E>
+__device__ __forceinline__ void store_slot(E* out, const Row<E>& row, int s, bool whole, const float (&y)[Type<E>::V]) {
+  constexpr int V = Type<E>::V;
+  if (whole) {
+    uint4 w;
+    if constexpr (sizeof(E) == 2)
+      w = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    else
+      w = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+    *reinterpret_cast<uint4*>(out + ((long long)s * V - row.lead)) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = s * V - row.lead + i;
+    if (v >= 0 && v < row.n) {
+      if constexpr (sizeof(E) == 2)
+        out[v] = __float2bfloat16_rn(y[i]);
+      else
+        out[v] = y[i];
+    }
+  }
+}
+
+// A whole row of k_grad by one CTA, ln p = (x - m) scale - ln S with m and S from the
+// row itself (three looks at it).  The other CTAs of the row leave it alone, since
+// the gradient may take the logits' place.  Bound by latency: one row of 131072 in bf16
+// 84 us (2.5 by all of its CTAs on the near path), 4000 x 65536 365 us (157).
+template <class E, int NT, bool ENT, bool VEC>
+__device__ __noinline__ void far_row(const GradArgs& a, int r, const unsigned* bits, float* sm, int e0, int e1, float ca,
+                                     float cb) {
+  constexpr int V = Type<E>::V;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Row<E> row(static_cast<const E*>(a.x) + (long long)r * a.stride, a.V);
+  E* out = static_cast<E*>(a.d) + (long long)r * a.d_stride;
+  const int slots = row.slots();
+  const float c1 = a.scale * 1.4426950408889634f;
+  float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+  for (int at = tid; at < slots; at += NT) {
+    float y[V];
+    row.get(at, y);
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, y[i]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  __syncthreads();  // (sm has been read)
+  if (lane == 0) sm[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, sm[w]);
+#pragma unroll 1
+  for (int at = tid; at < slots; at += NT) {
+    float y[V];
+    row.get(at, y);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s += ex2((y[i] - m) * c1);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  __syncthreads();
+  if (lane == 0) sm[warp] = s;
+  __syncthreads();
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) s += sm[w];
+  const float ln_s = logf(s);
+#pragma unroll 1
+  for (int at = tid; at < slots; at += NT) {
+    float y[V];
+    row.get(at, y);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float l = fmaxf(fmaf(y[i] - m, a.scale, -ln_s), -1000.f);
+      y[i] = ex2(l * 1.4426950408889634f) * (ENT ? fmaf(cb, l, ca) : ca);
+    }
+    add_entries<E>(a, row, bits, e0, e1, at, y);
+    store_slot<E>(out, row, at, VEC && row.whole(at), y);
+  }
+}
 
 template <class E, int NT, bool ENT, bool VEC>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const GradArgs a) {
+__global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const __grid_constant__ GradArgs a) {
   constexpr int V = Type<E>::V, U = VEC ? 4 : 1;
   __shared__ unsigned bits[kSlotBits / 32];
   __shared__ float sm_g[NT / 32];
@@ -805,6 +913,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const GradArgs a) {
   int e0, e1;
   a.e.range(r, e0, e1);
   float lse = a.lse[r];
+  const bool far = fabsf(lse) >= kFarLse && lse != -INFINITY;
   const float dh = ENT ? a.dH[r] * a.scale : 0.f, H = ENT ? a.H[r] : 0.f;
   if (lse == -INFINITY) lse = INFINITY;  // a row without a weight: every p is 0
   for (int i = tid; i < kSlotBits / 32; i += NT) bits[i] = 0;
@@ -827,37 +936,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const GradArgs a) {
   for (int w = 0; w < NT / 32; ++w) sum += sm_g[w];
   // d = p (ca + cb ln p) + scale * g of the entries
   const float ca = lse != lse ? lse : -(sum * a.scale + dh * H), cb = -dh;
+  if (far) {
+    if (part == 0) far_row<E, NT, ENT, VEC>(a, r, bits, sm_g, e0, e1, ca, cb);
+    return;
+  }
   auto one = [&](float x) {
     const float l = fmaxf(fmaf(x, a.scale, -lse), -1000.f);  // ln p (p is 0 from -104 on: its product with ln p too)
     const float p = ex2(l * 1.4426950408889634f);
     return p * (ENT ? fmaf(cb, l, ca) : ca);
   };
-  auto entries = [&](int s, float (&y)[V]) {
-    if (!(bits[(s & (kSlotBits - 1)) >> 5] >> (s & 31) & 1u)) return;
-#pragma unroll 1
-    for (int n = e0; n < e1; ++n) {
-      const int tok = a.e.token(n), target = a.e.target(tok, a.V);
-      if (target < 0) continue;
-      const int i = target + row.lead - s * V;
-      if (i < 0 || i >= V) continue;
-      const float g = a.g[tok] * a.scale;
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (k == i) y[k] += g;
-    }
-  };
-  auto store_some = [&](int s, const float (&y)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = s * V - row.lead + i;
-      if (v >= 0 && v < a.V) {
-        if constexpr (sizeof(E) == 2)
-          out[v] = __float2bfloat16_rn(y[i]);
-        else
-          out[v] = y[i];
-      }
-    }
-  };
+  auto entries = [&](int s, float (&y)[V]) { add_entries<E>(a, row, bits, e0, e1, s, y); };
 #pragma unroll 1
   for (int s = s0 + tid; s < s1; s += NT * U) {
     if (s != s0 + tid) fetch(s);
@@ -879,16 +967,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_grad(const GradArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = one(y[i]);
       entries(at, y);
-      if (VEC && whole) {
-        uint4 w;
-        if constexpr (sizeof(E) == 2)
-          w = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        else
-          w = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
-        *reinterpret_cast<uint4*>(out + ((long long)at * V - row.lead)) = w;
-      } else {
-        store_some(at, y);
-      }
+      store_slot<E>(out, row, at, VEC && whole, y);
     }
   }
 }
