@@ -661,6 +661,8 @@ pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, int32_t T, 
  * Infinities: a logit of -inf is a token that cannot be chosen; a row of nothing
  * else has LSE = -inf, entropy 0 and logp -inf.  A row with a NaN or +inf has
  * LSE, entropy and logp NaN (a NaN counts as -inf among the alternatives).
+ * Where scale times the largest logit is beyond fp32, LSE is the nearest finite
+ * number, and all else is as in any other row.
  * logp and entropy are taken from the row's maximum, so large logits cost them
  * nothing; LSE is one fp32 number.  The backward takes ln p from it while |LSE| is
  * below 256, where its rounding costs ln p less than 2^-17; a row beyond that

@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -719,15 +720,16 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 
     sync();
     st = sm_part;
     // the row's results
-    const float z = st.m * a.scale;  // (S is at least 1)
-    const float ln_s = st.m == -INFINITY ? 0.f : logf(st.s);
-    const float lse = st.s != st.s ? st.s : st.m == -INFINITY ? -INFINITY : z + ln_s;
+    // (a row without weight is one whose largest logit is -inf; that z is beyond fp32 says nothing about its weights)
+    const bool none = st.m == -INFINITY && st.s == st.s;
+    const float ln_s = st.m == -INFINITY ? 0.f : logf(st.s);  // (S is at least 1)
     if (tid == 0) {
-      a.lse[r] = lse;
-      if (a.H) a.H[r] = st.m == -INFINITY && st.s == st.s ? 0.f : ln_s - 0.69314718055994531f * (st.t / st.s);
+      const float lse = fminf(fmaxf(st.m * a.scale + ln_s, -FLT_MAX), FLT_MAX);
+      a.lse[r] = st.s != st.s ? st.s : none ? -INFINITY : lse;
+      if (a.H) a.H[r] = none ? 0.f : ln_s - 0.69314718055994531f * (st.t / st.s);
     }
     // (from m, not from LSE: large logits then lose nothing)
-    auto log_p = [&](float x) { return lse == -INFINITY ? -INFINITY : (x - st.m) * a.scale - ln_s; };
+    auto log_p = [&](float x) { return none ? -INFINITY : (x - st.m) * a.scale - ln_s; };
     if constexpr (TOP) {
       const unsigned long long* best = a.lparts > 0 ? sm_key : sm_best;
       for (int i = tid; i < a.k; i += ALL) {
