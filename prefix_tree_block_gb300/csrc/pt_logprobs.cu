@@ -249,6 +249,66 @@ __device__ __noinline__ int prune(unsigned long long* list, int n, int k, unsign
   return c;
 }
 
+// The alternatives' second look at slots [s0, s1) of a row, where many logits tie and
+// the first one listed too many: a thread keeps its largest key (of equal logits
+// the first), the bound is the k-th largest of them by halving, and the elements
+// that reach it are listed; returns their number, which is above `cap` where few
+// threads hold many large ones.  Two passes from L2, where a search for each
+// alternative takes k.
+template <class E, int ALL>
+__device__ __noinline__ int list_again(Row<E> row, int s0, int s1, int k, unsigned long long* list, int cap, int* count) {
+  constexpr int V = Type<E>::V;
+  const int tid = threadIdx.x;
+  auto look = [&](auto use) {  // use(slot, its elements, their largest)
+#pragma unroll 1
+    for (int s = s0 + tid; s < s1; s += ALL) {
+      float y[V];
+      row.get(s, y);
+      float m = y[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) m = fmaxf(m, y[i]);
+      use(s, y, m);
+    }
+  };
+  float top = -INFINITY;
+  int at = -1;
+  look([&](int s, const float (&y)[V], float m) {
+    if (at >= 0 && !(m > top)) return;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) {
+      const int v = s * V - row.lead + i;
+      if (v >= 0 && v < row.n && ordered(y[i]) == ordered(m)) at = v;
+    }
+    top = fmaxf(top, m);
+  });
+  const unsigned long long best = at < 0 ? 0ull : key_of(top, at);
+  if (tid == 0) *count = 0;
+  unsigned long long lo = 0, hi = ~0ull;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const unsigned long long mid = lo + ((hi - lo) >> 1);
+    if (__syncthreads_count(best >= mid) >= k)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const float least = value_of(lo);  // (of 0: NaN, which nothing is below)
+  look([&](int s, const float (&y)[V], float m) {
+    if (m < least) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = s * V - row.lead + i;
+      const unsigned long long key = key_of(y[i], v);
+      if (v >= 0 && v < row.n && key >= lo) {
+        const int x = atomicAdd(count, 1);
+        if (x < cap) list[x] = key;
+      }
+    }
+  });
+  __syncthreads();
+  return *count;
+}
+
 // ---------------------------------------------------------------------------
 // Scores: one pass over the logits.  A row is one CTA's, or a cluster's that
 // shares it where rows are few; a thread takes every NT-th 16 bytes, U of them
@@ -271,8 +331,11 @@ __device__ __noinline__ int prune(unsigned long long* list, int n, int k, unsign
 // (from L2), their elements at or above it listed, and the list ranked.  Where
 // many more threads reach the bound it is raised by halving, and equal maxima are
 // told apart by their first index, so that a row of equal logits lists few of
-// them.  A list that overflows all the same (many large elements in few threads)
-// is replaced by k searches through the part.
+// them.  CTAs of one warp or four have too few threads to tell that from; a list
+// that overflows there is made again with such a bound (1300 x 4096 equal logits
+// with 24 51 us, by searches 283, random ones 16; 700 x 30001 with 64 99, 1932, 24).  One that
+// overflows all the same (many large elements in few threads) is replaced by k
+// searches through the part.
 //
 // Bound by memory and, in bf16, nearly by issue: per element half an instruction
 // each for the maximum, the clamp, the exponent and the two sums, one each to
@@ -630,7 +693,7 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 
         float top = y[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) top = fmaxf(top, y[i]);
-        if (top < least) return;  // most slots (a NaN passes on)
+        if (top < least || *(volatile int*)&sm_n > CAND) return;  // most slots (a NaN passes on); a list that overflows is no use
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           if (y[i] < least) continue;
@@ -644,7 +707,7 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 
       };
       // (a group: U slots of every kGroups-th round)
       const int rounds = (w1 - w0 + NT * U - 1) / (NT * U), reps = (rounds + kGroups - 1) / kGroups, listed = sm_w;
-      const int all = min(listed, CAND) * U * reps;
+      const int all = listed > CAND ? 0 : listed * U * reps;
 #pragma unroll 1
       for (int x = tid; x < all; x += ALL) {
         const int y = x / U, i = reps == 1 ? y : y / reps, g = sm_who[i];
@@ -653,10 +716,14 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 
       }
       if (edge >= 0) put(edge, row.pack(edge));
       sync();
-      int n = sm_n;
-      if (n <= CAND && listed <= CAND) {
+      int n = listed <= CAND ? sm_n : CAND + 1;
+      if (n > CAND && !far) {
+        sync();  // (all have read sm_n)
+        n = list_again<E, ALL>(row, s0, s1, k, sm_cand, CAND, &sm_n);
+      }
+      if (n <= CAND) {
         if constexpr (NT == 32)  // (a row of fewer slots than k, mostly: fewer of them, for the ranking's n^2)
-          if (n > 2 * k && n > 45) n = prune(sm_cand, n, k, (unsigned)(bound >> 32));
+          if (n > 2 * k && n > 45) n = prune(sm_cand, n, k, (unsigned)(bound >> 32));  // (the bound of the first look will do)
 #pragma unroll 1
         for (int i = tid; i < n; i += ALL) {
           const unsigned long long key = sm_cand[i];
