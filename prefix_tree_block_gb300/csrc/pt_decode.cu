@@ -64,22 +64,22 @@ template <class E, int DL, int VEC, bool TREE>
 __global__ void __launch_bounds__(256, DL >= 16 ? 1 : 2) k_decode_simt(const DecArgs a, const DecClass c) {
   pdl_wait();
   extern __shared__ int chunk[];
-  dec_scan(a, c, c, kSimt, kSimt, chunk, nullptr, nullptr);
+  dec_scan(a, TREE, c, c, kSimt, kSimt, chunk, nullptr, nullptr);
   const int per = dec_share(chunk[(c.nseg + 31) >> 5], a.workers, a.min_units);
-  if (blockIdx.x == gridDim.x - 1) dec_publish(a, c, kSimt, chunk, per);
+  if (blockIdx.x == gridDim.x - 1) dec_publish(a, TREE, c, kSimt, chunk, per);
   const int lane = threadIdx.x & 31;
   constexpr int R = kSimtR, NV = DL / VEC;
   constexpr int STEP = DL <= 4 ? 8 : 4;  // tokens, as registers allow
   constexpr bool EARLY = DL <= 4;        // and whether for their values beside their keys
   using V = VecOf<E, VEC>;
   const E* Qp = static_cast<const E*>(a.Q);
-  DecWalk walk(a, c, kSimt, chunk, (int)blockIdx.x * 8 + (threadIdx.x >> 5), per);
+  DecWalk walk(a, TREE, c, kSimt, chunk, (int)blockIdx.x * 8 + (threadIdx.x >> 5), per);
   DecPiece p;
   const int my_r = lane >> 3;  // the row whose scores this lane holds
 #pragma unroll 1
   while (walk.next(p)) {
     int b, e;
-    dec_range(a, p.kind, p.len, b, e);
+    dec_range(a, TREE, p.kind, p.len, b, e);
     float q[R][DL], acc[R][DL];
     int lim_max = 0, lim_min = INT_MAX, my_lim = 0;  // (the least of the rows there are)
     int lim[R];
@@ -284,12 +284,12 @@ __device__ __forceinline__ void merge_pieces(const MergeArgs& m, int node, const
     const int rl = mine ? kTile.r : m.g0.r, bl = mine ? kTile.t : m.g0.t;
     const int before = pref[node], per = pref[m.c0.nseg];
     int b, e;
-    dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
+    dec_range(a, a.mask, sg.kind(), dec_clamp(a, raw), b, e);
     const int tiles = (e - b + (1 << bl) - 1) >> bl;
     if (tiles > 0) {
       const int row = (mem * a.q_len + j) * a.g + h0, rt = row >> rl, it = rt * a.Hkv + hk;
       two = mine && sg.rows() - (rt << rl) <= kTileR / 2;
-      const int nu = dec_line(DecTiling{rl, bl, mine ? dec_tile(a).k : m.g0.k}, sg.rows(), tiles);
+      const int nu = dec_line(DecTiling{rl, bl, mine ? dec_tile(a.mask).k : m.g0.k}, sg.rows(), tiles);
       const unsigned u0 = before + it * nu, w0 = u0 / (unsigned)per, w1 = (u0 + nu - 1) / (unsigned)per;
       row0 = (((int)w0 + sg.item0 + it) << rl) + row - (rt << rl);
       count = (int)(w1 - w0 + 1) << two;

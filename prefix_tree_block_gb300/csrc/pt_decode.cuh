@@ -130,8 +130,11 @@ __device__ __forceinline__ int dec_clamp(const DecArgs& a, int len) { return min
 
 // Tokens [b, e) of a node of len tokens.  With masks the tile kernel takes a
 // sample's own continuation whole (it masks by rows), and no tail is left.
-__device__ __forceinline__ void dec_range(const DecArgs& a, int kind, int len, int& b, int& e) {
-  if (a.mask) {
+// `masked` here and below: whether there are masks, a constant in the attention
+// kernels, whose template says so (asked of a.mask at run time, it cost the unmasked
+// tile kernel 336 bytes a thread of spill loads).
+__device__ __forceinline__ void dec_range(const DecArgs& a, bool masked, int kind, int len, int& b, int& e) {
+  if (masked) {
     b = kind == kSegTail ? len : 0;
     e = len;
     return;
@@ -233,7 +236,7 @@ __device__ __forceinline__ int dec_wide(DecTiling g, int rows) { return g.r == k
 // The tile class's tiling.  With masks small items are many (a sample's whole
 // continuation each) and cost more beside their tiles: the rows' limits, the masks
 // and the values' check are chains of latencies.
-__device__ __forceinline__ DecTiling dec_tile(const DecArgs& a) { return DecTiling{kTile.r, kTile.t, a.mask ? kTileMaskedK : kTile.k}; }
+__device__ __forceinline__ DecTiling dec_tile(bool masked) { return DecTiling{kTile.r, kTile.t, masked ? kTileMaskedK : kTile.k}; }
 
 // Units of an item of so many tiles.
 __device__ __forceinline__ int dec_line(DecTiling g, int rows, int tiles) {
@@ -242,8 +245,8 @@ __device__ __forceinline__ int dec_line(DecTiling g, int rows, int tiles) {
 
 // Units of segment i, and what it takes to know them: its entry, its length
 // and the tiles of one of its items (0 when its only sample has no queries).
-__device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, DecTiling g, int i, DecSeg& sg, int& raw,
-                                         int& tiles) {
+__device__ __forceinline__ int dec_units(const DecArgs& a, bool masked, const DecClass& c, DecTiling g, int i, DecSeg& sg,
+                                         int& raw, int& tiles) {
   sg = DecSeg{0, 0, 0, -1};
   raw = 0;
   if (i < c.nseg) {
@@ -251,7 +254,7 @@ __device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, De
     sg = load_seg(c.seg + i);
   }
   int b, e;
-  dec_range(a, sg.kind(), dec_clamp(a, raw), b, e);
+  dec_range(a, masked, sg.kind(), dec_clamp(a, raw), b, e);
   tiles = (e - b + (1 << g.t) - 1) >> g.t;
   if (a.q_count && sg.solo >= 0 && a.q_count[sg.solo] <= 0) tiles = 0;
   return ((sg.rows() + (1 << g.r) - 1) >> g.r) * a.Hkv * dec_line(g, sg.rows(), tiles);
@@ -261,8 +264,8 @@ __device__ __forceinline__ int dec_units(const DecArgs& a, const DecClass& c, De
 // (chunk[nc] = all of them); every thread of the block calls it.  With cost, of
 // two classes, the tile class first; cost[i], zero before, then receives class
 // i's units.
-__device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, const DecClass& c1, DecTiling g0,
-                                         DecTiling g1, int* chunk0, int* chunk1, unsigned long long* cost) {
+__device__ __forceinline__ void dec_scan(const DecArgs& a, bool masked, const DecClass& c0, const DecClass& c1,
+                                         DecTiling g0, DecTiling g1, int* chunk0, int* chunk1, unsigned long long* cost) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int nc = (c0.nseg + 31) >> 5;
 #pragma unroll 1
@@ -272,7 +275,7 @@ __device__ __forceinline__ void dec_scan(const DecArgs& a, const DecClass& c0, c
       DecSeg sg;
       int raw, tiles;
       const DecTiling g = {i ? g1.r : g0.r, i ? g1.t : g0.t, i ? g1.k : g0.k};
-      const int u = dec_units(a, i ? c1 : c0, g, k * 32 + lane, sg, raw, tiles);
+      const int u = dec_units(a, masked, i ? c1 : c0, g, k * 32 + lane, sg, raw, tiles);
       if (blockIdx.x == 0 && (raw < 0 || raw > a.cap)) record_status(PT_STATUS_INVALID);
       const int sum = __reduce_add_sync(0xffffffffu, u);
       if (lane == 0) (i ? chunk1 : chunk0)[k] = sum;
@@ -306,13 +309,14 @@ __device__ __forceinline__ int dec_share(int total, int workers, int min_units) 
 
 // What the merge needs of a class: the units before each segment, and a
 // worker's share.  One block of the grid calls it.
-__device__ __forceinline__ void dec_publish(const DecArgs& a, const DecClass& c, DecTiling g, const int* chunk, int per) {
+__device__ __forceinline__ void dec_publish(const DecArgs& a, bool masked, const DecClass& c, DecTiling g, const int* chunk,
+                                            int per) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll 1
   for (int k = warp; k < (c.nseg + 31) >> 5; k += nw) {
     DecSeg sg;
     int raw, tiles;
-    const int i = k * 32 + lane, u = dec_units(a, c, g, i, sg, raw, tiles);
+    const int i = k * 32 + lane, u = dec_units(a, masked, c, g, i, sg, raw, tiles);
     const int x = warp_incl_scan(u, lane) - u;
     if (i < c.nseg) c.pref[i] = chunk[k] + x;
   }
@@ -330,6 +334,7 @@ struct DecPiece {
 // A worker's way along the line of units; every lane of a warp walks alike.
 struct DecWalk {
   const DecArgs& a;
+  const bool masked;
   const DecClass& c;
   const DecTiling g;
   const int* chunk;
@@ -339,9 +344,9 @@ struct DecWalk {
   DecSeg sg;
   int raw, tiles, excl;
 
-  __device__ __forceinline__ DecWalk(const DecArgs& a_, const DecClass& c_, DecTiling g_, const int* ch, int worker,
-                                     int per)
-      : a(a_), c(c_), g(g_), chunk(ch), w(worker) {
+  __device__ __forceinline__ DecWalk(const DecArgs& a_, bool masked_, const DecClass& c_, DecTiling g_, const int* ch,
+                                     int worker, int per)
+      : a(a_), masked(masked_), c(c_), g(g_), chunk(ch), w(worker) {
     nc = (c.nseg + 31) >> 5;
     const int total = chunk[nc];
     pos = (int)min((long long)worker * per, (long long)total);
@@ -360,7 +365,7 @@ struct DecWalk {
 #pragma unroll 1
       do ++k;
       while (pos >= chunk[k + 1]);
-      const int lane = threadIdx.x & 31, u = dec_units(a, c, g, k * 32 + lane, sg, raw, tiles);
+      const int lane = threadIdx.x & 31, u = dec_units(a, masked, c, g, k * 32 + lane, sg, raw, tiles);
       excl = chunk[k] + warp_incl_scan(u, lane) - u;
     }
     // the segment that holds pos: the last that starts at or before it

@@ -108,7 +108,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
   const int lane = threadIdx.x & 31;
   const int col0 = SPLIT == 1 ? 0 : sw * 128;  // this warp's first column
   const uint32_t ring_u = smem_u32(ring);
-  DecWalk walk(a, c, kRows, chunk, worker, per);
+  DecWalk walk(a, TREE, c, kRows, chunk, worker, per);
   // loads: the piece they are at, its last page, pages l_page0 + lane, and the next tile's page and row in it
   DecPiece lp;
   lp.t0 = lp.t1 = 0;
@@ -139,7 +139,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
           continue;
         }
         int b, e;
-        dec_range(a, lp.kind, lp.len, b, e);
+        dec_range(a, TREE, lp.kind, lp.len, b, e);
         const int kv0 = b + lp.t0 * kRowsBT;
         l_last = (min(e, b + lp.t1 * kRowsBT) - 1) / a.ps;
         l_page0 = kv0 / a.ps - 32, l_page = 32;  // (looked up below)
@@ -219,7 +219,7 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
       __syncwarp();
       const DecPiece& p = pieces[at & 1];
       int e;
-      dec_range(a, p.kind, p.len, kv_base, e);
+      dec_range(a, TREE, p.kind, p.len, kv_base, e);
       t = p.t0, t1 = p.t1, slot = p.slot;
       rows_left = p.rows - p.rt * kRowsR;
       int own_lo = INT_MAX;
@@ -451,14 +451,14 @@ struct DecSplit {
   int n_tile;         // SMs of the tile kernel; the rows kernel has the others
   int per_t, per_r;   // units per worker
 };
-template <int NP>
+template <int NP, bool TREE>
 __device__ __forceinline__ DecSplit dec_split(const DecArgs& a, const DecClass& ct, const DecClass& cr, int* chunk_t,
                                               int* chunk_r, unsigned long long* cost, int sms, int rows_per_sm) {
   const bool both = ct.nitems && cr.nitems;
   if (both)
-    dec_scan(a, ct, cr, dec_tile(a), kRows, chunk_t, chunk_r, cost);
+    dec_scan(a, TREE, ct, cr, dec_tile(TREE), kRows, chunk_t, chunk_r, cost);
   else
-    dec_scan(a, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t, ct.nitems ? dec_tile(a).k : kRows.k}, kRows,
+    dec_scan(a, TREE, ct.nitems ? ct : cr, cr, DecTiling{ct.nitems ? kTile.r : kRows.r, ct.nitems ? kTile.t : kRows.t, ct.nitems ? dec_tile(TREE).k : kRows.k}, kRows,
              ct.nitems ? chunk_t : chunk_r, chunk_r, nullptr);
   const int nc = (max(ct.nseg, cr.nseg) + 31) >> 5;
   const int units_t = ct.nitems ? chunk_t[nc] : 0, units_r = cr.nitems ? chunk_r[nc] : 0;
@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(RowsCfg<NP, SPLIT>::WARPS * 32, RowsCfg<NP, SP
     prefetch_tmap(&mV);
   }
   if (beside) __syncthreads();  // (the costs; the scan's barriers publish the rest)
-  const DecSplit sp = dec_split<NP>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::GROUPS);
-  if ((int)blockIdx.x == 0) dec_publish(a, c, kRows, chunk, sp.per_r);
+  const DecSplit sp = dec_split<NP, TREE>(a, ct, c, chunk + ((c.nseg + 31) >> 5) + 1, chunk, cost, a.sms, C::CTAS * C::GROUPS);
+  if ((int)blockIdx.x == 0) dec_publish(a, TREE, c, kRows, chunk, sp.per_r);
   if ((int)blockIdx.x < (a.sms - sp.n_tile) * C::CTAS)
     rows_worker<NP, SPLIT, TREE>(mK, mV, a, c, chunk, sp.per_r, (int)blockIdx.x * C::GROUPS + warp / SPLIT, warp % SPLIT,
                            smem + warp * C::RING, bars + warp * C::STAGES,
@@ -683,8 +683,8 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
     prefetch_tmap(&mV);
   }
   __syncthreads();
-  const DecSplit sp = dec_split<NP>(a, c, cr, chunk, chunk + ((c.nseg + 31) >> 5) + 1, cost, gridDim.x, rows_per_sm);
-  if (blockIdx.x == 0) dec_publish(a, c, dec_tile(a), chunk, sp.per_t);
+  const DecSplit sp = dec_split<NP, TREE>(a, c, cr, chunk, chunk + ((c.nseg + 31) >> 5) + 1, cost, gridDim.x, rows_per_sm);
+  if (blockIdx.x == 0) dec_publish(a, TREE, c, dec_tile(TREE), chunk, sp.per_t);
   if ((int)blockIdx.x >= sp.n_tile) return;
   const int worker = blockIdx.x, per = sp.per_t;
   if (warp == 9) {
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   };
 
   const auto producer_role = [&]() {
-    DecWalk walk(a, c, dec_tile(a), chunk, worker, per);
+    DecWalk walk(a, TREE, c, dec_tile(TREE), chunk, worker, per);
     DecPiece p;
     uint32_t n = 0, np = 0;  // tiles issued; pieces
     bool ok = true;
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
       ++np;
       if (!more) break;
       int b, e;
-      dec_range(a, p.kind, p.len, b, e);
+      dec_range(a, TREE, p.kind, p.len, b, e);
       const int bt = lane & (boxes - 1);  // this lane's box of the tile; its page, looked up a tile ahead
       auto page_of = [&](int t) {
         const int kv = t * kTileBT + bt * box_rows;
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         if (!get_piece(p, it)) break;
         if (it++ == 0) gather_rows(p, warp, 8);
         int b;
-        dec_range(a, p.kind, p.len, b, tok);
+        dec_range(a, TREE, p.kind, p.len, b, tok);
         tok -= p.t0 * kTileBT;
         const int left = p.rows - p.rt * kTileR;
         pair = left > kTileR / 2 ? 1 : 0;
