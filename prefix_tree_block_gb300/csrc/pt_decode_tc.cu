@@ -661,7 +661,11 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ unsigned long long cost[2];
   __shared__ volatile int odd_piece[8];  // TREE: the piece (by its number modulo 8) in which a value was not finite
-  if (TREE && threadIdx.x < 8) odd_piece[threadIdx.x] = 0;
+  __shared__ volatile int odd_row[TREE ? 2 : 1][TREE ? kTileBT : 1];  // TREE: the tile (its number + 1, by that modulo 2) whose row's values are being cleared
+  if constexpr (TREE) {
+    if (threadIdx.x < 8) odd_piece[threadIdx.x] = 0;
+    if (threadIdx.x < 2 * kTileBT) odd_row[threadIdx.x / kTileBT][threadIdx.x % kTileBT] = 0;
+  }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 8);
     mbar_init(q_empty, 1);
@@ -949,8 +953,11 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
         const int from = (u >> pair) * kTileBT;  // the tile's first token, from the piece's first tile on
         const bool masked = TREE && from + kTileBT > mixed;
         if (masked) {
-          // Values that are not finite, of tokens that some rows do not see, are cleared (see add_odd_values; first it
-          // is said that there are some: the other warpgroup of a pair may find them cleared).
+          // Values that are not finite, of tokens that some rows do not see, are cleared (see add_odd_values).  Both
+          // warpgroups of a pair do so, each before its own product.  One may read a row while the other clears it, and
+          // find what was not finite gone but the rest still there, which its product would add a second time: so
+          // which row and that there are some is said first, and asked after the reading.  (The two are never two
+          // tiles apart: S of a tile comes after both products of the last but one.)
           const uint32_t x = n + (u >> pair), vs = x % C::VS;
           ok = mbar_wait(v_full + vs, (x / C::VS) & 1, abort_flag);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -959,7 +966,9 @@ __global__ void __launch_bounds__(TileCfg<NP>::THREADS, 1)
 #pragma unroll
             for (int pn = 0; pn < NP; ++pn)
               odd |= odd_values(reinterpret_cast<const uint4*>(smem + C::OFF_V + vs * C::TILE + pn * C::PANEL + r * 128), 8);
-            if (odd) {
+            __threadfence_block();
+            if (odd || odd_row[x & 1][r] == (int)x + 1) {
+              odd_row[x & 1][r] = (int)x + 1;
               odd_piece[it & 7] = (int)it;
               __threadfence_block();
 #pragma unroll
