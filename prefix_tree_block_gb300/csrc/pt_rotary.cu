@@ -278,9 +278,10 @@ extern "C" pt_status pt_rotary(const void* X, int64_t x_stride, pt_dtype dtype, 
   const int most = std::max(1, std::min((H + each - 1) / each, 256 / per));
   a.lanes = 1;  // (a power of two, so that warps are full: 40 heads in four lanes 89 us, in five 93)
   while (2 * a.lanes <= most) a.lanes *= 2;
-  a.tokens = std::max(1, 256 / (per * a.lanes));
+  // (a CTA's elements are counted in 32 bits; H * D is at most INT_MAX / 4)
+  a.tokens = std::max(1, std::min(256 / (per * a.lanes), INT_MAX / 4 / (H * D)));
   const int threads = per * a.lanes * a.tokens;
-  const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
+  const dim3 grid((unsigned)(((long long)T + a.tokens - 1) / a.tokens));
   const size_t smem = (size_t)a.tokens * half * 8;
   cudaError_t e;
   {
