@@ -575,6 +575,9 @@ class FoldPlan:
 
         device = device or torch.device("cuda")
         ptr, succ = _empty((self.T + 1,), torch.int32, device), _empty((self.T,), torch.int32, device)
+        if isinstance(stream, torch.cuda.Stream):
+            ptr.record_stream(stream)
+            succ.record_stream(stream)
         _check(self._lib.pt_fold_successors(self._h, _ptr(ptr), _ptr(succ), ctypes.c_void_p(_stream(stream))))
         return ptr, succ
 
@@ -647,7 +650,10 @@ def _out(shape, dtype, like):
 
 def _launch_stream(stream, dev, *held):
     """The raw stream of a call.  On a stream of the caller's choice, the
-    tensors allocated here (`held`) are marked as used on it."""
+    tensors allocated here (`held`) are marked as used on it.  They are allocated
+    on the current stream: what the caller's stream does behind that stream's
+    work (stream.wait_stream(torch.cuda.current_stream())) finds their memory
+    free."""
     if stream is None:
         return _T[5](dev)
     if isinstance(stream, _T[0].cuda.Stream):
