@@ -323,14 +323,15 @@ __device__ __forceinline__ void rows_worker(const CUtensorMap& mK, const CUtenso
           }
           const float2 f = __bfloat1622float2(__hadd2(sum[0], sum[1]));
           odd = !(f.x == 0.f && f.y == 0.f);
-        }
+        } else {
 #pragma unroll 1
-        for (int i = TREE ? INT_MAX : n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
-          const uint4 v = *reinterpret_cast<const uint4*>(vs + ((i % (NP * 8)) >> 3) * C::PANEL + (i / (NP * 8)) * 128 +
-                                                          (i & 7) * 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int i = n_all * (NP * 8) + lane; i < n_any * (NP * 8); i += 32) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vs + ((i % (NP * 8)) >> 3) * C::PANEL + (i / (NP * 8)) * 128 +
+                                                            (i & 7) * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+            for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+          }
         }
         if (__any_sync(0xffffffffu, odd)) n_mul = n_all;
       }

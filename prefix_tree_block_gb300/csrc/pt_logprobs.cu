@@ -348,16 +348,6 @@ constexpr int kStages = 3;  // (four: the same; two: 2% more without alternative
 // Shared memory of the ring: stages of four slots a thread.
 constexpr int ring_bytes(int nt) { return kStages * nt * 4 * 16; }
 
-template <int N>
-__device__ __forceinline__ int bar_count(bool p) {  // how many of the N threads of barrier 1 say yes
-  int r;
-  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, 1, %2, q;\n\t}"
-               : "=r"(r)
-               : "r"((unsigned)p), "n"(N)
-               : "memory");
-  return r;
-}
-
 template <class E, int NT, bool TOP, bool CLERK, bool RING>
 __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 && TOP ? 24 : 1024 / (NT + 32 * CLERK)) k_score(const ScoreArgs a) {
   constexpr int V = Type<E>::V, U = 4, ALL = NT + 32 * CLERK;  // ALL: without the warp that loads
@@ -380,12 +370,8 @@ __global__ void __launch_bounds__(NT + 32 * (CLERK + RING), RING ? 3 : NT == 32 
     else
       __syncthreads();
   };
-  const auto count = [&](bool p) {
-    if constexpr (RING)
-      return bar_count<ALL>(p);
-    else
-      return __syncthreads_count(p);
-  };
+  static_assert(!(RING && TOP), "the alternatives' barriers are the whole CTA's");
+  const auto count = [](bool p) { return __syncthreads_count(p); };
   if constexpr (RING) {
     if (tid == 0) {
       for (int i = 0; i < kStages; ++i) mbar_init(sm_full + i, 1), mbar_init(sm_empty + i, NT / 32);
