@@ -831,7 +831,7 @@ pt_status attn_decode(const char* who, const void* Q, int64_t q_stride, const vo
     if (tiles && a.mask && !plan->few) m.c0.nitems = 0;  // (masks leave no tails)
     m.g0 = kRows;
     a.q_vec = (reinterpret_cast<uintptr_t>(Q) & 15u) == 0 && q_stride % 8 == 0;
-    const int rc = decode_tc(plan, a, m.c0, m.c1, stream);
+    const int rc = decode_tc(who, plan, a, m.c0, m.c1, stream);
     if (rc) return (pt_status)rc;
   } else {
     m.c0 = class_args(plan, kDecSimt, D, ws);

@@ -414,7 +414,8 @@ struct pt_decodeplan {
 namespace pt {
 // Tensor-core kernels (pt_decode_tc.cu).  Returns a PT_* status code.
 bool decode_tc_supported(int D, int ps);
-int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile, cudaStream_t s);
+int decode_tc(const char* who, const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile,
+              cudaStream_t s);
 int take_status_decode_tc(cudaStream_t s);
 constexpr int kRowsWarps = 12;  // workers of the rows kernel per SM, at most
 inline int dec_workers(const pt_decodeplan* p, int cls) {

@@ -1195,10 +1195,11 @@ cudaError_t launch_tile(const CUtensorMap& mK, const CUtensorMap& mV, const DecA
 
 bool decode_tc_supported(int D, int ps) { return D % 8 == 0 && D <= 512 && ps % 16 == 0; }
 
-int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile, cudaStream_t s) {
+int decode_tc(const char* who, const pt_decodeplan* p, DecArgs a, const DecClass& rows, const DecClass& tile,
+              cudaStream_t s) {
   const long long heads = (long long)a.n_pages * a.Hkv;
   if (heads > INT_MAX - 1) {
-    set_error("pt_attn_decode: %d pages of %d heads are out of range", a.n_pages, a.Hkv);
+    set_error("%s: %d pages of %d heads are out of range", who, a.n_pages, a.Hkv);
     return PT_ERR_INVALID_ARG;
   }
   CUtensorMap mK, mV, mKt, mVt;
@@ -1222,7 +1223,7 @@ int decode_tc(const pt_decodeplan* p, DecArgs a, const DecClass& rows, const Dec
     e = a.mask ? launch_rows<true>(mK, mV, a, rows, tile, s) : launch_rows<false>(mK, mV, a, rows, tile, s);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
-    set_error("pt_attn_decode: launch failed: %s", cudaGetErrorString(e));
+    set_error("%s: launch failed: %s", who, cudaGetErrorString(e));
     return PT_ERR_CUDA;
   }
   return PT_OK;
