@@ -994,7 +994,8 @@ def token_logprobs_bwd(dlogp, logits, targets, lse, row_ptr=None, index=None, de
                        scale: float = 1.0, dlogits=None, stream=None):
     """dlogits [R, V] from dlogp [N] and, with the forward's entropy, dentropy
     [R] (pt_token_logprobs_bwd); lse and entropy as token_logprobs returned them.
-    dlogits may be logits."""
+    dlogits may be logits.  Beside logits that are columns of a wider buffer give
+    one with their row stride (without, it is dense and stored by elements)."""
     _, _, _, f32, _, _, device = _torch()
     dev = device() if logits.is_cuda else -1
     if logits.dim() != 2:
