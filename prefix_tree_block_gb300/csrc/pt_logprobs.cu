@@ -893,7 +893,7 @@ __device__ __forceinline__ void store_slot(E* out, const Row<E>& row, int s, boo
 // A whole row of k_grad by one CTA, ln p = (x - m) scale - ln S with m and S from the
 // row itself (three looks at it).  The other CTAs of the row leave it alone, since
 // the gradient may take the logits' place.  Bound by latency: one row of 131072 in bf16
-// 84 us (2.5 by all of its CTAs on the near path), 4000 x 65536 365 us (157).
+// 90 us (2.5 by all of its CTAs on the near path), 4000 x 65536 379 us (157).
 template <class E, int NT, bool ENT, bool VEC>
 __device__ __noinline__ void far_row(const GradArgs& a, int r, const unsigned* bits, float* sm, int e0, int e1, float ca,
                                      float cb) {
@@ -902,12 +902,18 @@ __device__ __noinline__ void far_row(const GradArgs& a, int r, const unsigned* b
   const Row<E> row(static_cast<const E*>(a.x) + (long long)r * a.stride, a.V);
   E* out = static_cast<E*>(a.d) + (long long)r * a.d_stride;
   const int slots = row.slots();
+  auto get = [&](int at, float (&y)[V]) {  // (not as read-only memory: the gradient may be written there)
+    if (row.whole(at))
+      unpack(*reinterpret_cast<const uint4*>(row.x + ((long long)at * V - row.lead)), y);
+    else
+      row.get(at, y);
+  };
   const float c1 = a.scale * 1.4426950408889634f;
   float m = -INFINITY, s = 0.f;
 #pragma unroll 1
   for (int at = tid; at < slots; at += NT) {
     float y[V];
-    row.get(at, y);
+    get(at, y);
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, y[i]);
   }
@@ -921,7 +927,7 @@ __device__ __noinline__ void far_row(const GradArgs& a, int r, const unsigned* b
 #pragma unroll 1
   for (int at = tid; at < slots; at += NT) {
     float y[V];
-    row.get(at, y);
+    get(at, y);
 #pragma unroll
     for (int i = 0; i < V; ++i) s += ex2((y[i] - m) * c1);
   }
@@ -937,7 +943,7 @@ __device__ __noinline__ void far_row(const GradArgs& a, int r, const unsigned* b
 #pragma unroll 1
   for (int at = tid; at < slots; at += NT) {
     float y[V];
-    row.get(at, y);
+    get(at, y);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float l = fmaxf(fmaf(y[i] - m, a.scale, -ln_s), -1000.f);
